@@ -69,6 +69,7 @@ typedef enum { FAR_F32 = 0, FAR_F16 = 1, FAR_BF16 = 2 } far_dtype;
 #define FAR_ERR_TIMEOUT 8    /* a bounded wait inside a kernel ran out (far_device_status) */
 #define FAR_ERR_WORKSPACE 9  /* the host-buffer entry points got too small a workspace */
 #define FAR_ERR_SCRATCH 10   /* a row does not fit the allocation-free entry point's fixed scratch */
+#define FAR_ERR_POSITION 11  /* a position lies past the rotation table (far_device_status) */
 
 /*
  * Fused residual add + RMSNorm.
@@ -225,6 +226,123 @@ int fused_add_rmsnorm_quant_strided(const void* x, int64_t x_row_stride, const v
 
 int rmsnorm_quant_strided(const void* x, int64_t x_row_stride, const void* weight, float eps, void* q, float* scale,
                           int64_t tokens, int64_t hidden, int dtype, int qtype, void* stream);
+
+/*
+ * Per-head RMSNorm of queries and keys and the rotation by position, in one pass.  For
+ * each token t and head, with x the head's head_dim values (widened to binary32):
+ *   r   = fl32(1 / fl32(sqrt(fl32(fl32(S / head_dim) + eps)))),  S = the binary32 sum of x_i^2
+ *   n_i = x_i * r * w_i                                          (w: q_weight or k_weight)
+ *   for the first rot_dim values, with c_j and s_j the table's row positions[t]:
+ *     pairs FAR_PAIRS_HALF:        j = 0 .. rot_dim/2 - 1, (a, b) = (n_j, n_{j + rot_dim/2})
+ *     pairs FAR_PAIRS_INTERLEAVED: (a, b) = (n_{2j}, n_{2j+1})
+ *     (a, b) -> (a c_j - b s_j, b c_j + a s_j)
+ *   the other values keep n_i.  Everything is binary32 and rounded once, to the
+ *   activations' dtype, when it is stored: nothing is rounded between the norm and the
+ *   rotation, and the outputs have the activations' dtype whatever the weights' is (they
+ *   stand where q and k stood).
+ * rope is the rotation alone (n_i = x_i); with transpose = 1 it turns the other way, which
+ * is its gradient: given the gradients of its outputs in q and k's place it writes those of
+ * its inputs (the transpose, also of a table with an attention factor in it).
+ *   q, k        [tokens, q_heads, head_dim], [tokens, k_heads, head_dim] act, device; a
+ *               token and a head stride each in ELEMENTS (>= 0, so a broadcast input has
+ *               stride 0); the values of a head contiguous.  k_heads = 0: no keys (the k
+ *               arguments are ignored); the same with q_heads = 0.
+ *   q_weight, k_weight  [head_dim] wd, device
+ *   table       [table_rows, rot_dim] binary32, contiguous, device: the row's rot_dim/2
+ *               cosines, then its rot_dim/2 sines (rope_table makes one)
+ *   positions   [tokens] device, int32 (position_bytes 4) or int64 (8).  A negative
+ *               position marks a padding token: its output rows are written as zeros.  One
+ *               at or past table_rows is a caller error found on the device: its rows are
+ *               written as NaN and far_device_status reports FAR_ERR_POSITION.
+ *   q_out, k_out  as q and k, act, strides of their own; no two values may share a place
+ *   tokens >= 0 (0 is a no-op), 1 <= head_dim <= 2048, 2 <= rot_dim <= head_dim (even)
+ *   dtype       FAR_DTYPES(act, wd) for qk_norm_rope, the activations' dtype code for rope
+ * In place (q_out exactly q: pointer and strides; likewise k) is allowed; otherwise an
+ * output shares no byte with any other buffer (FAR_ERR_ALIAS).  FAR_ERR_SHAPE for sizes or
+ * strides outside the above.  16-byte aligned heads of whole 16-byte chunks whose pairs
+ * fall in whole chunks take the vector kernel, anything else a scalar one; the order of
+ * the sums differs between the two, so their results may differ in the last place.
+ */
+#define FAR_PAIRS_HALF 0
+#define FAR_PAIRS_INTERLEAVED 1
+
+int qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_token_stride,
+                 int64_t k_head_stride, const void* q_weight, const void* k_weight, float eps, const float* table,
+                 int64_t table_rows, const void* positions, int position_bytes, void* q_out,
+                 int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out, int64_t k_out_token_stride,
+                 int64_t k_out_head_stride, int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t head_dim,
+                 int64_t rot_dim, int pairs, int dtype, void* stream);
+
+int rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_token_stride,
+         int64_t k_head_stride, const float* table, int64_t table_rows, const void* positions, int position_bytes,
+         void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out, int64_t k_out_token_stride,
+         int64_t k_out_head_stride, int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t head_dim,
+         int64_t rot_dim, int pairs, int transpose, int act, void* stream);
+
+/*
+ * The gradients of qk_norm_rope: given dy, the gradient of an output, and the forward
+ * call's q, k, weights, table and positions, per token and head with g the rotation's
+ * transpose applied to dy, r as above and u_i = x_i * r:
+ *   dw_i = sum over tokens and heads of g_i u_i
+ *   dx_i = r * (h_i - u_i * mean_j(h_j u_j)),  h_i = g_i w_i
+ * in binary32, dx rounded once to act.  The weights' gradients are binary32 whatever the
+ * weights' dtype; their sums are taken in a fixed order (the same bits every run).
+ *   dq_out, dk_out        act, device, read: shapes of q and k, strides of their own
+ *   dq, dk                act, device, written: shapes of q and k; each may be exactly its
+ *                         q / k or its dq_out / dk_out (pointer and strides)
+ *   dq_weight, dk_weight  [head_dim] binary32, device, written (with tokens = 0 too: zeros)
+ *   workspace             far_qk_backward_workspace_bytes(...) bytes of device memory, 16-byte
+ *                         aligned, the caller's: two calls that may run side by side (other
+ *                         streams, other graphs) need one each.  Nothing in it is kept.
+ * A padding token (negative position) gets zero gradients and adds nothing to the
+ * weights'; a position past the table gives NaN rows, adds nothing, and is reported.
+ * Everything else is as for qk_norm_rope.  FAR_ERR_WORKSPACE: too small or misaligned.
+ */
+int64_t far_qk_backward_workspace_bytes(int64_t head_dim);
+
+int qk_norm_rope_backward(const void* dq_out, int64_t dq_out_token_stride, int64_t dq_out_head_stride,
+                          const void* dk_out, int64_t dk_out_token_stride, int64_t dk_out_head_stride, const void* q,
+                          int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_token_stride,
+                          int64_t k_head_stride, const void* q_weight, const void* k_weight, float eps,
+                          const float* table, int64_t table_rows, const void* positions, int position_bytes, void* dq,
+                          int64_t dq_token_stride, int64_t dq_head_stride, void* dk, int64_t dk_token_stride,
+                          int64_t dk_head_stride, float* dq_weight, float* dk_weight, void* workspace,
+                          int64_t workspace_bytes, int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t head_dim,
+                          int64_t rot_dim, int pairs, int dtype, void* stream);
+
+/*
+ * Rotation frequencies, in binary64 on the host: freq[j], j = 0 .. rot_dim/2 - 1, from
+ * f_j = base^(-2j / rot_dim), scaled for contexts longer than a model was trained on:
+ *   FAR_ROPE_PLAIN   f_j
+ *   FAR_ROPE_LINEAR  f_j / a                              a = params[0], the stretch (> 0)
+ *   FAR_ROPE_NTK     f_j of base * a^(rot_dim / (rot_dim - 2))   a = params[0] (> 0); rot_dim > 2
+ *   FAR_ROPE_YARN    params = {a, trained length, fast turns, slow turns, attention factor}:
+ *                    with d(b) = rot_dim ln(trained / (2 pi b)) / (2 ln base), low = floor(d(fast)),
+ *                    high = ceil(d(slow)) (both within 0 .. rot_dim - 1, high >= low + 0.001) and
+ *                    m_j = (j - low) / (high - low) within 0 .. 1: f_j (1 - m_j) + f_j / a m_j.
+ *                    *attention_factor = the factor given, or 0.1 ln(a) + 1 (1 for a <= 1) if it is 0
+ *   FAR_ROPE_BANDS   params = {a, trained length, low, high}: with t = trained f_j / (2 pi) turns over the
+ *                    trained length, f_j where t > high, f_j / a where t < low, and between them
+ *                    f_j (m + (1 - m) / a), m = (t - low) / (high - low)
+ * (the attention factor is 1 but for FAR_ROPE_YARN).  2 <= rot_dim <= 2048, even; base > 1.
+ * FAR_ERR_SHAPE for sizes, FAR_ERR_DTYPE for an unknown scaling, FAR_ERR_EPS for parameters
+ * that are not finite or out of range.
+ *
+ * rope_table writes a device table [rows, rot_dim]: factor * cos(t * freq[j]) and
+ * factor * sin(t * freq[j]), t the row's number plus first_position, each rounded once to
+ * binary32 from binary64 (the angle of a far position loses nothing).  freq: host memory,
+ * rot_dim/2 values, read before the call returns.
+ */
+#define FAR_ROPE_PLAIN 0
+#define FAR_ROPE_LINEAR 1
+#define FAR_ROPE_NTK 2
+#define FAR_ROPE_YARN 3
+#define FAR_ROPE_BANDS 4
+
+int far_rope_frequencies(int64_t rot_dim, double base, int scaling, const double* params, double* freq,
+                         double* attention_factor);
+int rope_table(float* table, int64_t rows, int64_t rot_dim, int64_t first_position, const double* freq, double factor,
+               void* stream);
 
 /* the output dtype od of FAR_DTYPES(act, wd), or -status when the pair is rejected */
 int far_output_dtype(int dtype);

@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(_PKG, "_build", "libfar.so")
 F32, F16, BF16 = 0, 1, 2
 STATUS = {0: "FAR_OK", 1: "FAR_ERR_DTYPE_MIX", 2: "FAR_ERR_DTYPE", 3: "FAR_ERR_NULL", 4: "FAR_ERR_SHAPE",
           5: "FAR_ERR_ALIAS", 6: "FAR_ERR_EPS", 7: "FAR_ERR_CUDA", 8: "FAR_ERR_TIMEOUT",
-          9: "FAR_ERR_WORKSPACE", 10: "FAR_ERR_SCRATCH"}
+          9: "FAR_ERR_WORKSPACE", 10: "FAR_ERR_SCRATCH", 11: "FAR_ERR_POSITION"}
 FAR_OK, FAR_ERR_TIMEOUT = 0, 8
 TORCH_TO_CODE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 CODE_TO_TORCH = {v: k for k, v in TORCH_TO_CODE.items()}
@@ -540,3 +540,7 @@ def rmsnorm_quant_host(x, weight, eps, qtype, q, scale, workspace, stream=None) 
     _check(lib.rmsnorm_quant_host(_ptr(x), _ptr(weight), eps, _ptr(q), _ptr(scale), tokens, hidden,
                                   dtypes(x.dtype, weight.dtype), QUANT[qtype], _ptr(workspace), _wsb(workspace),
                                   _stream_handle(stream)))
+
+
+from .heads import (qk_backward_workspace_bytes, qk_norm_rope, qk_norm_rope_backward, rope, rope_backward,  # noqa: E402
+                    rope_frequencies, rope_table)

@@ -14,11 +14,12 @@
 #include "far.h"
 #include "far_device.cuh"
 #include "far_params.h"
+#include "far_region.h"
 
 namespace far {
 
 // Device error word: bit FAR_ERR_TIMEOUT is set by a kernel that gave up a
-// bounded wait.  Read and cleared by far_device_status.
+// bounded wait, bit FAR_ERR_POSITION by one that met a position past its table.  Read and cleared by far_device_status.
 __device__ unsigned int g_status;
 
 // Row counters of the staged kernel's claimed rows: pairs {next claim, CTAs done}, zero
@@ -235,46 +236,6 @@ int dsize(int dt) { return dt == FAR_F32 ? 4 : 2; }
 struct Strides {
   int64_t x, r, out, res;
 };
-
-// A strided tensor in memory: `rows` rows of `width` bytes, `stride` bytes apart.
-struct Region {
-  uint64_t base;
-  int64_t rows, width, stride;
-};
-
-Region region(const void* p, int64_t rows, int64_t width, int64_t stride) {
-  return Region{(uint64_t)(uintptr_t)p, rows, width, stride};
-}
-
-int64_t floor_div(int64_t a, int64_t b) {  // b > 0
-  return a >= 0 ? a / b : -((-a + b - 1) / b);
-}
-
-// Do any bytes of A and B coincide?  Exact for equal strides (rows of two column
-// slices of one matrix interleave without touching); otherwise any overlap of the
-// spanned byte ranges counts.
-bool regions_overlap(const Region& A, const Region& B) {
-  if (A.rows == 0 || B.rows == 0 || A.width == 0 || B.width == 0) return false;
-  const uint64_t a_end = A.base + (uint64_t)((A.rows - 1) * A.stride + A.width);
-  const uint64_t b_end = B.base + (uint64_t)((B.rows - 1) * B.stride + B.width);
-  if (!(A.base < b_end && B.base < a_end)) return false;
-  if (A.stride != B.stride || A.rows == 1 || B.rows == 1) return true;
-  // row i of A and row j of B meet iff -B.width < d + (j - i) * s < A.width, d = B.base - A.base
-  const int64_t s = A.stride;
-  const int64_t d = (int64_t)(B.base - A.base);
-  const int64_t kmin = floor_div(-B.width - d, s) + 1;
-  const int64_t kmax = -floor_div(-(A.width - d), s) - 1;  // ceil((A.width - d) / s) - 1
-  const int64_t lo = kmin > -(B.rows - 1) ? kmin : -(B.rows - 1);
-  const int64_t hi = kmax < (A.rows - 1) ? kmax : (A.rows - 1);
-  return lo <= hi;
-}
-
-bool same_region(const Region& A, const Region& B) {
-  return A.base == B.base && A.rows == B.rows && A.width == B.width && A.stride == B.stride;
-}
-
-// an output may be exactly an input region (in place); no other byte may be shared
-bool bad_overlap(const Region& out, const Region& in) { return regions_overlap(out, in) && !same_region(out, in); }
 
 struct Call {
   const void* x;
@@ -1190,6 +1151,7 @@ const char* far_status_string(int status) {
     case FAR_ERR_WORKSPACE: return "workspace too small or misaligned for one row";
     case FAR_ERR_SCRATCH:
       return "one row (plus the weight) does not fit the fixed device scratch of the allocation-free entry point";
+    case FAR_ERR_POSITION: return "a position lies past the rotation table; its rows were written as NaN";
     default: return "unknown status";
   }
 }
@@ -1210,6 +1172,7 @@ int far_device_status(void* stream) {
     if (e != cudaSuccess) return cuda_fail(e);
   }
   if (word & (1u << FAR_ERR_TIMEOUT)) return FAR_ERR_TIMEOUT;
+  if (word == (1u << FAR_ERR_POSITION)) return FAR_ERR_POSITION;
   return word ? FAR_ERR_SHAPE : FAR_OK;  // a kernel refused an inconsistent launch plan
 }
 

@@ -344,6 +344,69 @@ int far_rope_frequencies(int64_t rot_dim, double base, int scaling, const double
 int rope_table(float* table, int64_t rows, int64_t rot_dim, int64_t first_position, const double* freq, double factor,
                void* stream);
 
+/*
+ * Output quantised to FP8 E4M3 in blocks of 128: the same two operations followed by a
+ * symmetric quantisation of each 128 neighbouring values of out (the last block of a row may
+ * be shorter), applied to the values out would have.  For a block with largest magnitude amax:
+ *   scale = fl32(amax / 448), q_i = E4M3(fl32(out_i * fl32(448 / amax)))   (nearest, ties to
+ *   even, finite values saturated to +-448); a block with amax below 2^-100 counts as zero
+ *   (scale 0, codes 0); NaN gives a NaN scale, an infinity an infinite one.
+ *   q      [tokens, hidden] E4M3 codes, contiguous, device
+ *   scale  [tokens, ceil(hidden / 128)] binary32, contiguous, device; dequantise a block as
+ *          q * scale: the operand form of gemm_fp8_block's x
+ * Row strides, aliasing and everything else as for the strided quantised forms (pass hidden
+ * for contiguous rows).
+ */
+int fused_add_rmsnorm_quant_block(const void* x, int64_t x_row_stride, const void* residual,
+                                  int64_t residual_row_stride, const void* weight, float eps, void* q, float* scale,
+                                  void* residual_out, int64_t residual_out_row_stride, int64_t tokens, int64_t hidden,
+                                  int dtype, void* stream);
+
+int rmsnorm_quant_block(const void* x, int64_t x_row_stride, const void* weight, float eps, void* q, float* scale,
+                        int64_t tokens, int64_t hidden, int dtype, void* stream);
+
+/*
+ * A matrix quantised to FP8 E4M3 in blocks of 128, as above, as it stands or transposed:
+ *   x      [rows, cols] act (FAR_F32, FAR_F16 or FAR_BF16), row stride in elements, device
+ *   block  FAR_BLOCK_ROW: 128 neighbouring values of a row of the OUTPUT share a scale;
+ *          FAR_BLOCK_TILE: the 128 x 128 values of a tile do (the last ones may be smaller)
+ *   transpose  0: q [rows, cols]; 1: q [cols, rows], q[j, i] the code of x[i, j]
+ *   q      E4M3 codes, contiguous, device
+ *   scale  binary32, contiguous, device: for q [r, c] FAR_BLOCK_ROW [r, ceil(c / 128)],
+ *          FAR_BLOCK_TILE [ceil(r / 128), ceil(c / 128)]
+ * So a weight [n, k] is quantised once by tiles; its transpose for the gradient of x, by
+ * tiles and transposed; activations and gradients by rows, and transposed by rows where a
+ * weight's gradient sums over the tokens.  rows, cols >= 0 (0: nothing to do), at most
+ * 2^31 - 1 each.  q and scale share no byte with another buffer.
+ */
+#define FAR_BLOCK_ROW 0
+#define FAR_BLOCK_TILE 1
+
+int quant_block_fp8(const void* x, int64_t x_row_stride, void* q, float* scale, int64_t rows, int64_t cols, int block,
+                    int transpose, int act, void* stream);
+
+/*
+ * The product of two FP8 E4M3 matrices scaled in blocks of 128 along k:
+ *   out[i, j] = RNE_od( sum_b xs[i, b] * ws[j, b] * sum_{k in block b} x[i, k] * wt[j, k] )
+ *   x        [m, k] E4M3 codes, row stride in elements (>= k), device
+ *   x_scale  [m, ceil(k / 128)] binary32, contiguous, device
+ *   wt       [n, k] E4M3 codes (the transposed weight: y = x @ wt^T), row stride >= k, device
+ *   wt_scale binary32, contiguous, device: wt_block FAR_BLOCK_TILE [ceil(n / 128), ceil(k / 128)]
+ *            (ws[j, b] = wt_scale[j / 128, b]), FAR_BLOCK_ROW [n, ceil(k / 128)]
+ *   out      [m, n] out_dtype (FAR_F32, FAR_F16, FAR_BF16), row stride >= n, device
+ * Products of two codes are exact; a block's sum is taken by the tensor cores in binary32,
+ * scaled and added to the others in binary32, in an order that is not specified but the
+ * same every run.  NaN codes and scales give NaN; a zero scale with finite codes gives 0.
+ * Tensor cores (tcgen05) are used when the row strides of x and wt are multiples of 16 and
+ * x and wt lie on 16-byte boundaries; any other call takes a plain kernel with the same
+ * contract.  out shares no byte with another buffer.  k = 0 gives zeros; m = 0 or n = 0 is a
+ * no-op.  Statuses: FAR_ERR_DTYPE (out_dtype, wt_block), FAR_ERR_SHAPE (sizes negative or
+ * above 2^31 - 1, a row stride too small), FAR_ERR_NULL, FAR_ERR_ALIAS, FAR_ERR_CUDA.
+ */
+int gemm_fp8_block(const void* x, int64_t x_row_stride, const float* x_scale, const void* wt, int64_t wt_row_stride,
+                   const float* wt_scale, int wt_block, void* out, int64_t out_row_stride, int64_t m, int64_t n,
+                   int64_t k, int out_dtype, void* stream);
+
 /* the output dtype od of FAR_DTYPES(act, wd), or -status when the pair is rejected */
 int far_output_dtype(int dtype);
 

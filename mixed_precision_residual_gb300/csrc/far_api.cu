@@ -316,9 +316,9 @@ int validate_ln(const void* x, const void* r, const void* gamma, const void* bet
 // the quantised entry points: q and scale replace out and must share no byte with anything
 int validate_quant(const void* x, const void* r, const void* w, float eps, void* q, float* scale, void* res_out,
                    int64_t tokens, int64_t hidden, int dtype, int qtype, bool residual, Call& c,
-                   const Strides* strides = nullptr) {
-  if (qtype != kQuantInt8 && qtype != kQuantFp8) return FAR_ERR_DTYPE;
-  c.quant = qtype;
+                   const Strides* strides = nullptr, bool block = false) {
+  if (!block && qtype != kQuantInt8 && qtype != kQuantFp8) return FAR_ERR_DTYPE;
+  c.quant = block ? kQuantFp8Block : qtype;
   c.q = q;
   c.scale = scale;
   // q is always contiguous ([tokens, hidden] bytes); x, the residual and residual_out may
@@ -335,7 +335,8 @@ int validate_quant(const void* x, const void* r, const void* w, float eps, void*
   }
   const int64_t sa = dsize(c.act);
   const Region Q = region(q, tokens, hidden, hidden);
-  const Region S = region(scale, 1, tokens * 4, tokens * 4);
+  const int64_t scales = tokens * (block ? (hidden + kBlock - 1) / kBlock : 1);
+  const Region S = region(scale, 1, scales * 4, scales * 4);
   const Region X = region(x, tokens, hidden * sa, sd.x * sa);
   const Region W = region(w, 1, hidden * dsize(c.wd), hidden * dsize(c.wd));
   // q: one byte an element, never an exact alias of an input
@@ -726,7 +727,7 @@ int64_t claim_rows_for(const Call& c, const Launch& L, int mode) {
   // codes plus the row's binary32 scale (LayerNorm's beta, like the weight, is read once a
   // launch, not a row)
   const int64_t row_traffic = c.hidden * (dsize(c.act) * (c.residual ? 3 : 1) + (c.quant ? 1 : dsize(c.od))) +
-                              (c.quant ? 4 : 0);
+                              (c.quant == kQuantFp8Block ? (c.hidden + kBlock - 1) / kBlock * 4 : c.quant ? 4 : 0);
   const int64_t claim_rows = (45333 + row_traffic - 1) / row_traffic;
   const int64_t r0 = (int64_t)L.grid.x * L.p.stages;
   const bool packed16 = !c.residual && !c.ln && c.act != FAR_F32 && (c.quant || c.od != FAR_F32);
@@ -782,6 +783,12 @@ int launch(const Call& c, const DeviceState& dev, cudaStream_t stream) {
       case FAR_BF16: e = launch_ln_act_bf16(c.wd, c.residual, L); break;
       default: e = launch_ln_act_f32(c.wd, c.residual, L); break;
     }
+  } else if (c.quant == kQuantFp8Block) {
+    switch (c.act) {
+      case FAR_F16: e = launch_qb_act_f16(c.wd, c.residual, L); break;
+      case FAR_BF16: e = launch_qb_act_bf16(c.wd, c.residual, L); break;
+      default: e = launch_qb_act_f32(c.wd, c.residual, L); break;
+    }
   } else if (c.quant) {
     switch (c.act) {
       case FAR_F16: e = launch_q_act_f16(c.wd, c.residual, L); break;
@@ -815,9 +822,9 @@ int run(const void* x, const void* r, const void* w, float eps, void* out, void*
 
 int run_quant(const void* x, const void* r, const void* w, float eps, void* q, float* scale, void* res_out,
               int64_t tokens, int64_t hidden, int dtype, int qtype, bool residual, void* stream,
-              const Strides* strides = nullptr) {
+              const Strides* strides = nullptr, bool block = false) {
   Call c;
-  int st = validate_quant(x, r, w, eps, q, scale, res_out, tokens, hidden, dtype, qtype, residual, c, strides);
+  int st = validate_quant(x, r, w, eps, q, scale, res_out, tokens, hidden, dtype, qtype, residual, c, strides, block);
   if (st != FAR_OK || tokens == 0) return st;
   DeviceState* dev = nullptr;
   st = current_device(dev);
@@ -1101,6 +1108,20 @@ int fused_add_layernorm(const void* x, const void* residual, const void* gamma, 
 int layernorm(const void* x, const void* gamma, const void* beta, float eps, void* out, int64_t tokens,
               int64_t hidden, int dtype, void* stream) {
   return run_ln(x, nullptr, gamma, beta, eps, out, nullptr, tokens, hidden, dtype, false, stream);
+}
+
+int fused_add_rmsnorm_quant_block(const void* x, int64_t x_row_stride, const void* residual,
+                                  int64_t residual_row_stride, const void* weight, float eps, void* q, float* scale,
+                                  void* residual_out, int64_t residual_out_row_stride, int64_t tokens, int64_t hidden,
+                                  int dtype, void* stream) {
+  Strides sd{x_row_stride, residual_row_stride, hidden, residual_out_row_stride};
+  return run_quant(x, residual, weight, eps, q, scale, residual_out, tokens, hidden, dtype, 0, true, stream, &sd, true);
+}
+
+int rmsnorm_quant_block(const void* x, int64_t x_row_stride, const void* weight, float eps, void* q, float* scale,
+                        int64_t tokens, int64_t hidden, int dtype, void* stream) {
+  Strides sd{x_row_stride, hidden, hidden, hidden};
+  return run_quant(x, nullptr, weight, eps, q, scale, nullptr, tokens, hidden, dtype, 0, false, stream, &sd, true);
 }
 
 int fused_add_layernorm_strided(const void* x, int64_t x_row_stride, const void* residual,

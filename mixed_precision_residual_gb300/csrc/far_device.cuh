@@ -425,10 +425,25 @@ template <> __device__ __forceinline__ uint32_t quantise4<1>(float a, float b, f
   asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(qd) : "f"(d));
   return __byte_perm(__byte_perm(qa, qb, 0x0040), __byte_perm(qc, qd, 0x0040), 0x5410);
 }
-template <> __device__ __forceinline__ uint32_t quantise4<2>(float a, float b, float c, float d) {
+template <> __device__ __forceinline__ uint32_t quantise4<kQuantFp8>(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return __byte_perm(lo, hi, 0x5410);
+}
+
+// 128-block quantisation to E4M3: scale = amax / 448 and the factor 448 / amax that the
+// values are multiplied by, both IEEE divisions.  A block whose largest magnitude is below
+// 2^-100 counts as zero (scale 0, codes 0): further down 448 / amax would leave binary32's
+// range and turn the block's zeros into NaN.  NaN and infinite blocks keep a NaN / infinite scale.
+constexpr int kBlock = 128;
+constexpr float kBlockTiny = 7.888609052210118e-31f;  // 2^-100
+__device__ __forceinline__ float block_scale(float amax) { return amax < kBlockTiny ? 0.f : __fdiv_rn(amax, 448.0f); }
+__device__ __forceinline__ float block_inverse(float amax) { return amax < kBlockTiny ? 0.f : __fdiv_rn(448.0f, amax); }
+
+// the largest value over aligned groups of `lanes` lanes (NaN-propagating)
+__device__ __forceinline__ float lanes_max(float v, int lanes) {
+  for (int off = lanes >> 1; off > 0; off >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, off));
+  return v;
 }
 
 // rstd from the row's sum of squares, IEEE-rounded at every step:

@@ -467,12 +467,18 @@ __global__ void __launch_bounds__(max_threads(NCH, packed_rows(RES, ACT) && !LN)
     // row's largest |out| is known.
     char* orow = Q ? nullptr : static_cast<char*>(p.out) + row * p.out_stride;
     char* rrow = (RES && !LN) ? static_cast<char*>(p.res_out) + row * p.res_stride : nullptr;
-    uint32_t okeep[Q ? NCH : 1][Q ? OB / 4 : 1];
+    constexpr bool ROWQ = Q == kQuantInt8 || Q == kQuantFp8;  // one scale a row
+    constexpr bool BLKQ = Q == kQuantFp8Block;                // one scale for each 128 values
+    uint32_t okeep[ROWQ ? NCH : 1][Q ? OB / 4 : 1];
     float amax = 0.f;
     uint32_t amax2 = 0u;  // packed running max of |out| for a 16-bit out
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       const Where w = where(j);
+      if constexpr (BLKQ) {
+#pragma unroll
+        for (int e = 0; e < OB / 4; ++e) okeep[0][e] = 0u;  // a chunk past the row adds nothing to its block
+      }
       if (w.va) {
         float sj[V];  // s for this chunk: kept in registers, or widened from the packed x
         if constexpr (PACKED) widen<ACT, V>(xk[j], sj);
@@ -533,7 +539,10 @@ __global__ void __launch_bounds__(max_threads(NCH, packed_rows(RES, ACT) && !LN)
           for (int e = 0; e < V; ++e) o[e] = __fmul_rn(o[e], wf[e]);
           narrow<OD, V>(o, ow);
         }
-        if constexpr (Q) {
+        if constexpr (BLKQ) {
+#pragma unroll
+          for (int e = 0; e < OB / 4; ++e) okeep[0][e] = ow[e];
+        } else if constexpr (Q) {
           if constexpr (OD == FAR_F32) {
 #pragma unroll
             for (int e = 0; e < V; ++e) amax = max_nan(amax, fabsf(__uint_as_float(ow[e])));
@@ -553,8 +562,43 @@ __global__ void __launch_bounds__(max_threads(NCH, packed_rows(RES, ACT) && !LN)
           store_row(rrow, w, rw, std::integral_constant<int, 16>{});
         }
       }
+      if constexpr (BLKQ) {
+        // a block of 128 values is the same chunk of 128 / V neighbouring lanes: its maximum is
+        // a few shuffles, and its codes leave at once (nothing is kept for a second sweep)
+        constexpr int LANES = kBlock / V;
+        float bm = 0.f;
+        if constexpr (OD == FAR_F32) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) bm = max_nan(bm, fabsf(__uint_as_float(okeep[0][e])));
+        } else {
+          uint32_t m2 = 0u;
+#pragma unroll
+          for (int e = 0; e < OB / 4; ++e) m2 = habs_max2<OD>(m2, okeep[0][e]);
+          const float2 f2 = widen2<OD>(m2);
+          bm = max_nan(f2.x, f2.y);
+        }
+        bm = lanes_max(bm, LANES);
+        const float inv = block_inverse(bm);
+        if (w.va) {
+          if ((lane & (LANES - 1)) == 0)
+            p.scale[row * (int64_t)((p.hidden + kBlock - 1) / kBlock) + w.pa / LANES] = block_scale(bm);
+          float of[V];
+          widen<OD, V>(okeep[0], of);
+          uint32_t qw[V / 4];
+#pragma unroll
+          for (int e = 0; e < V / 4; ++e)
+            qw[e] = quantise4<kQuantFp8>(__fmul_rn(of[4 * e], inv), __fmul_rn(of[4 * e + 1], inv),
+                                         __fmul_rn(of[4 * e + 2], inv), __fmul_rn(of[4 * e + 3], inv));
+          unsigned char* qrow = static_cast<unsigned char*>(p.q) + row * (int64_t)p.hidden;
+          if constexpr (V == 8) {
+            store_bytes<8>(qrow + (size_t)w.pa * 8, qw);
+          } else {
+            asm volatile("st.global.b32 [%0], %1;" ::"l"(qrow + (size_t)w.pa * 4), "r"(qw[0]) : "memory");
+          }
+        }
+      }
     }
-    if constexpr (Q) {
+    if constexpr (ROWQ) {
       if constexpr (OD != FAR_F32) {
         const float2 m2 = widen2<OD>(amax2);
         amax = max_nan(m2.x, m2.y);
@@ -736,18 +780,49 @@ __global__ void __launch_bounds__(kGenericThreads) generic_kernel(const Params p
     char* orow = Q ? nullptr : static_cast<char*>(p.out) + row * p.out_stride;
     char* rrow = RES ? static_cast<char*>(p.res_out) + row * p.res_stride : nullptr;
     float amax = 0.f;
-    for (int64_t i = threadIdx.x; i < H; i += blockDim.x) {
-      float s = load_elem<ACT>(xr, i);  // each element is read and written by the same thread
-      if constexpr (RES) {
-        s = __fadd_rn(s, load_elem<ACT>(rr, i));
-        store_elem<ACT>(rrow, i, s);
+    if constexpr (Q != kQuantFp8Block) {
+      for (int64_t i = threadIdx.x; i < H; i += blockDim.x) {
+        float s = load_elem<ACT>(xr, i);  // each element is read and written by the same thread
+        if constexpr (RES) {
+          s = __fadd_rn(s, load_elem<ACT>(rr, i));
+          // (with a quantised output the row is read once more: residual_out, which may be x or
+          // the residual themselves, is stored in that last sweep)
+          if constexpr (Q == kQuantNone) store_elem<ACT>(rrow, i, s);
+        }
+        const float n = round_one<WD>(__fmul_rn(s, rstd));
+        const float o = __fmul_rn(n, load_elem<WD>(p.w, i));
+        if constexpr (Q) amax = max_nan(amax, fabsf(round_one<OD>(o)));
+        else store_elem<OD>(orow, i, o);
       }
-      const float n = round_one<WD>(__fmul_rn(s, rstd));
-      const float o = __fmul_rn(n, load_elem<WD>(p.w, i));
-      if constexpr (Q) amax = max_nan(amax, fabsf(round_one<OD>(o)));
-      else store_elem<OD>(orow, i, o);
     }
-    if constexpr (Q) {
+    if constexpr (Q == kQuantFp8Block) {
+      // second pass, two blocks of 128 values at a time: out, the block's maximum over its four
+      // warps, then its codes
+      unsigned char* qrow = static_cast<unsigned char*>(p.q) + row * H;
+      float* srow = p.scale + row * ((H + kBlock - 1) / kBlock);
+      for (int64_t base = 0; base < H; base += kGenericThreads) {
+        const int64_t i = base + threadIdx.x;
+        float o = 0.f;
+        if (i < H) {
+          float s = load_elem<ACT>(xr, i);
+          if constexpr (RES) {
+            s = __fadd_rn(s, load_elem<ACT>(rr, i));
+            store_elem<ACT>(rrow, i, s);
+          }
+          o = round_one<OD>(__fmul_rn(round_one<WD>(__fmul_rn(s, rstd)), load_elem<WD>(p.w, i)));
+        }
+        const float wm = warp_max_allreduce(fabsf(o));
+        if (lane == 0) mpart[warp] = wm;
+        __syncthreads();
+        const int w0 = warp & ~3;
+        const float m = max_nan(max_nan(mpart[w0], mpart[w0 + 1]), max_nan(mpart[w0 + 2], mpart[w0 + 3]));
+        __syncthreads();  // `mpart` is reused by the next two blocks
+        if (i < H) {
+          if ((threadIdx.x & (kBlock - 1)) == 0) srow[i / kBlock] = block_scale(m);
+          qrow[i] = (unsigned char)(quantise4<kQuantFp8>(__fmul_rn(o, block_inverse(m)), 0.f, 0.f, 0.f) & 0xffu);
+        }
+      }
+    } else if constexpr (Q != kQuantNone) {
       // third pass: the row's largest |out|, then the quantised bytes (out recomputed)
       amax = warp_max_allreduce(amax);
       if (lane == 0) mpart[warp] = amax;
@@ -761,7 +836,10 @@ __global__ void __launch_bounds__(kGenericThreads) generic_kernel(const Params p
       unsigned char* qrow = static_cast<unsigned char*>(p.q) + row * H;
       for (int64_t i = threadIdx.x; i < H; i += blockDim.x) {
         float s = load_elem<ACT>(xr, i);
-        if constexpr (RES) s = __fadd_rn(s, load_elem<ACT>(rr, i));
+        if constexpr (RES) {
+          s = __fadd_rn(s, load_elem<ACT>(rr, i));
+          store_elem<ACT>(rrow, i, s);
+        }
         const float n = round_one<WD>(__fmul_rn(s, rstd));
         const float v = __fmul_rn(round_one<OD>(__fmul_rn(n, load_elem<WD>(p.w, i))), inv);
         qrow[i] = (unsigned char)(quantise4<Q>(v, 0.f, 0.f, 0.f) & 0xffu);
@@ -851,6 +929,12 @@ cudaError_t launch_quant(bool residual, const Launch& L) {
   if (L.quant == kQuantFp8)
     return residual ? launch_typed<ACT, WD, true, kQuantFp8>(L) : launch_typed<ACT, WD, false, kQuantFp8>(L);
   return cudaErrorInvalidValue;
+}
+
+// an E4M3 output with a scale for each 128 values
+template <int ACT, int WD>
+cudaError_t launch_quant_block(bool residual, const Launch& L) {
+  return residual ? launch_typed<ACT, WD, true, kQuantFp8Block>(L) : launch_typed<ACT, WD, false, kQuantFp8Block>(L);
 }
 
 // LayerNorm (plain output)

@@ -53,7 +53,7 @@ struct Params {
   uint32_t w_smem_bytes; // hidden * sizeof(wd), rounded up to 16 (twice that for LayerNorm: gamma, beta)
   uint32_t stage_bytes;  // bytes of one ring slot (x row, then residual row), 128-aligned
   void* q;               // quantised output [tokens, hidden] bytes (quantised variants)
-  float* scale;          // per-row scale [tokens] (quantised variants)
+  float* scale;          // scales [tokens], or [tokens, ceil(hidden / 128)] (quantised variants)
   unsigned int* status;  // device error word
   uint64_t timeout_ns;
   // staged kernel: this launch's row counter pair {next row claim, CTAs done}, zero at
@@ -65,7 +65,9 @@ struct Params {
 
 enum Kind { kStaged = 0, kGeneric = 1 };
 
-enum QuantKind { kQuantNone = 0, kQuantInt8 = 1, kQuantFp8 = 2 };
+// kQuantFp8Block: E4M3 with a scale for each 128 values of a row (its own entry points; the
+// others take the first two by number)
+enum QuantKind { kQuantNone = 0, kQuantInt8 = 1, kQuantFp8 = 2, kQuantFp8Block = 3 };
 
 struct Launch {
   Params p;
@@ -81,9 +83,11 @@ struct Launch {
 };
 
 // cross-warp reduction buffers per group: two (the sum of squares, double-buffered over
-// rows), four with a quantised output (the row maximum too) or for LayerNorm (the sum
-// for the mean, then the sum of the squared deviations)
-__host__ __device__ constexpr int reduce_buffers(int q, bool ln = false) { return (q || ln) ? 4 : 2; }
+// rows), four with a row-quantised output (the row maximum too) or for LayerNorm (the sum
+// for the mean, then the sum of the squared deviations); a block's maximum stays in its warp
+__host__ __device__ constexpr int reduce_buffers(int q, bool ln = false) {
+  return (q == kQuantInt8 || q == kQuantFp8 || ln) ? 4 : 2;
+}
 
 // shared-memory bytes the staged kernel needs for a plan
 inline size_t staged_smem_bytes(int stages, int groups, int warps_per_row, uint32_t w_smem_bytes,
@@ -103,6 +107,9 @@ cudaError_t launch_act_f32(int wd, bool residual, const Launch& L);
 cudaError_t launch_q_act_f16(int wd, bool residual, const Launch& L);
 cudaError_t launch_q_act_bf16(int wd, bool residual, const Launch& L);
 cudaError_t launch_q_act_f32(int wd, bool residual, const Launch& L);
+cudaError_t launch_qb_act_f16(int wd, bool residual, const Launch& L);
+cudaError_t launch_qb_act_bf16(int wd, bool residual, const Launch& L);
+cudaError_t launch_qb_act_f32(int wd, bool residual, const Launch& L);
 cudaError_t launch_ln_act_f16(int wd, bool residual, const Launch& L);
 cudaError_t launch_ln_act_bf16(int wd, bool residual, const Launch& L);
 cudaError_t launch_ln_act_f32(int wd, bool residual, const Launch& L);

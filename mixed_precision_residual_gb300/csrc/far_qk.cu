@@ -21,6 +21,7 @@
 
 #include "far.h"
 #include "far_device.cuh"
+#include "far_launch.h"
 #include "far_params.h"
 #include "far_region.h"
 
@@ -740,21 +741,6 @@ QkPlan plan_qk(const QkCall& c, int sms) {
   g.block = dim3(32 * warps);
   g.smem = c.back ? (size_t)warps * D * 4 : 0;
   return g;
-}
-
-template <typename... A>
-cudaError_t launch_k(void (*k)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = far_get_programmatic_launch() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
 template <int ACT>

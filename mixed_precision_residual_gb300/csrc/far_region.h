@@ -33,8 +33,8 @@ inline bool regions_overlap(const Region& A, const Region& B) {
   const int64_t d = (int64_t)(B.base - A.base);
   const int64_t kmin = floor_div(-B.width - d, s) + 1;
   const int64_t kmax = -floor_div(-(A.width - d), s) - 1;  // ceil((A.width - d) / s) - 1
-  const int64_t lo = kmin > -(B.rows - 1) ? kmin : -(B.rows - 1);
-  const int64_t hi = kmax < (A.rows - 1) ? kmax : (A.rows - 1);
+  const int64_t lo = kmin > -(A.rows - 1) ? kmin : -(A.rows - 1);  // j - i, 0 <= i < A.rows, 0 <= j < B.rows
+  const int64_t hi = kmax < (B.rows - 1) ? kmax : (B.rows - 1);
   return lo <= hi;
 }
 

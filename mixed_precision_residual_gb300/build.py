@@ -22,7 +22,7 @@ SOURCES = ["far_api.cu", "far_inst_f16.cu", "far_inst_bf16.cu", "far_inst_f32.cu
            "far_inst_q_bf16.cu", "far_inst_q_f32.cu", "far_inst_ln_f16.cu", "far_inst_ln_bf16.cu",
            "far_inst_ln_f32.cu", "far_inst_qb_f16.cu", "far_inst_qb_bf16.cu", "far_inst_qb_f32.cu", "far_noalloc.cu",
            "far_gemm.cu", "far_qk.cu", "far_qblock.cu", "far_gemm8.cu"]
-HEADERS = ["far_launch.h", "far_region.h", "far_device.cuh", "far_kernels.cuh", "far_params.h", "far_tcgen05.cuh"]
+HEADERS = ["far_launch.h", "far_region.h", "far_device.cuh", "far_kernels.cuh", "far_params.h", "far_tcgen05.cuh", "far_tma.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-fmad=false",
                      "-ftz=false", "-prec-div=true", "-prec-sqrt=true",

@@ -32,6 +32,7 @@
 #include "far.h"
 #include "far_params.h"
 #include "far_tcgen05.cuh"
+#include "far_tma.h"
 
 namespace far {
 
@@ -462,11 +463,8 @@ __global__ void __launch_bounds__(256) generic_gemm_kernel(const GemmParams p) {
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-namespace {
-
-std::mutex g_encode_mu;
-std::atomic<int> g_gemm_force_kind{-1}, g_gemm_force_bn{0};  // tuning override (-1 / 0: automatic)
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+static std::mutex g_encode_mu;
+static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 int get_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) {
   std::lock_guard<std::mutex> lk(g_encode_mu);
@@ -480,6 +478,10 @@ int get_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) {
   *fn = g_encode;
   return FAR_OK;
 }
+
+namespace {
+
+std::atomic<int> g_gemm_force_kind{-1}, g_gemm_force_bn{0};  // tuning override (-1 / 0: automatic)
 
 // a row-major [rows, K] fp16 matrix read in boxes of box_rows x 64, 128-byte swizzled;
 // out-of-range elements of a box read as zero

@@ -2,6 +2,16 @@
 // (gemm_fp8_block):
 //   out[i, j] = RNE( sum_b xs[i, b] ws[j, b] sum_{k in b} x[i, k] wt[j, k] ).
 //
+// The scales are arbitrary binary32 values, so the tensor cores sum one block of 128 at a
+// time (four tcgen05.mma of 32 values) into TMEM, and the block's sums are scaled and added
+// to the result in registers ("promoted").  Per block a tile's every accumulator is loaded
+// from TMEM and takes one or two FMA-pipe operations while the tensor cores work on the next
+// block in the other half of TMEM; the register tile is what limits the tile's size.
+//
+// pair_kernel  -- many rows: 256 x 256 tiles over CTA pairs, x's rows on the TMEM lanes.
+// small_kernel -- few rows (a decode batch): wt's rows on the lanes, 16 to 128 rows of x as the
+//                 columns, k split over a cluster of CTAs that add their sums through
+//                 distributed shared memory.  Bound by reading wt once.
 // plain_kernel -- any shape, stride and alignment: 64 x 64 tiles in binary32.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -11,8 +21,12 @@
 #include "far_launch.h"
 #include "far_params.h"
 #include "far_region.h"
+#include "far_tcgen05.cuh"
+#include "far_tma.h"
 
 namespace far {
+
+cudaError_t ensure_smem_attribute(const void* func, size_t bytes);
 
 namespace {
 
@@ -26,6 +40,10 @@ struct Gemm8Params {
   int32_t M, N, K, KB;    // KB: blocks of 128 along k
   int32_t tile_scales;    // ws: one a 128 rows of wt (1) or one a row (0)
   int32_t out_dtype;
+  int32_t out_align;      // bytes that out and its row stride are multiples of: 32, 16 or less
+  int32_t tiles_m, tiles_n, num_tiles;  // pair_kernel
+  unsigned int* status;
+  uint64_t timeout_ns;
 };
 
 __device__ __forceinline__ float e4m3_value(unsigned char c) {
@@ -95,6 +113,540 @@ __global__ void __launch_bounds__(256) plain_kernel(const Gemm8Params p) {
   }
 }
 
+__device__ __forceinline__ uint64_t fma_x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pk_bits(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+
+// The scales of blocks kb .. kb + 3 of one row of a [rows, KB] scale matrix (0 past the end, or
+// without a row): consecutive in memory, one sector or two.
+struct Scale4 {
+  float v[4];
+  __device__ __forceinline__ void load(const float* row, int kb, int KB) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = row != nullptr && kb + j < KB ? __ldg(row + kb + j) : 0.f;
+  }
+  __device__ __forceinline__ float at(int j) const {
+    return j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3];
+  }
+};
+
+// A ring of column scales in shared memory: slot kb % kScaleSlots holds the scales of block kb for
+// the tile's columns.  One warp fills it four blocks at a time (their values are neighbours
+// in memory), the epilogue warps read it.
+constexpr int kScaleSlots = 8;
+template <int COLS>
+__device__ __forceinline__ bool fill_scales(float* ring, uint32_t full0, uint32_t empty0, const float* scales,
+                                            int64_t first, int64_t rows, int kb0, int kb1, int KB, uint32_t g0, int lane,
+                                            const Gemm8Params& p) {
+  constexpr int PER = (COLS + 31) / 32;
+  for (int kb = kb0; kb < kb1; kb += 4) {
+    float v[PER][4];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = lane + 32 * i;
+      const bool in = c < COLS && first + c < rows;
+      const float* src = scales + (first + c) * KB;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i][j] = in && kb + j < kb1 ? __ldg(src + kb + j) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (kb + j >= kb1) break;
+      const uint32_t g = g0 + (uint32_t)(kb + j - kb0), slot = g % kScaleSlots;
+      if (!mbar_wait(empty0 + 8 * slot, ((g / kScaleSlots) & 1u) ^ 1u, p.timeout_ns, p.status)) return false;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (lane + 32 * i < COLS) ring[slot * COLS + lane + 32 * i] = v[i][j];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full0 + 8 * slot);
+    }
+  }
+  return true;
+}
+
+// 32 neighbouring outputs of one row
+__device__ __forceinline__ void store_row32(const Gemm8Params& p, int64_t row, int64_t col, const float* v) {
+  if (row >= p.M || col >= p.N) return;
+  if (col + 32 <= p.N && p.out_align >= 16) {
+    uint32_t w[32];
+    int words;
+    if (p.out_dtype == FAR_F32) {
+      narrow<FAR_F32, 32>(v, w);
+      words = 32;
+    } else {
+      if (p.out_dtype == FAR_F16) narrow<FAR_F16, 32>(v, w);
+      else narrow<FAR_BF16, 32>(v, w);
+      words = 16;
+    }
+    char* o = static_cast<char*>(p.out) + (row * p.ldo + col) * (p.out_dtype == FAR_F32 ? 4 : 2);
+    if (p.out_align >= 32) {
+      // a whole 32-byte sector a lane and instruction
+#pragma unroll
+      for (int i = 0; i < 32; i += 8)
+        if (i < words)
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + 4 * i), "r"(w[i]),
+                       "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
+                       "r"(w[i + 7])
+                       : "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; i += 4)
+        if (i < words) *reinterpret_cast<uint4*>(o + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (col + i < p.N) store_out(p, row, col + i, v[i]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// pair_kernel: 256 x 256 output tiles over a cluster of 2.  Each CTA holds its 128 rows of x
+// and half of the tile's rows of wt (up to 128) per block of k; one thread of the even CTA issues
+// tcgen05.mma.cta_group::2 over both, each CTA's TMEM receiving the sums of its 128 rows.
+//   warp 0      TMA producer (both CTAs), a ring of kPairStages blocks of k running across tiles
+//   warp 1      MMA issuer (even CTA); allocates TMEM: two halves of 256 columns
+//   warp 2      column scales (wt scaled by rows)
+//   warps 4-11  epilogue: warp w the TMEM lanes 32 (w % 4) .., columns 128 ((w - 4) / 4) ..; a
+//               thread keeps 128 outputs of one row in registers
+// The registers a thread: 384 threads are launched at 168; warps 0-3 give theirs up to 72 and
+// the epilogue's take 216 (128 x 72 + 256 x 216 = 384 x 168).
+// The last column of tiles runs at the width that is left (a multiple of 32).
+// ---------------------------------------------------------------------------
+constexpr int kPairThreads = 384;
+constexpr int kPairStages = 6;
+constexpr uint32_t kPairABytes = 128 * kBlock, kPairBBytes = 128 * kBlock;
+constexpr uint32_t kPairRing = kPairStages * (kPairABytes + kPairBBytes);
+constexpr int kPairBars = 2 * kPairStages + 4 + 2 * kScaleSlots;
+constexpr size_t kPairSmem = kPairRing + kScaleSlots * 256 * 4 + kPairBars * 8 + 16 + 1024;
+constexpr int kPairGroup = 8;  // tile rows that are walked together, so that CTAs at work share panels in L2
+
+struct PairTile {
+  int64_t row0, col0;
+  int cols;  // of the tile, 32 .. 256
+};
+__device__ __forceinline__ PairTile pair_tile(const Gemm8Params& p, int t) {
+  const int per = kPairGroup * p.tiles_n, g = t / per, first = g * kPairGroup;
+  const int gm = min(p.tiles_m - first, kPairGroup), r = t - g * per;
+  PairTile w;
+  w.row0 = (int64_t)(first + r % gm) * 256;
+  w.col0 = (int64_t)(r / gm) * 256;
+  const int64_t left = p.N - w.col0;
+  w.cols = left >= 256 ? 256 : (int)((left + 31) / 32 * 32);
+  return w;
+}
+
+template <bool COLS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const Gemm8Params p) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  unsigned char* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);  // the same offset in both CTAs
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t a_base = sbase, b_base = sbase + kPairStages * kPairABytes;
+  float* scales = reinterpret_cast<float*>(smem + kPairRing);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kPairRing + kScaleSlots * 256 * 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kPairBars);
+  const uint32_t full0 = smem_addr(&bars[0]), empty0 = smem_addr(&bars[kPairStages]);
+  const uint32_t acc_full0 = smem_addr(&bars[2 * kPairStages]), acc_empty0 = acc_full0 + 16;
+  const uint32_t sc_full0 = acc_full0 + 32, sc_empty0 = sc_full0 + 8 * kScaleSlots;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_cta_rank();
+  const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);   // even CTA: its producer's arrive + both CTAs' bytes
+      mbar_init(empty0 + 8 * s, 1);  // one multicast commit
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(acc_full0 + 8 * a, 1);    // one multicast commit
+      mbar_init(acc_empty0 + 8 * a, 16);  // even CTA: 8 epilogue warps in each CTA
+    }
+    for (int s = 0; s < kScaleSlots; ++s) {
+      mbar_init(sc_full0 + 8 * s, 1);   // the scale warp
+      mbar_init(sc_empty0 + 8 * s, 8);  // this CTA's epilogue warps
+    }
+    fence_barrier_init();
+    tma_prefetch_map(&map_x);
+    tma_prefetch_map(&map_w);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_addr(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any remote arrive or copy
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0 && lane == 0) {
+      // ---------------- TMA producer (both CTAs) ----------------
+      uint32_t g = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < p.num_tiles; t += pairs) {
+        const PairTile w = pair_tile(p, t);
+        const int x_row = (int)w.row0 + (int)rank * 128, w_row = (int)w.col0 + (int)rank * (w.cols / 2);
+        for (int kb = 0; kb < p.KB; ++kb, ++g) {
+          const uint32_t s = g % kPairStages;
+          if (!mbar_wait(empty0 + 8 * s, ((g / kPairStages) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * (kPairABytes + kPairBBytes));
+          const uint32_t full_even = map_to_cta(full0 + 8 * s, 0);
+          tma_load_2d_pair(a_base + s * kPairABytes, &map_x, kb * kBlock, x_row, full_even);
+          tma_load_2d_pair(b_base + s * kPairBBytes, &map_w, kb * kBlock, w_row, full_even);
+        }
+      }
+      if (rank == 0)  // the pair's copies of the last blocks must have landed before exit
+        for (uint32_t j = (g > (uint32_t)kPairStages ? g - kPairStages : 0u); j < g; ++j)
+          mbar_wait(full0 + 8 * (j % kPairStages), (j / kPairStages) & 1u, p.timeout_ns, p.status);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ---------------- MMA issuer (even CTA) ----------------
+      uint32_t g = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < p.num_tiles; t += pairs) {
+        const uint32_t idesc = umma_idesc_e4m3_f32(256, pair_tile(p, t).cols);
+        for (int kb = 0; kb < p.KB; ++kb, ++g) {
+          const uint32_t s = g % kPairStages, acc = g & 1u;
+          if (!mbar_wait(full0 + 8 * s, (g / kPairStages) & 1u, p.timeout_ns, p.status) ||
+              !mbar_wait_cluster(acc_empty0 + 8 * acc, ((g >> 1) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = a_base + s * kPairABytes, b = b_base + s * kPairBBytes;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_e4m3_pair(tmem + acc * 256, sw128_kmajor_desc(a + k * 32), sw128_kmajor_desc(b + k * 32), idesc, k != 0);
+          umma_commit_pair(empty0 + 8 * s, 0x3);       // both CTAs' slots are free once read
+          umma_commit_pair(acc_full0 + 8 * acc, 0x3);  // the block's sums are there
+        }
+      }
+    } else if (COLS && warp == 2) {
+      uint32_t g = 0;
+      for (int t = pair; t < p.num_tiles; t += pairs, g += p.KB)
+        if (!fill_scales<256>(scales, sc_full0, sc_empty0, p.ws, pair_tile(p, t).col0, p.N, 0, p.KB, p.KB, g, lane, p)) break;
+    }
+  } else {
+    // ---------------- epilogue ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * 128);
+    uint32_t g = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < p.num_tiles; t += pairs) {
+      const PairTile w = pair_tile(p, t);
+      const int64_t row = w.row0 + (int)rank * 128 + quarter * 32 + lane;
+      const int64_t col = w.col0 + half * 128;
+      const int mine = w.cols - half * 128;  // columns of this half (may be none)
+      const float* xrow = row < p.M ? p.xs + row * p.KB : nullptr;
+      const float* wrow = !COLS && col < p.N ? p.ws + col / kBlock * p.KB : nullptr;
+      Scale4 xn, wn;
+      xn.load(xrow, 0, p.KB);
+      if constexpr (!COLS) wn.load(wrow, 0, p.KB);
+      uint64_t acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+      for (int kb4 = 0; ok && kb4 < p.KB; kb4 += 4) {
+        Scale4 sc;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc.v[j] = COLS ? xn.v[j] : __fmul_rn(xn.v[j], wn.v[j]);
+        xn.load(xrow, kb4 + 4, p.KB);  // the next four blocks', while these are worked on
+        if constexpr (!COLS) wn.load(wrow, kb4 + 4, p.KB);
+#pragma unroll 1
+        for (int j = 0; j < 4 && kb4 + j < p.KB; ++j, ++g) {
+          const uint32_t buf = g & 1u, slot = g % kScaleSlots;
+          const float sr = sc.at(j);
+          const uint64_t s2 = pk(sr, sr);
+          if (!mbar_wait(acc_full0 + 8 * buf, (g >> 1) & 1u, p.timeout_ns, p.status) ||
+              (COLS && !mbar_wait(sc_full0 + 8 * slot, (g / kScaleSlots) & 1u, p.timeout_ns, p.status))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const float4* cs = reinterpret_cast<const float4*>(scales + slot * 256 + half * 128);
+          // 16 columns at a time, the next 16 on their way while these are added
+          uint32_t r[2][16];
+          if (mine > 0) {
+            tmem_ld16(lanes + buf * 256, r[0]);
+            tmem_ld_wait(r[0]);
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const bool more = c < 7 && mine > 16 * (c + 1);
+            if (more) tmem_ld16(lanes + buf * 256 + 16 * (c + 1), r[(c + 1) & 1]);
+            if (!more && (mine > 16 * c || c == 0)) {
+              // this warp's last columns have been read: its share of the buffer is free
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(map_to_cta(acc_empty0 + 8 * buf, 0));
+            }
+            if (mine > 16 * c) {
+#pragma unroll
+              for (int i = 0; i < 8; i += 2) {
+                uint64_t v0 = pk_bits(r[c & 1][2 * i], r[c & 1][2 * i + 1]);
+                uint64_t v1 = pk_bits(r[c & 1][2 * i + 2], r[c & 1][2 * i + 3]);
+                if constexpr (COLS) {
+                  const float4 q = cs[4 * c + i / 2];
+                  v0 = mul_x2(v0, pk(q.x, q.y));
+                  v1 = mul_x2(v1, pk(q.z, q.w));
+                }
+                acc[8 * c + i] = fma_x2(v0, s2, acc[8 * c + i]);
+                acc[8 * c + i + 1] = fma_x2(v1, s2, acc[8 * c + i + 1]);
+              }
+            }
+            if (more) tmem_ld_wait(r[(c + 1) & 1]);
+          }
+          if constexpr (COLS) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sc_empty0 + 8 * slot);
+          }
+        }
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (mine > 32 * c) {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 f = unpk(acc[16 * c + i]);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+          }
+          store_row32(p, row, col + 32 * c, v);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while its peer may still signal its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// small_kernel: 128 rows of wt x NT rows of x a CTA, the blocks of k shared out over a cluster
+// of gridDim's x dimension (CTA rank r takes blocks KB r / S .. KB (r + 1) / S - 1).
+//   warp 0 TMA producer, 1 MMA issuer (and TMEM), 2 x's scales, 4-7 epilogue: a thread keeps the NT
+//   sums of one row of wt.
+// Then each CTA leaves its sums in its shared memory and adds up every S-th row of x over the
+// cluster's CTAs, in the order of k.
+// ---------------------------------------------------------------------------
+constexpr int kSmallThreads = 256;
+template <int NT>
+struct SmallShape {
+  static constexpr int ctas = NT <= 64 ? 2 : 1;    // CTAs an SM
+  static constexpr int bufs = NT <= 64 ? 4 : 2;    // TMEM accumulators
+  static constexpr uint32_t a_bytes = 128 * kBlock, b_bytes = NT * kBlock;
+  static constexpr int stages = NT == 16 ? 5 : NT == 32 ? 5 : NT == 64 ? 4 : 6;
+  static constexpr uint32_t ring = stages * (a_bytes + b_bytes);
+  static constexpr uint32_t tmem_cols = bufs * NT < 32 ? 32 : bufs * NT;
+  static constexpr int bars = 2 * stages + 2 * bufs + 2 * kScaleSlots;
+  static constexpr size_t smem = ring + kScaleSlots * NT * 4 + bars * 8 + 16 + 1024;
+  static_assert(NT * 128 * 4 <= ring, "the sums that the cluster adds up lie in the ring");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kSmallThreads, SmallShape<NT>::ctas)
+    small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const Gemm8Params p) {
+  using S = SmallShape<NT>;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  unsigned char* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);  // the same offset in every CTA
+  const uint32_t a_base = smem_addr(smem), b_base = a_base + S::stages * S::a_bytes;
+  float* scales = reinterpret_cast<float*>(smem + S::ring);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::ring + kScaleSlots * NT * 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + S::bars);
+  const uint32_t full0 = smem_addr(&bars[0]), empty0 = full0 + 8 * S::stages;
+  const uint32_t acc_full0 = empty0 + 8 * S::stages, acc_empty0 = acc_full0 + 8 * S::bufs;
+  const uint32_t sc_full0 = acc_empty0 + 8 * S::bufs, sc_empty0 = sc_full0 + 8 * kScaleSlots;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = (int)gridDim.x, rank = (int)blockIdx.x;  // the cluster spans gridDim.x
+  const int64_t n0 = (int64_t)blockIdx.y * 128, m0 = (int64_t)blockIdx.z * NT;
+  const int kb0 = (int)((int64_t)p.KB * rank / split), kb1 = (int)((int64_t)p.KB * (rank + 1) / split);
+
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::stages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int a = 0; a < S::bufs; ++a) {
+      mbar_init(acc_full0 + 8 * a, 1);
+      mbar_init(acc_empty0 + 8 * a, 4);
+    }
+    for (int s = 0; s < kScaleSlots; ++s) {
+      mbar_init(sc_full0 + 8 * s, 1);
+      mbar_init(sc_empty0 + 8 * s, 4);
+    }
+    fence_barrier_init();
+    tma_prefetch_map(&map_x);
+    tma_prefetch_map(&map_w);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_slot), S::tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+
+  bool ok = true;
+  uint64_t acc[NT / 2];
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t g = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
+        const uint32_t s = g % S::stages;
+        if (!mbar_wait(empty0 + 8 * s, ((g / S::stages) & 1u) ^ 1u, p.timeout_ns, p.status)) break;
+        mbar_arrive_expect_tx(full0 + 8 * s, S::a_bytes + S::b_bytes);
+        tma_load_2d(a_base + s * S::a_bytes, &map_w, kb * kBlock, (int)n0, full0 + 8 * s);
+        tma_load_2d(b_base + s * S::b_bytes, &map_x, kb * kBlock, (int)m0, full0 + 8 * s);
+      }
+      for (uint32_t j = (g > (uint32_t)S::stages ? g - S::stages : 0u); j < g; ++j)  // landed before anything else lies there
+        mbar_wait(full0 + 8 * (j % S::stages), (j / S::stages) & 1u, p.timeout_ns, p.status);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t IDESC = umma_idesc_e4m3_f32(128, NT);
+      uint32_t g = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
+        const uint32_t s = g % S::stages, b = g % S::bufs;
+        if (!mbar_wait(full0 + 8 * s, (g / S::stages) & 1u, p.timeout_ns, p.status) ||
+            !mbar_wait(acc_empty0 + 8 * b, ((g / S::bufs) & 1u) ^ 1u, p.timeout_ns, p.status))
+          break;
+        tc_fence_after();
+        const uint32_t a = a_base + s * S::a_bytes, x = b_base + s * S::b_bytes;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          umma_e4m3(tmem + b * NT, sw128_kmajor_desc(a + k * 32), sw128_kmajor_desc(x + k * 32), IDESC, k != 0);
+        umma_commit(empty0 + 8 * s);
+        umma_commit(acc_full0 + 8 * b);
+      }
+    }
+  } else if (warp == 2) {
+    fill_scales<NT>(scales, sc_full0, sc_empty0, p.xs, m0, p.M, kb0, kb1, p.KB, 0u, lane, p);
+  } else if (warp >= 4) {
+    const int quarter = warp & 3;
+    const int64_t n = n0 + quarter * 32 + lane;
+    const float* wrow = n < p.N ? p.ws + (p.tile_scales ? n / kBlock : n) * p.KB : nullptr;
+    Scale4 next;
+    next.load(wrow, kb0, kb1);
+#pragma unroll
+    for (int i = 0; i < NT / 2; ++i) acc[i] = 0ull;
+    uint32_t g = 0;
+    for (int kb4 = kb0; ok && kb4 < kb1; kb4 += 4) {
+      const Scale4 sc = next;
+      next.load(wrow, kb4 + 4, kb1);
+#pragma unroll 1
+      for (int j = 0; j < 4 && kb4 + j < kb1; ++j, ++g) {
+        const uint32_t b = g % S::bufs, slot = g % kScaleSlots;
+        const float sr = sc.at(j);
+        const uint64_t s2 = pk(sr, sr);
+        if (!mbar_wait(sc_full0 + 8 * slot, (g / kScaleSlots) & 1u, p.timeout_ns, p.status) ||
+            !mbar_wait(acc_full0 + 8 * b, (g / S::bufs) & 1u, p.timeout_ns, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float4* cs = reinterpret_cast<const float4*>(scales + slot * NT);
+        const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + b * NT;
+        constexpr int W = NT >= 32 ? 32 : 16;  // columns a load
+#pragma unroll
+        for (int c = 0; c < NT; c += W) {
+          uint32_t r[W];
+          if constexpr (W == 32) tmem_ld32(src + c, r);
+          else tmem_ld16(src + c, r);
+          tmem_ld_wait(r);
+          if (c + W == NT) {  // all read: the accumulator is free
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty0 + 8 * b);
+          }
+#pragma unroll
+          for (int i = 0; i < W / 2; i += 2) {
+            const float4 q = cs[(c + 2 * i) / 4];
+            const int a = c / 2 + i;
+            acc[a] = fma_x2(mul_x2(pk_bits(r[2 * i], r[2 * i + 1]), pk(q.x, q.y)), s2, acc[a]);
+            acc[a + 1] = fma_x2(mul_x2(pk_bits(r[2 * i + 2], r[2 * i + 3]), pk(q.z, q.w)), s2, acc[a + 1]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sc_empty0 + 8 * slot);
+      }
+    }
+    if (split == 1) {
+      if (ok && n < p.N) {
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i) {
+          const float2 f = unpk(acc[i]);
+          if (m0 + 2 * i < p.M) store_out(p, m0 + 2 * i, n, f.x);
+          if (m0 + 2 * i + 1 < p.M) store_out(p, m0 + 2 * i + 1, n, f.y);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::tmem_cols);
+  }
+  if (split > 1) {
+    // every copy has landed and every MMA has read: the ring now holds this CTA's sums [NT][128]
+    float* sums = reinterpret_cast<float*>(smem);
+    const int r = (int)threadIdx.x - 128;
+    if (warp >= 4) {
+#pragma unroll
+      for (int i = 0; i < NT / 2; ++i) {
+        const float2 f = unpk(acc[i]);
+        sums[(2 * i) * 128 + r] = f.x;
+        sums[(2 * i + 1) * 128 + r] = f.y;
+      }
+    }
+    cluster_sync();
+    const int64_t n = n0 + (threadIdx.x & 127);
+    const uint32_t mine = smem_addr(sums) + (threadIdx.x & 127) * 4;
+    for (int c = rank + split * (int)(threadIdx.x >> 7); c < NT && m0 + c < p.M; c += 2 * split) {
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < split) {
+          const uint32_t a = map_to_cta(mine + c * 512, q);
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[q]) : "r"(a) : "memory");
+        }
+      float s = v[0];
+#pragma unroll
+      for (int q = 1; q < 8; ++q)
+        if (q < split) s = __fadd_rn(s, v[q]);
+      if (n < p.N) store_out(p, m0 + c, n, s);
+    }
+    cluster_sync();  // no CTA leaves while another still reads its sums
+  }
+}
+
 int validate_gemm8(const Gemm8Params& p, int64_t m, int64_t n, int64_t k, int wt_block) {
   if ((p.out_dtype != FAR_F32 && p.out_dtype != FAR_F16 && p.out_dtype != FAR_BF16) ||
       (wt_block != FAR_BLOCK_ROW && wt_block != FAR_BLOCK_TILE))
@@ -115,6 +667,115 @@ int validate_gemm8(const Gemm8Params& p, int64_t m, int64_t n, int64_t k, int wt
       if (regions_overlap(O, r)) return FAR_ERR_ALIAS;
   }
   return FAR_OK;
+}
+
+// a [rows, K] matrix of codes read in boxes of box_rows x 128, 128-byte swizzled; elements out of
+// range read as zero
+int encode_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t ld, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  const int st = get_encoder(&enc);
+  if (st != FAR_OK) return st;
+  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld};
+  cuuint32_t box[2] = {(cuuint32_t)kBlock, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FAR_OK : FAR_ERR_CUDA;
+}
+
+struct Gemm8Plan {
+  int kind;   // 0 plain, 1 pairs, 2 small
+  int nt;     // small: rows of x a CTA
+  int split;  // small: CTAs that share a tile's k
+};
+
+Gemm8Plan plan_gemm8(const Gemm8Params& p, int sms) {
+  Gemm8Plan g{0, 0, 0};
+  const bool tma = p.K > 0 && p.ldx % 16 == 0 && p.ldw % 16 == 0 && (((uintptr_t)p.x | (uintptr_t)p.wt) & 15) == 0;
+  if (!tma) return g;
+  const int64_t tiles_n = ((int64_t)p.N + 127) / 128;
+  g.nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  const int64_t tiles_m = ((int64_t)p.M + g.nt - 1) / g.nt;
+  const int64_t slots = (int64_t)sms * (g.nt <= 64 ? 2 : 1);
+  g.split = 1;
+  while (g.split < 8 && tiles_n * tiles_m * g.split * 2 <= slots && p.KB >= 4 * g.split) g.split *= 2;
+  const int64_t pair_tiles = (((int64_t)p.M + 255) / 256) * (((int64_t)p.N + 255) / 256);
+  // estimated time, in cycles: a block of k takes the pair kernel 540, the small kernel about
+  // 2.8 a column and no less than its 16 KB of wt take to arrive
+  const int64_t waves = (tiles_n * tiles_m * g.split + slots - 1) / slots;
+  const double small = (double)waves * ((p.KB + g.split - 1) / g.split) * (g.nt == 128 ? 360.0 : 700.0) + 1000.0;
+  const double pair = (double)((pair_tiles + sms / 2 - 1) / (sms / 2)) * p.KB * 540.0 + 3000.0;
+  const bool fits = tiles_n <= 65535 && tiles_m <= 65535;
+  g.kind = fits && (p.M <= 64 || small <= pair) ? 2 : 1;
+  if (g.kind == 1 && pair_tiles > INT32_MAX) g.kind = 0;
+  return g;
+}
+
+template <int NT>
+cudaError_t launch_small(const CUtensorMap& mx, const CUtensorMap& mw, const Gemm8Params& p, int split, cudaStream_t s) {
+  const void* f = reinterpret_cast<const void*>(small_kernel<NT>);
+  cudaError_t e = ensure_smem_attribute(f, SmallShape<NT>::smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)split, (unsigned)((p.N + 127ll) / 128), (unsigned)(((int64_t)p.M + NT - 1) / NT));
+  cfg.blockDim = dim3(kSmallThreads);
+  cfg.dynamicSmemBytes = SmallShape<NT>::smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = far_get_programmatic_launch() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, small_kernel<NT>, mx, mw, p);
+}
+
+template <bool COLS>
+cudaError_t launch_pair(const CUtensorMap& mx, const CUtensorMap& mw, const Gemm8Params& p, int sms, cudaStream_t s) {
+  cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(pair_kernel<COLS>), kPairSmem);
+  if (e != cudaSuccess) return e;
+  const int pairs = p.num_tiles < sms / 2 ? p.num_tiles : sms / 2;
+  return launch_k(pair_kernel<COLS>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, s, mx, mw, p);
+}
+
+int run_gemm8(Gemm8Params& p, void* stream) {
+  unsigned int* status = nullptr;
+  int sms = 0;
+  int st = device_info(&status, &sms);
+  if (st != FAR_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  p.status = status;
+  p.timeout_ns = kWaitTimeoutNs;
+  const int64_t so = p.out_dtype == FAR_F32 ? 4 : 2;
+  const uint64_t bits = (uint64_t)(uintptr_t)p.out | (uint64_t)(p.ldo * so);
+  p.out_align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
+  const Gemm8Plan g = plan_gemm8(p, sms);
+  cudaError_t e;
+  if (g.kind == 0) {
+    const int64_t tiles = (((int64_t)p.M + 63) / 64) * (((int64_t)p.N + 63) / 64), cap = (int64_t)sms * 8;
+    e = launch_k(plain_kernel, dim3((unsigned)(tiles < cap ? tiles : cap)), dim3(256), 0, s, p);
+  } else {
+    CUtensorMap mx, mw;
+    st = encode_codes(&mx, p.x, p.M, p.K, p.ldx, g.kind == 1 ? 128 : g.nt);
+    if (st == FAR_OK) st = encode_codes(&mw, p.wt, p.N, p.K, p.ldw, 128);
+    if (st != FAR_OK) return st;
+    if (g.kind == 1) {
+      p.tiles_m = (int32_t)(((int64_t)p.M + 255) / 256);
+      p.tiles_n = (int32_t)(((int64_t)p.N + 255) / 256);
+      p.num_tiles = p.tiles_m * p.tiles_n;
+      e = p.tile_scales ? launch_pair<false>(mx, mw, p, sms, s) : launch_pair<true>(mx, mw, p, sms, s);
+    } else {
+      e = g.nt == 16   ? launch_small<16>(mx, mw, p, g.split, s)
+          : g.nt == 32 ? launch_small<32>(mx, mw, p, g.split, s)
+          : g.nt == 64 ? launch_small<64>(mx, mw, p, g.split, s)
+                       : launch_small<128>(mx, mw, p, g.split, s);
+    }
+  }
+  return e == cudaSuccess ? FAR_OK : cuda_error_status(e);
 }
 
 }  // namespace
@@ -143,13 +804,5 @@ extern "C" int gemm_fp8_block(const void* x, int64_t x_row_stride, const float* 
   p.N = (int32_t)n;
   p.K = (int32_t)k;
   p.KB = (int32_t)((k + kBlock - 1) / kBlock);
-  unsigned int* status = nullptr;
-  int sms = 0;
-  st = device_info(&status, &sms);
-  if (st != FAR_OK) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int64_t tiles = ((m + 63) / 64) * ((n + 63) / 64);
-  const int64_t cap = (int64_t)sms * 8;
-  const cudaError_t e = launch_k(plain_kernel, dim3((unsigned)(tiles < cap ? tiles : cap)), dim3(256), 0, s, p);
-  return e == cudaSuccess ? FAR_OK : cuda_error_status(e);
+  return run_gemm8(p, stream);
 }

@@ -323,7 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         for (int kb = 0; kb < p.KB; ++kb, ++g) {
           const uint32_t s = g % kPairStages, acc = g & 1u;
           if (!mbar_wait(full0 + 8 * s, (g / kPairStages) & 1u, p.timeout_ns, p.status) ||
-              !mbar_wait_cluster(acc_empty0 + 8 * acc, ((g >> 1) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+              !mbar_wait(acc_empty0 + 8 * acc, ((g >> 1) & 1u) ^ 1u, p.timeout_ns, p.status)) {
             ok = false;
             break;
           }
@@ -358,9 +358,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       Scale4 xn, wn;
       xn.load(xrow, 0, p.KB);
       if constexpr (!COLS) wn.load(wrow, 0, p.KB);
-      uint64_t acc[64];
+      float acc[128];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
       for (int kb4 = 0; ok && kb4 < p.KB; kb4 += 4) {
         Scale4 sc;
 #pragma unroll
@@ -371,7 +371,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         for (int j = 0; j < 4 && kb4 + j < p.KB; ++j, ++g) {
           const uint32_t buf = g & 1u, slot = g % kScaleSlots;
           const float sr = sc.at(j);
-          const uint64_t s2 = pk(sr, sr);
           if (!mbar_wait(acc_full0 + 8 * buf, (g >> 1) & 1u, p.timeout_ns, p.status) ||
               (COLS && !mbar_wait(sc_full0 + 8 * slot, (g / kScaleSlots) & 1u, p.timeout_ns, p.status))) {
             ok = false;
@@ -379,37 +378,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
           tc_fence_after();
           const float4* cs = reinterpret_cast<const float4*>(scales + slot * 256 + half * 128);
-          // 16 columns at a time, the next 16 on their way while these are added
-          uint32_t r[2][16];
-          if (mine > 0) {
-            tmem_ld16(lanes + buf * 256, r[0]);
-            tmem_ld_wait(r[0]);
-          }
+          // 32 columns at a time, the next 32 on their way while these are added.  (All 128
+          // columns always: those past a narrow tile's hold what nobody stores.)
+          uint32_t r[2][32];
+          tmem_ld32(lanes + buf * 256, r[0]);
+          tmem_ld_wait(r[0]);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const bool more = c < 7 && mine > 16 * (c + 1);
-            if (more) tmem_ld16(lanes + buf * 256 + 16 * (c + 1), r[(c + 1) & 1]);
-            if (!more && (mine > 16 * c || c == 0)) {
-              // this warp's last columns have been read: its share of the buffer is free
+          for (int c = 0; c < 4; ++c) {
+            if (c < 3) tmem_ld32(lanes + buf * 256 + 32 * (c + 1), r[(c + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              float4 q;
+              if constexpr (COLS) q = cs[8 * c + i / 4];
+              const uint32_t* v = &r[c & 1][i];
+              float* a = &acc[32 * c + i];
+              a[0] = __fmaf_rn(COLS ? __fmul_rn(__uint_as_float(v[0]), q.x) : __uint_as_float(v[0]), sr, a[0]);
+              a[1] = __fmaf_rn(COLS ? __fmul_rn(__uint_as_float(v[1]), q.y) : __uint_as_float(v[1]), sr, a[1]);
+              a[2] = __fmaf_rn(COLS ? __fmul_rn(__uint_as_float(v[2]), q.z) : __uint_as_float(v[2]), sr, a[2]);
+              a[3] = __fmaf_rn(COLS ? __fmul_rn(__uint_as_float(v[3]), q.w) : __uint_as_float(v[3]), sr, a[3]);
+            }
+            if (c < 3) tmem_ld_wait(r[(c + 1) & 1]);
+            if (c == 2) {
+              // the last columns have been read: this warp's share of the buffer is free
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(map_to_cta(acc_empty0 + 8 * buf, 0));
+              if (lane == 0) mbar_arrive_remote(map_to_cta(acc_empty0 + 8 * buf, 0));
             }
-            if (mine > 16 * c) {
-#pragma unroll
-              for (int i = 0; i < 8; i += 2) {
-                uint64_t v0 = pk_bits(r[c & 1][2 * i], r[c & 1][2 * i + 1]);
-                uint64_t v1 = pk_bits(r[c & 1][2 * i + 2], r[c & 1][2 * i + 3]);
-                if constexpr (COLS) {
-                  const float4 q = cs[4 * c + i / 2];
-                  v0 = mul_x2(v0, pk(q.x, q.y));
-                  v1 = mul_x2(v1, pk(q.z, q.w));
-                }
-                acc[8 * c + i] = fma_x2(v0, s2, acc[8 * c + i]);
-                acc[8 * c + i + 1] = fma_x2(v1, s2, acc[8 * c + i + 1]);
-              }
-            }
-            if (more) tmem_ld_wait(r[(c + 1) & 1]);
           }
           if constexpr (COLS) {
             __syncwarp();
@@ -419,18 +413,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       if (!ok) break;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (mine > 32 * c) {
-          float v[32];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 f = unpk(acc[16 * c + i]);
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-          }
-          store_row32(p, row, col + 32 * c, v);
-        }
-      }
+      for (int c = 0; c < 4; ++c)
+        if (mine > 32 * c) store_row32(p, row, col + 32 * c, acc + 32 * c);
     }
   }
   __syncwarp();

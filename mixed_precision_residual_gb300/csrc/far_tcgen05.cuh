@@ -175,6 +175,13 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// The same without ordering this thread's other memory accesses for the cluster (release at
+// CTA scope): enough where the barrier only says that TMEM has been read, which
+// tcgen05.wait and tcgen05.fence order by themselves.  A cluster-scope release waits for the
+// thread's outstanding memory accesses first (a membar, a microsecond under load).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // a bounded wait on a local mbarrier whose arrivals come from other CTAs of the cluster
 // (acquire at cluster scope); FAR_ERR_TIMEOUT in the error word when it runs out
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint64_t timeout_ns,

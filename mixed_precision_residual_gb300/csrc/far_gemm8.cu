@@ -41,6 +41,7 @@ struct Gemm8Params {
   int32_t tile_scales;    // ws: one a 128 rows of wt (1) or one a row (0)
   int32_t out_dtype;
   int32_t out_align;      // bytes that out and its row stride are multiples of: 32, 16 or less
+  int32_t xs_vec, ws_vec; // rows of scales start on 16-byte boundaries
   int32_t tiles_m, tiles_n, num_tiles;  // pair_kernel
   unsigned int* status;
   uint64_t timeout_ns;
@@ -128,9 +129,22 @@ __device__ __forceinline__ uint64_t pk_bits(uint32_t lo, uint32_t hi) {
 // without a row): consecutive in memory, one sector or two.
 struct Scale4 {
   float v[4];
-  __device__ __forceinline__ void load(const float* row, int kb, int KB) {
+  // (volatile: the compiler would otherwise move the loads down to their use, four blocks of k
+  // later, and their latency with them)
+  __device__ __forceinline__ void load(const float* row, int kb, int KB, bool vec) {
+    if (row == nullptr || kb >= KB) {
+      v[0] = v[1] = v[2] = v[3] = 0.f;
+    } else if (vec) {
+      asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                   : "l"(row + kb));
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = row != nullptr && kb + j < KB ? __ldg(row + kb + j) : 0.f;
+      for (int j = 0; j < 4; ++j) {
+        v[j] = 0.f;
+        if (kb + j < KB) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v[j]) : "l"(row + kb + j));
+      }
+    }
   }
   __device__ __forceinline__ float at(int j) const {
     return j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3];
@@ -221,11 +235,12 @@ __device__ __forceinline__ void store_row32(const Gemm8Params& p, int64_t row, i
 // The last column of tiles runs at the width that is left (a multiple of 32).
 // ---------------------------------------------------------------------------
 constexpr int kPairThreads = 384;
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 5;
 constexpr uint32_t kPairABytes = 128 * kBlock, kPairBBytes = 128 * kBlock;
 constexpr uint32_t kPairRing = kPairStages * (kPairABytes + kPairBBytes);
 constexpr int kPairBars = 2 * kPairStages + 4 + 2 * kScaleSlots;
-constexpr size_t kPairSmem = kPairRing + kScaleSlots * 256 * 4 + kPairBars * 8 + 16 + 1024;
+constexpr uint32_t kPairOut = 8 * 4096;  // a box of 32 rows x 128 bytes of outputs an epilogue warp
+constexpr size_t kPairSmem = kPairRing + kPairOut + kScaleSlots * 256 * 4 + kPairBars * 8 + 16 + 1024;
 constexpr int kPairGroup = 8;  // tile rows that are walked together, so that CTAs at work share panels in L2
 
 struct PairTile {
@@ -245,14 +260,15 @@ __device__ __forceinline__ PairTile pair_tile(const Gemm8Params& p, int t) {
 
 template <bool COLS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const Gemm8Params p) {
+    pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                const __grid_constant__ CUtensorMap map_out, const Gemm8Params p) {
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   unsigned char* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);  // the same offset in both CTAs
   const uint32_t sbase = smem_addr(smem);
   const uint32_t a_base = sbase, b_base = sbase + kPairStages * kPairABytes;
-  float* scales = reinterpret_cast<float*>(smem + kPairRing);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kPairRing + kScaleSlots * 256 * 4);
+  float* scales = reinterpret_cast<float*>(smem + kPairRing + kPairOut);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kPairRing + kPairOut + kScaleSlots * 256 * 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kPairBars);
   const uint32_t full0 = smem_addr(&bars[0]), empty0 = smem_addr(&bars[kPairStages]);
   const uint32_t acc_full0 = smem_addr(&bars[2 * kPairStages]), acc_empty0 = acc_full0 + 16;
@@ -316,24 +332,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           mbar_wait(full0 + 8 * (j % kPairStages), (j / kPairStages) & 1u, p.timeout_ns, p.status);
     } else if (warp == 1 && lane == 0 && rank == 0) {
       // ---------------- MMA issuer (even CTA) ----------------
-      uint32_t g = 0;
+      // One thread issues everything, so what it does for a block of k is kept short: ring
+      // positions by counters, descriptors by adding to those of the first slot (16-byte units)
+      const uint64_t a0 = sw128_kmajor_desc(a_base), b0 = sw128_kmajor_desc(b_base);
+      uint32_t s = 0, s_phase = 0, acc = 0, acc_phase = 1;
       bool ok = true;
       for (int t = pair; ok && t < p.num_tiles; t += pairs) {
         const uint32_t idesc = umma_idesc_e4m3_f32(256, pair_tile(p, t).cols);
-        for (int kb = 0; kb < p.KB; ++kb, ++g) {
-          const uint32_t s = g % kPairStages, acc = g & 1u;
-          if (!mbar_wait(full0 + 8 * s, (g / kPairStages) & 1u, p.timeout_ns, p.status) ||
-              !mbar_wait(acc_empty0 + 8 * acc, ((g >> 1) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+        for (int kb = 0; kb < p.KB; ++kb) {
+          if (!mbar_wait(acc_empty0 + 8 * acc, acc_phase, p.timeout_ns, p.status) ||
+              !mbar_wait(full0 + 8 * s, s_phase, p.timeout_ns, p.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a = a_base + s * kPairABytes, b = b_base + s * kPairBBytes;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_e4m3_pair(tmem + acc * 256, sw128_kmajor_desc(a + k * 32), sw128_kmajor_desc(b + k * 32), idesc, k != 0);
-          umma_commit_pair(empty0 + 8 * s, 0x3);       // both CTAs' slots are free once read
+          const uint64_t a = a0 + s * (kPairABytes >> 4), b = b0 + s * (kPairBBytes >> 4);
+          const uint32_t d = tmem + acc * 256;
+          umma_e4m3_pair<false>(d, a, b, idesc);
+          umma_e4m3_pair<true>(d, a + 2, b + 2, idesc);
+          umma_e4m3_pair<true>(d, a + 4, b + 4, idesc);
+          umma_e4m3_pair<true>(d, a + 6, b + 6, idesc);
           umma_commit_pair(acc_full0 + 8 * acc, 0x3);  // the block's sums are there
+          umma_commit_pair(empty0 + 8 * s, 0x3);       // both CTAs' slots are free once read
+          acc ^= 1;
+          acc_phase ^= acc == 0;
+          if (++s == kPairStages) {
+            s = 0;
+            s_phase ^= 1;
+          }
         }
       }
     } else if (COLS && warp == 2) {
@@ -346,6 +372,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * 128);
+    const uint32_t acc_empty_even = map_to_cta(acc_empty0, 0);
+    unsigned char* box = smem + kPairRing + (warp - 4) * 4096;
     uint32_t g = 0;
     bool ok = true;
     for (int t = pair; ok && t < p.num_tiles; t += pairs) {
@@ -356,8 +384,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const float* xrow = row < p.M ? p.xs + row * p.KB : nullptr;
       const float* wrow = !COLS && col < p.N ? p.ws + col / kBlock * p.KB : nullptr;
       Scale4 xn, wn;
-      xn.load(xrow, 0, p.KB);
-      if constexpr (!COLS) wn.load(wrow, 0, p.KB);
+      xn.load(xrow, 0, p.KB, p.xs_vec);
+      if constexpr (!COLS) wn.load(wrow, 0, p.KB, p.ws_vec);
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
@@ -365,8 +393,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         Scale4 sc;
 #pragma unroll
         for (int j = 0; j < 4; ++j) sc.v[j] = COLS ? xn.v[j] : __fmul_rn(xn.v[j], wn.v[j]);
-        xn.load(xrow, kb4 + 4, p.KB);  // the next four blocks', while these are worked on
-        if constexpr (!COLS) wn.load(wrow, kb4 + 4, p.KB);
+        xn.load(xrow, kb4 + 4, p.KB, p.xs_vec);  // the next four blocks', while these are worked on
+        if constexpr (!COLS) wn.load(wrow, kb4 + 4, p.KB, p.ws_vec);
 #pragma unroll 1
         for (int j = 0; j < 4 && kb4 + j < p.KB; ++j, ++g) {
           const uint32_t buf = g & 1u, slot = g % kScaleSlots;
@@ -378,31 +406,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
           tc_fence_after();
           const float4* cs = reinterpret_cast<const float4*>(scales + slot * 256 + half * 128);
-          // 32 columns at a time, the next 32 on their way while these are added.  (All 128
-          // columns always: those past a narrow tile's hold what nobody stores.)
-          uint32_t r[2][32];
-          tmem_ld32(lanes + buf * 256, r[0]);
-          tmem_ld_wait(r[0]);
+          // All 128 columns always: those past a narrow tile's hold what nobody stores.  (The
+          // other warp of this SM quarter adds while this one loads.)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            if (c < 3) tmem_ld32(lanes + buf * 256 + 32 * (c + 1), r[(c + 1) & 1]);
+            uint32_t r[32];
+            tmem_ld32_sync(lanes + buf * 256 + 32 * c, r);
+            if (c == 3) {  // all read: this warp's share of the buffer is free
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
+            }
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
               float4 q;
               if constexpr (COLS) q = cs[8 * c + i / 4];
-              const uint32_t* v = &r[c & 1][i];
+              else q = make_float4(1.f, 1.f, 1.f, 1.f);
               float* a = &acc[32 * c + i];
-              a[0] = __fmaf_rn(COLS ? __fmul_rn(__uint_as_float(v[0]), q.x) : __uint_as_float(v[0]), sr, a[0]);
-              a[1] = __fmaf_rn(COLS ? __fmul_rn(__uint_as_float(v[1]), q.y) : __uint_as_float(v[1]), sr, a[1]);
-              a[2] = __fmaf_rn(COLS ? __fmul_rn(__uint_as_float(v[2]), q.z) : __uint_as_float(v[2]), sr, a[2]);
-              a[3] = __fmaf_rn(COLS ? __fmul_rn(__uint_as_float(v[3]), q.w) : __uint_as_float(v[3]), sr, a[3]);
-            }
-            if (c < 3) tmem_ld_wait(r[(c + 1) & 1]);
-            if (c == 2) {
-              // the last columns have been read: this warp's share of the buffer is free
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_remote(map_to_cta(acc_empty0 + 8 * buf, 0));
+              const float v0 = __uint_as_float(r[i]), v1 = __uint_as_float(r[i + 1]), v2 = __uint_as_float(r[i + 2]),
+                          v3 = __uint_as_float(r[i + 3]);
+              a[0] = __fmaf_rn(COLS ? __fmul_rn(v0, q.x) : v0, sr, a[0]);
+              a[1] = __fmaf_rn(COLS ? __fmul_rn(v1, q.y) : v1, sr, a[1]);
+              a[2] = __fmaf_rn(COLS ? __fmul_rn(v2, q.z) : v2, sr, a[2]);
+              a[3] = __fmaf_rn(COLS ? __fmul_rn(v3, q.w) : v3, sr, a[3]);
             }
           }
           if constexpr (COLS) {
@@ -412,10 +438,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       }
       if (!ok) break;
+      if (p.out_align >= 16) {
+        // through shared memory in boxes of 32 rows x 128 bytes (128-byte swizzle), copied out by TMA
+        // while the next tile's blocks arrive; the copy leaves out what lies past the edges
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (mine > 32 * c) store_row32(p, row, col + 32 * c, acc + 32 * c);
+        for (int c = 0; c < 4; ++c) {
+          if (mine <= 32 * c) break;
+          const bool f32 = p.out_dtype == FAR_F32;
+          if (f32 || (c & 1) == 0) {  // a new box: the copy of the last one has read it
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+          }
+          uint32_t v[32];
+          if (f32) narrow<FAR_F32, 32>(acc + 32 * c, v);
+          else if (p.out_dtype == FAR_F16) narrow<FAR_F16, 32>(acc + 32 * c, v);
+          else narrow<FAR_BF16, 32>(acc + 32 * c, v);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            if (u < 4 || f32) {
+              const int unit = (f32 || (c & 1) == 0 ? u : u + 4) ^ (lane & 7);
+              *reinterpret_cast<uint4*>(box + lane * 128 + unit * 16) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+            }
+          }
+          if (f32 || (c & 1) == 1 || mine <= 32 * (c + 1)) {
+            fence_async_shared();
+            __syncwarp();
+            const int64_t x = col + (f32 ? 32 * c : 64 * (c / 2)), y = row - lane;
+            if (lane == 0 && x < p.N && y < p.M) {
+              tma_store_2d(&map_out, smem_addr(box), (int)x, (int)y);
+              bulk_commit();
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (mine > 32 * c) store_row32(p, row, col + 32 * c, acc + 32 * c);
+      }
     }
+    if (lane == 0) bulk_wait_all();
   }
   __syncwarp();
   tc_fence_before();
@@ -514,6 +575,7 @@ __global__ void __launch_bounds__(kSmallThreads, SmallShape<NT>::ctas)
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t IDESC = umma_idesc_e4m3_f32(128, NT);
+      const uint64_t a0 = sw128_kmajor_desc(a_base), x0 = sw128_kmajor_desc(b_base);
       uint32_t g = 0;
       for (int kb = kb0; kb < kb1; ++kb, ++g) {
         const uint32_t s = g % S::stages, b = g % S::bufs;
@@ -521,10 +583,11 @@ __global__ void __launch_bounds__(kSmallThreads, SmallShape<NT>::ctas)
             !mbar_wait(acc_empty0 + 8 * b, ((g / S::bufs) & 1u) ^ 1u, p.timeout_ns, p.status))
           break;
         tc_fence_after();
-        const uint32_t a = a_base + s * S::a_bytes, x = b_base + s * S::b_bytes;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          umma_e4m3(tmem + b * NT, sw128_kmajor_desc(a + k * 32), sw128_kmajor_desc(x + k * 32), IDESC, k != 0);
+        const uint64_t a = a0 + s * (S::a_bytes >> 4), x = x0 + s * (S::b_bytes >> 4);
+        umma_e4m3<false>(tmem + b * NT, a, x, IDESC);
+        umma_e4m3<true>(tmem + b * NT, a + 2, x + 2, IDESC);
+        umma_e4m3<true>(tmem + b * NT, a + 4, x + 4, IDESC);
+        umma_e4m3<true>(tmem + b * NT, a + 6, x + 6, IDESC);
         umma_commit(empty0 + 8 * s);
         umma_commit(acc_full0 + 8 * b);
       }
@@ -536,13 +599,13 @@ __global__ void __launch_bounds__(kSmallThreads, SmallShape<NT>::ctas)
     const int64_t n = n0 + quarter * 32 + lane;
     const float* wrow = n < p.N ? p.ws + (p.tile_scales ? n / kBlock : n) * p.KB : nullptr;
     Scale4 next;
-    next.load(wrow, kb0, kb1);
+    next.load(wrow, kb0, kb1, p.ws_vec && kb0 % 4 == 0);
 #pragma unroll
     for (int i = 0; i < NT / 2; ++i) acc[i] = 0ull;
     uint32_t g = 0;
     for (int kb4 = kb0; ok && kb4 < kb1; kb4 += 4) {
       const Scale4 sc = next;
-      next.load(wrow, kb4 + 4, kb1);
+      next.load(wrow, kb4 + 4, kb1, p.ws_vec && kb0 % 4 == 0);
 #pragma unroll 1
       for (int j = 0; j < 4 && kb4 + j < kb1; ++j, ++g) {
         const uint32_t b = g % S::bufs, slot = g % kScaleSlots;
@@ -653,20 +716,24 @@ int validate_gemm8(const Gemm8Params& p, int64_t m, int64_t n, int64_t k, int wt
   return FAR_OK;
 }
 
-// a [rows, K] matrix of codes read in boxes of box_rows x 128, 128-byte swizzled; elements out of
-// range read as zero
-int encode_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t ld, int box_rows) {
+// a [rows, cols] matrix moved in boxes of box_rows x box_cols (128 bytes), 128-byte swizzled;
+// elements out of range read as zero and are not written
+int encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t row_bytes, int box_cols,
+               int box_rows, CUtensorMapDataType type) {
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   const int st = get_encoder(&enc);
   if (st != FAR_OK) return st;
-  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)ld};
-  cuuint32_t box[2] = {(cuuint32_t)kBlock, (cuuint32_t)box_rows};
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const CUresult r = enc(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FAR_OK : FAR_ERR_CUDA;
+}
+int encode_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t ld, int box_rows) {
+  return encode_map(map, base, rows, K, ld, kBlock, box_rows, CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 
 struct Gemm8Plan {
@@ -719,11 +786,12 @@ cudaError_t launch_small(const CUtensorMap& mx, const CUtensorMap& mw, const Gem
 }
 
 template <bool COLS>
-cudaError_t launch_pair(const CUtensorMap& mx, const CUtensorMap& mw, const Gemm8Params& p, int sms, cudaStream_t s) {
+cudaError_t launch_pair(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& mo, const Gemm8Params& p, int sms,
+                        cudaStream_t s) {
   cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(pair_kernel<COLS>), kPairSmem);
   if (e != cudaSuccess) return e;
   const int pairs = p.num_tiles < sms / 2 ? p.num_tiles : sms / 2;
-  return launch_k(pair_kernel<COLS>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, s, mx, mw, p);
+  return launch_k(pair_kernel<COLS>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, s, mx, mw, mo, p);
 }
 
 int run_gemm8(Gemm8Params& p, void* stream) {
@@ -737,6 +805,8 @@ int run_gemm8(Gemm8Params& p, void* stream) {
   const int64_t so = p.out_dtype == FAR_F32 ? 4 : 2;
   const uint64_t bits = (uint64_t)(uintptr_t)p.out | (uint64_t)(p.ldo * so);
   p.out_align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
+  p.xs_vec = p.KB % 4 == 0 && ((uintptr_t)p.xs & 15) == 0;
+  p.ws_vec = p.KB % 4 == 0 && ((uintptr_t)p.ws & 15) == 0;
   const Gemm8Plan g = plan_gemm8(p, sms);
   cudaError_t e;
   if (g.kind == 0) {
@@ -751,7 +821,16 @@ int run_gemm8(Gemm8Params& p, void* stream) {
       p.tiles_m = (int32_t)(((int64_t)p.M + 255) / 256);
       p.tiles_n = (int32_t)(((int64_t)p.N + 255) / 256);
       p.num_tiles = p.tiles_m * p.tiles_n;
-      e = p.tile_scales ? launch_pair<false>(mx, mw, p, sms, s) : launch_pair<true>(mx, mw, p, sms, s);
+      CUtensorMap mo = mx;  // (not used where out's rows are not 16-byte aligned)
+      if (p.out_align >= 16) {
+        const int dt = p.out_dtype;
+        st = encode_map(&mo, p.out, p.M, p.N, p.ldo * so, (int)(128 / so), 32,
+                        dt == FAR_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                        : dt == FAR_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+        if (st != FAR_OK) return st;
+      }
+      e = p.tile_scales ? launch_pair<false>(mx, mw, mo, p, sms, s) : launch_pair<true>(mx, mw, mo, p, sms, s);
     } else {
       e = g.nt == 16   ? launch_small<16>(mx, mw, p, g.split, s)
           : g.nt == 32 ? launch_small<32>(mx, mw, p, g.split, s)

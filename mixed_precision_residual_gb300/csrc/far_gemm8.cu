@@ -330,10 +330,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (rank == 0)  // the pair's copies of the last blocks must have landed before exit
         for (uint32_t j = (g > (uint32_t)kPairStages ? g - kPairStages : 0u); j < g; ++j)
           mbar_wait(full0 + 8 * (j % kPairStages), (j / kPairStages) & 1u, p.timeout_ns, p.status);
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
       // ---------------- MMA issuer (even CTA) ----------------
-      // One thread issues everything, so what it does for a block of k is kept short: ring
+      // One warp issues everything, so what it does for a block of k is kept short: ring
       // positions by counters, descriptors by adding to those of the first slot (16-byte units)
+      const bool leader = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint64_t a0 = sw128_kmajor_desc(a_base), b0 = sw128_kmajor_desc(b_base);
       uint32_t s = 0, s_phase = 0, acc = 0, acc_phase = 1;
       bool ok = true;
@@ -347,13 +349,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
           tc_fence_after();
           const uint64_t a = a0 + s * (kPairABytes >> 4), b = b0 + s * (kPairBBytes >> 4);
-          const uint32_t d = tmem + acc * 256;
-          umma_e4m3_pair<false>(d, a, b, idesc);
-          umma_e4m3_pair<true>(d, a + 2, b + 2, idesc);
-          umma_e4m3_pair<true>(d, a + 4, b + 4, idesc);
-          umma_e4m3_pair<true>(d, a + 6, b + 6, idesc);
-          umma_commit_pair(acc_full0 + 8 * acc, 0x3);  // the block's sums are there
-          umma_commit_pair(empty0 + 8 * s, 0x3);       // both CTAs' slots are free once read
+          const uint32_t d = tm + acc * 256;
+          if (leader) {
+            umma_e4m3_pair<false>(d, a, b, idesc);
+            umma_e4m3_pair<true>(d, a + 2, b + 2, idesc);
+            umma_e4m3_pair<true>(d, a + 4, b + 4, idesc);
+            umma_e4m3_pair<true>(d, a + 6, b + 6, idesc);
+            umma_commit_pair(acc_full0 + 8 * acc, 0x3);  // the block's sums are there
+            umma_commit_pair(empty0 + 8 * s, 0x3);       // both CTAs' slots are free once read
+          }
+          __syncwarp();
           acc ^= 1;
           acc_phase ^= acc == 0;
           if (++s == kPairStages) {
@@ -573,23 +578,34 @@ __global__ void __launch_bounds__(kSmallThreads, SmallShape<NT>::ctas)
         mbar_wait(full0 + 8 * (j % S::stages), (j / S::stages) & 1u, p.timeout_ns, p.status);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t IDESC = umma_idesc_e4m3_f32(128, NT);
-      const uint64_t a0 = sw128_kmajor_desc(a_base), x0 = sw128_kmajor_desc(b_base);
-      uint32_t g = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++g) {
-        const uint32_t s = g % S::stages, b = g % S::bufs;
-        if (!mbar_wait(full0 + 8 * s, (g / S::stages) & 1u, p.timeout_ns, p.status) ||
-            !mbar_wait(acc_empty0 + 8 * b, ((g / S::bufs) & 1u) ^ 1u, p.timeout_ns, p.status))
-          break;
-        tc_fence_after();
-        const uint64_t a = a0 + s * (S::a_bytes >> 4), x = x0 + s * (S::b_bytes >> 4);
-        umma_e4m3<false>(tmem + b * NT, a, x, IDESC);
-        umma_e4m3<true>(tmem + b * NT, a + 2, x + 2, IDESC);
-        umma_e4m3<true>(tmem + b * NT, a + 4, x + 4, IDESC);
-        umma_e4m3<true>(tmem + b * NT, a + 6, x + 6, IDESC);
-        umma_commit(empty0 + 8 * s);
+    constexpr uint32_t IDESC = umma_idesc_e4m3_f32(128, NT);
+    const bool leader = elect_one();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t a0 = sw128_kmajor_desc(a_base), x0 = sw128_kmajor_desc(b_base);
+    uint32_t s = 0, s_phase = 0, b = 0, b_phase = 1;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(acc_empty0 + 8 * b, b_phase, p.timeout_ns, p.status) ||
+          !mbar_wait(full0 + 8 * s, s_phase, p.timeout_ns, p.status))
+        break;
+      tc_fence_after();
+      const uint64_t a = a0 + s * (S::a_bytes >> 4), x = x0 + s * (S::b_bytes >> 4);
+      const uint32_t d = tm + b * NT;
+      if (leader) {
+        umma_e4m3<false>(d, a, x, IDESC);
+        umma_e4m3<true>(d, a + 2, x + 2, IDESC);
+        umma_e4m3<true>(d, a + 4, x + 4, IDESC);
+        umma_e4m3<true>(d, a + 6, x + 6, IDESC);
         umma_commit(acc_full0 + 8 * b);
+        umma_commit(empty0 + 8 * s);
+      }
+      __syncwarp();
+      if (++s == S::stages) {
+        s = 0;
+        s_phase ^= 1;
+      }
+      if (++b == S::bufs) {
+        b = 0;
+        b_phase ^= 1;
       }
     }
   } else if (warp == 2) {

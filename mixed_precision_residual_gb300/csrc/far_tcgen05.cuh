@@ -84,6 +84,15 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16_f32(int M, int N) {
          | ((uint32_t)(M >> 4) << 24);  // M / 16
 }
 
+// True in one lane of a converged warp.  A loop that issues MMAs runs in the whole warp, with
+// only the issuing itself under this: its descriptors then stay in the warp's uniform
+// registers, where the instructions want them, instead of being moved there each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // FP8: kind::f8f6f4, E4M3 operands (32 values of K an instruction), fp32 accumulators.  An
 // operand tile's rows of 128 bytes hold 128 values of K; the descriptors are the same.
 __host__ __device__ constexpr uint32_t umma_idesc_e4m3_f32(int M, int N) {

@@ -1,73 +1,47 @@
-"""What the bindings of the per-head and block-scaled operators share: device and stream of a call.
+"""The native binding of the per-head and block-scaled operators, and their explicit streams.
 
-A call runs on its tensors' device, whatever the current one is, and on `stream` or that
-device's current stream.  With an explicit stream that is not the current one, outputs are
-allocated on it, and the inputs (and the outputs, for the current stream) are recorded, so
-that the caching allocator hands none of that memory out again before both streams are done
-with it; ordering the two streams is the caller's part, as for any work on two streams.
+``_build/_far_torch.so`` (csrc/far_torch.cpp) checks a call's tensors, allocates its outputs and
+enqueues it on the tensors' device, whatever the current one is, and that device's current
+stream.  A call with ``stream=`` runs with that stream current: outputs are allocated on it,
+and the inputs (and the outputs, for the stream that was current) are recorded, so that the
+caching allocator hands none of that memory out again before both streams are done with it;
+ordering the two streams is the caller's part, as for any work on two streams.
 """
 from __future__ import annotations
 
+import importlib.util
+import os
+
 import torch
 
-from . import _check
+from . import FarError, _PKG
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+BINDING_PATH = os.path.join(_PKG, "_build", "_far_torch.so")
+if not os.path.exists(BINDING_PATH):
+    raise ImportError(f"{BINDING_PATH} is missing: build the CUDA library first "
+                      "(python -c 'import __graft_entry__ as g; g.build()')")
+_spec = importlib.util.spec_from_file_location("_far_torch", BINDING_PATH)
+native = importlib.util.module_from_spec(_spec)
+_spec.loader.exec_module(native)
+native.init_errors(FarError, torch.OutOfMemoryError)
 
 
-def device_of(*tensors) -> int:
-    """The one CUDA device all tensors (None: not given) are on."""
-    dev = None
+def on_stream(stream, call, *args):
+    """call(*args) on an explicit stream."""
+    tensors = [a for a in args if isinstance(a, torch.Tensor)]
     for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d < 0:
-                raise ValueError("tensors must be on a CUDA device")
-            if dev is None:
-                dev = d
-            elif d != dev:
-                raise ValueError("tensors must be on one device")
-    return dev
-
-
-class Launch:
-    """The device and stream of one call; `inputs` are what it reads."""
-
-    __slots__ = ("dev", "handle", "stream", "other")
-
-    def __init__(self, stream, *tensors):
-        self.dev = dev = device_of(*tensors)
-        current = _raw_stream(dev)
-        self.stream = stream
-        if stream is None:
-            self.handle, self.other = current, False
-            return
-        if stream.device.index != dev:
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        if t.device != stream.device:
             raise ValueError("the stream belongs to another device than the tensors")
-        self.handle = stream.cuda_stream
-        self.other = self.handle != current
-        if self.other:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-
-    def empty(self, shape, dtype):
-        """An output or workspace of this call."""
-        if not self.other:
-            return torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.dev))
-        here = torch.cuda.current_stream(self.dev)
-        with torch.cuda.stream(self.stream):
-            t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", self.dev))
-        t.record_stream(here)
-        return t
-
-    def run(self, fn, *args) -> None:
-        if self.dev == torch.cuda.current_device():
-            _check(fn(*args, self.handle))
-        else:
-            with torch.cuda.device(self.dev):
-                _check(fn(*args, self.handle))
-
-
-def ptr(t):
-    return None if t is None else t.data_ptr()
+    here = torch.cuda.current_stream(stream.device)
+    if stream == here:
+        return call(*args)
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    for t in tensors:
+        t.record_stream(stream)
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None and not any(t is a for a in tensors):
+            t.record_stream(here)
+    return out

@@ -1,7 +1,9 @@
 """Compile the CUDA library for sm_103a into an in-tree shared library.
 
 nvcc compiles each translation unit (one per activation dtype, plus the C-ABI
-unit) in parallel, then links ``_build/libfar.so``.  No GPU is needed: nvcc
+unit) in parallel, then links ``_build/libfar.so``; g++ compiles the PyTorch
+binding of the per-head and block-scaled operators beside them, linked against
+it as ``_build/_far_torch.so``.  No GPU is needed: nvcc
 cross-compiles.  ``-fmad=false`` keeps every binary32 add and multiply
 separately rounded (the kernels also use explicit rounding intrinsics); IEEE
 division and square root are nvcc's defaults and are kept (no fast-math).
@@ -11,6 +13,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libfar.so")
+BINDING = os.path.join(BUILD, "_far_torch.so")
+BINDING_SOURCE = "far_torch.cpp"
 SOURCES = ["far_api.cu", "far_inst_f16.cu", "far_inst_bf16.cu", "far_inst_f32.cu", "far_inst_q_f16.cu",
            "far_inst_q_bf16.cu", "far_inst_q_f32.cu", "far_inst_ln_f16.cu", "far_inst_ln_bf16.cu",
            "far_inst_ln_f32.cu", "far_inst_qb_f16.cu", "far_inst_qb_bf16.cu", "far_inst_qb_f32.cu", "far_noalloc.cu",
@@ -36,11 +41,29 @@ def _nvcc() -> str:
     return "nvcc"
 
 
+def _torch_flags() -> tuple[list, list]:
+    """g++'s compile and link flags for a Python module on PyTorch's C++ API."""
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    lib = os.path.join(t, "lib")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [sysconfig.get_paths()["include"], os.path.join(t, "include"),
+           os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda if os.path.isdir(os.path.join(cuda, "include")) else "/usr/local/cuda", "include"),
+           os.path.join(ROOT, "include")]
+    cc = ["-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *(f"-I{i}" for i in inc)]
+    ld = ["-shared", f"-L{lib}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}",
+          f"-L{BUILD}", "-lfar", "-Wl,-rpath,$ORIGIN"]
+    return cc, ld
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "far.h")]
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [BINDING_SOURCE]] + [os.path.join(ROOT, "include", "far.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -50,16 +73,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
 
+    cc, ld = _torch_flags()
+
     def compile_one(src):
-        obj = os.path.join(BUILD, src.replace(".cu", ".o"))
-        cmd = [nvcc, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+        obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+        if src == BINDING_SOURCE:
+            cmd = ["g++", *cc, "-c", os.path.join(CSRC, src), "-o", obj]
+        else:
+            cmd = [nvcc, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        results = list(ex.map(compile_one, SOURCES))
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        *results, (binding, _) = ex.map(compile_one, SOURCES + [BINDING_SOURCE])
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for (_, log), src in zip(results, SOURCES):
             f.write(f"==== {src}\n{log}\n")
@@ -69,6 +97,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    r = subprocess.run(["g++", binding, "-o", tmp, *ld], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
     if verbose:
         print(f"built {LIB}", file=sys.stderr)
     return LIB

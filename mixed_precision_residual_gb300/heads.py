@@ -14,14 +14,14 @@ taken as they are.  k may be None (queries alone).
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
-from . import TORCH_TO_CODE, FarError, _check, dtypes, lib
-from ._launch import Launch, ptr
+from . import FarError, _check, lib
+from ._launch import native, on_stream
 
-_vp, _f32, _i64, _int, _f64 = ctypes.c_void_p, ctypes.c_float, ctypes.c_int64, ctypes.c_int, ctypes.c_double
+_vp, _i64, _int, _f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_double
+_f32 = ctypes.c_float
 _HEADS = [_vp, _i64, _i64]
 _PLACE = [_vp, _i64, _vp, _int]  # table, rows, positions, bytes a position
 _SIZES = [_i64] * 5
@@ -39,83 +39,7 @@ lib.far_rope_frequencies.restype = _int
 lib.rope_table.argtypes = [_vp, _i64, _i64, _i64, _vp, _f64, _vp]
 lib.rope_table.restype = _int
 
-_NONE = (None, 0, 0)
 SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
-
-
-def _heads(t: torch.Tensor):
-    """(pointer, token stride, head stride) of a [..., heads, dim] tensor."""
-    if t.dim() == 3:
-        n, h, d = t.shape
-        ts, hs, ds = t.stride()
-    else:
-        if t.dim() < 3:
-            raise ValueError("q and k are [..., heads, head_dim]")
-        *lead, h, d = t.shape
-        *ls, hs, ds = t.stride()
-        n, ts = math.prod(lead), 0
-        run = None  # the stride the axes inside would need to continue
-        for size, st in zip(reversed(lead), reversed(ls)):
-            if size == 1:
-                continue
-            if run is None:
-                ts = st
-            elif st != run and n > 0:
-                raise ValueError("the leading axes do not collapse to one stride: call once a sequence, or copy")
-            run = st * size
-    if ds != 1 and d > 1:
-        raise ValueError("the values of a head must be contiguous")
-    return t.data_ptr(), (ts if n > 1 else 0), (hs if h > 1 else 0)
-
-
-def _place(table, positions, tokens, rot):
-    if table.dim() != 2 or table.dtype != torch.float32 or not table.is_contiguous():
-        raise ValueError("table must be a contiguous float32 [rows, rot_dim] tensor (rope_table)")
-    if positions.dtype not in (torch.int64, torch.int32) or not positions.is_contiguous():
-        raise ValueError("positions must be a contiguous int32 or int64 tensor")
-    if positions.numel() != tokens:
-        raise ValueError("one position for each token")
-    return table.data_ptr(), table.shape[0], positions.data_ptr(), positions.element_size()
-
-
-def _sizes(q, k):
-    """tokens, query heads, key heads, head_dim; the tensors' agreement."""
-    if q.dim() < 3:
-        raise ValueError("q and k are [..., heads, head_dim]")
-    *lead, h, d = q.shape
-    hk = 0
-    if k is not None:
-        if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != d:
-            raise ValueError("q and k must agree but in their number of heads")
-        if k.dtype != q.dtype:
-            raise ValueError("q and k must share a dtype")
-        hk = k.shape[-2]
-    n = lead[0] if len(lead) == 1 else math.prod(lead)
-    return n, h, hk, d
-
-
-def _outputs(go, q, k, q_out, k_out):
-    """The outputs given, checked, or new ones."""
-    outs = []
-    for x, y in ((q, q_out), (k, k_out)):
-        if x is None:
-            if y is not None:
-                raise ValueError("an output without its input")
-        elif y is None:
-            y = go.empty(x.shape, x.dtype)
-        elif y.shape != x.shape or y.dtype != x.dtype:
-            raise ValueError("an output has its input's shape and dtype")
-        outs.append(y)
-    return outs
-
-
-def _pair_weights(q, k, q_weight, k_weight, d):
-    for x, w in ((q, q_weight), (k, k_weight)):
-        if x is not None and (w is None or w.numel() != d or not w.is_contiguous()):
-            raise ValueError("a weight is a contiguous [head_dim] tensor")
-    if k is not None and q_weight.dtype != k_weight.dtype:
-        raise ValueError("q_weight and k_weight must share a dtype")
-    return dtypes(q.dtype, q_weight.dtype)
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor, k_weight: torch.Tensor | None,
@@ -127,39 +51,26 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor
     (2i, 2i + 1) with interleaved=True.  Outputs have the inputs' dtype; pass q_out=q,
     k_out=k to work in place.  A negative position marks a padding token (zeros out).
     """
-    n, h, hk, d = _sizes(q, k)
-    code = _pair_weights(q, k, q_weight, k_weight, d)
-    go = Launch(stream, q, k, q_weight, k_weight, table, positions, q_out, k_out)
-    yq, yk = _outputs(go, q, k, q_out, k_out)
-    go.run(lib.qk_norm_rope, *_heads(q), *(_NONE if k is None else _heads(k)), ptr(q_weight), ptr(k_weight), eps,
-           *_place(table, positions, n, d), *_heads(yq), *(_NONE if k is None else _heads(yk)), n, h, hk, d,
-           table.shape[1], int(interleaved), code)
-    return yq, yk
-
-
-def _rope(q, k, table, positions, interleaved, transpose, q_out, k_out, stream):
-    n, h, hk, d = _sizes(q, k)
-    if q.dtype not in TORCH_TO_CODE:
-        raise FarError(2)
-    go = Launch(stream, q, k, table, positions, q_out, k_out)
-    yq, yk = _outputs(go, q, k, q_out, k_out)
-    go.run(lib.rope, *_heads(q), *(_NONE if k is None else _heads(k)), *_place(table, positions, n, d), *_heads(yq),
-           *(_NONE if k is None else _heads(yk)), n, h, hk, d, table.shape[1], int(interleaved), transpose,
-           TORCH_TO_CODE[q.dtype])
-    return yq, yk
+    if stream is None:
+        return native.qk_norm_rope(q, k, q_weight, k_weight, eps, table, positions, interleaved, q_out, k_out)
+    return on_stream(stream, native.qk_norm_rope, q, k, q_weight, k_weight, eps, table, positions, interleaved, q_out, k_out)
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, table: torch.Tensor, positions: torch.Tensor,
          interleaved: bool = False, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
     """(q_out, k_out): qk_norm_rope's rotation alone."""
-    return _rope(q, k, table, positions, interleaved, 0, q_out, k_out, stream)
+    if stream is None:
+        return native.rope(q, k, table, positions, interleaved, False, q_out, k_out)
+    return on_stream(stream, native.rope, q, k, table, positions, interleaved, False, q_out, k_out)
 
 
 def rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor | None, table: torch.Tensor, positions: torch.Tensor,
                   interleaved: bool = False, dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
                   stream=None):
     """(dq, dk): rope's gradients, the transposed rotation of the outputs' gradients."""
-    return _rope(dq_out, dk_out, table, positions, interleaved, 1, dq, dk, stream)
+    if stream is None:
+        return native.rope(dq_out, dk_out, table, positions, interleaved, True, dq, dk)
+    return on_stream(stream, native.rope, dq_out, dk_out, table, positions, interleaved, True, dq, dk)
 
 
 def qk_backward_workspace_bytes(head_dim: int) -> int:
@@ -179,26 +90,8 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q: 
     tokens and heads in a fixed order.  workspace: qk_backward_workspace_bytes(head_dim)
     bytes, allocated when not given; calls that may overlap need one each.
     """
-    n, h, hk, d = _sizes(q, k)
-    code = _pair_weights(q, k, q_weight, k_weight, d)
-    for x, g in ((q, dq_out), (k, dk_out)):
-        if (x is None) != (g is None) or (x is not None and (g.shape != x.shape or g.dtype != x.dtype)):
-            raise ValueError("an output's gradient has its input's shape and dtype")
-    go = Launch(stream, q, k, q_weight, k_weight, table, positions, dq_out, dk_out, dq, dk, workspace)
-    yq, yk = _outputs(go, q, k, dq, dk)
-    dw = go.empty((2 if k is not None else 1, d), torch.float32)
-    if workspace is None:
-        workspace = go.empty(qk_backward_workspace_bytes(d), torch.uint8)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    dqw = dw[0]
-    dkw = dw[1] if k is not None else None
-    none = _NONE if k is None else None
-    go.run(lib.qk_norm_rope_backward, *_heads(dq_out), *(none or _heads(dk_out)), *_heads(q), *(none or _heads(k)),
-           ptr(q_weight), ptr(k_weight), eps, *_place(table, positions, n, d), *_heads(yq), *(none or _heads(yk)),
-           ptr(dqw), ptr(dkw), ptr(workspace), workspace.numel() * workspace.element_size(), n, h, hk, d,
-           table.shape[1], int(interleaved), code)
-    return yq, yk, dqw, dkw
+    args = (dq_out, dk_out, q, k, q_weight, k_weight, eps, table, positions, interleaved, dq, dk, workspace)
+    return native.qk_norm_rope_backward(*args) if stream is None else on_stream(stream, native.qk_norm_rope_backward, *args)
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: dict | None = None) -> tuple[list, float]:
@@ -239,8 +132,11 @@ def rope_table(rows: int, rot_dim: int, base: float = 10000.0, scaling: dict | N
     host = (ctypes.c_double * len(freq))(*freq)
     if torch.device(device).type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
-    anchor = torch.empty(0, device=device)
-    go = Launch(stream, anchor)
-    table = go.empty((rows, rot_dim), torch.float32)
-    go.run(lib.rope_table, ptr(table), rows, rot_dim, first_position, ctypes.addressof(host), factor)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        here = torch.cuda.current_stream()
+        table = torch.empty((rows, rot_dim), dtype=torch.float32, device=here.device)
+        _check(lib.rope_table(table.data_ptr(), rows, rot_dim, first_position, ctypes.addressof(host), factor,
+                              here.cuda_stream))
+    if stream is not None:
+        table.record_stream(torch.cuda.current_stream(table.device))
     return table

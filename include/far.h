@@ -230,7 +230,7 @@ int rmsnorm_quant_strided(const void* x, int64_t x_row_stride, const void* weigh
 /*
  * Per-head RMSNorm of queries and keys and the rotation by position, in one pass.  For
  * each token t and head, with x the head's head_dim values (widened to binary32):
- *   r   = fl32(1 / fl32(sqrt(fl32(fl32(S / head_dim) + eps)))),  S = the binary32 sum of x_i^2
+ *   r   = 1 / sqrt(S / head_dim + eps) in binary32 (within 4 * 2^-24), S the binary32 sum of x_i^2
  *   n_i = x_i * r * w_i                                          (w: q_weight or k_weight)
  *   for the first rot_dim values, with c_j and s_j the table's row positions[t]:
  *     pairs FAR_PAIRS_HALF:        j = 0 .. rot_dim/2 - 1, (a, b) = (n_j, n_{j + rot_dim/2})

@@ -201,6 +201,12 @@ __device__ __forceinline__ uint64_t mul_x2(uint64_t a, uint64_t b) {
   return d;
 }
 
+__device__ __forceinline__ uint64_t fma_x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
 // vector memory access of N bytes (N = 8, 16 or 32), N-aligned
 template <int N> __device__ __forceinline__ void load_bytes(const void* p, uint32_t* w) {
   if constexpr (N == 8) {

@@ -14,7 +14,12 @@
 //   interleaved: both values of a pair lie in one chunk; the second chunk is the one half a
 //                head further, so that each load instruction reads whole sectors.
 // A warp keeps one token's cosines and sines, and one weight vector, in registers for all
-// the heads it takes of that token (blockIdx.y picks the heads: queries' or keys').
+// the heads it takes of that token (a block takes queries or keys).  Its heads
+// arrive through a ring in shared memory (cp.async, each lane its own chunks, so no lane
+// waits for another), several steps ahead: the registers hold one step's values, and what is
+// in flight does not depend on how many warps they leave room for.  With loads into
+// registers instead, 128 bytes a lane and 16 warps an SM, the forward pass over 16384 tokens
+// of 32 + 8 heads of 128 bf16 values took 70.4 us and the backward pass over 8192 77.9.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -30,6 +35,9 @@ namespace far {
 namespace {
 
 constexpr int kQkThreads = 256;
+constexpr int kQkCtas = 2;       // CTAs an SM that the vector kernels' registers leave room for
+constexpr int kQkSteps = 6;      // ring slots of 1 KB a warp: 48 KB a CTA
+constexpr int kQkBackSteps = 3;  // ... of 2 KB
 constexpr int kQkMaxDim = 2048;
 constexpr int kQkParts = 1024;  // partial rows of the weights' gradients a backward call may write
 
@@ -49,12 +57,14 @@ struct QkParams {
   float* parts;  // backward: [gridDim.y * gridDim.x][D] partial sums of the weights' gradients
   int64_t table_rows, tokens;
   unsigned int* status;
-  float eps, dim_f, sign;  // sign: -1 turns the other way
+  float eps, inv_dim, sign;  // inv_dim: 1 / D rounded; sign: -1 turns the other way
   int32_t D, rot;
   int32_t pos64, w32;
   int32_t log_l;    // vector kernels: log2 of the lanes a head takes
-  int32_t units_q;  // blockIdx.y below this: queries, else keys
-  int32_t hb;       // heads a unit takes
+  // vector kernels: blocks below blocks_q take queries, the others keys.  A warp's item is
+  // nb steps of neighbouring heads of one token; parts_a_token items a token.
+  int32_t blocks_q, nb, parts_a_token[2];
+  int32_t units_q;  // scalar kernels: blockIdx.y below this: queries, else keys
 };
 
 __device__ __forceinline__ int64_t load_pos(const QkParams& p, int64_t t) {
@@ -76,6 +86,11 @@ template <int ACT> __device__ __forceinline__ float load_w(const void* w, int w3
   if (w32 == 1) return static_cast<const float*>(w)[i];
   if constexpr (ACT == FAR_F32) return w32 == 2 ? load_one<FAR_F16>(w, i) : load_one<FAR_BF16>(w, i);
   else return load_one<ACT>(w, i);
+}
+
+// 1 / sqrt(S / D + eps), within 4 units of 2^-24: S times the rounded 1 / D, CUDA's rsqrtf
+__device__ __forceinline__ float head_rstd(float S, const QkParams& p) {
+  return rsqrtf(__fadd_rn(__fmul_rn(S, p.inv_dim), p.eps));
 }
 
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
@@ -117,169 +132,269 @@ __device__ __forceinline__ Slot slot_of(int s, int C, int RC) {
   return r;
 }
 
-// The cosines and sines a lane needs: for half pairs V of each (c, s), shared by its two
-// chunks; for interleaved pairs V/2 of each for either chunk.
+// Two chunks of V values each, as packed pairs: P pairs a chunk.
+template <int V>
+struct Pair2 {
+  uint64_t a[V / 2], b[V / 2];
+};
+template <int ACT, int V> __device__ __forceinline__ void widen2x(const uint4& r, uint64_t (&p)[V / 2]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  float f[V];
+  widen<ACT, V>(w, f);
+#pragma unroll
+  for (int e = 0; e < V / 2; ++e) p[e] = pk(f[2 * e], f[2 * e + 1]);
+}
+template <int ACT, int V> __device__ __forceinline__ void store_chunk(char* dst, int chunk, const uint64_t (&p)[V / 2]) {
+  if (chunk < 0) return;
+  float f[V];
+#pragma unroll
+  for (int e = 0; e < V / 2; ++e) {
+    const float2 t = unpk(p[e]);
+    f[2 * e] = t.x;
+    f[2 * e + 1] = t.y;
+  }
+  uint32_t w[4];
+  narrow<ACT, V>(f, w);
+  store_bytes<16>(dst + 16 * chunk, w);
+}
+
+__device__ __forceinline__ uint64_t swap_x2(uint64_t v) { return (v >> 32) | (v << 32); }
+
+// The cosines and sines a lane needs.  Half pairs: V of each, shared by its two chunks, packed
+// two neighbours a word: c and s.  Interleaved pairs: V/2 of each for either chunk, each
+// cosine twice in a word and the sine as (-s, s), so that a pair (x, y) turns to
+// (x, y) (c, c) + (y, x) (-s, s).
 template <bool INTER, int V>
 struct Turn {
-  float c[V], s[V];
+  uint64_t c[V / 2 * (INTER ? 2 : 1)], s[V / 2 * (INTER ? 2 : 1)];
   __device__ __forceinline__ void load(const float* row, const Slot& k, int half, float sign) {
     if constexpr (INTER) {
       constexpr int P = V / 2;
 #pragma unroll
-      for (int e = 0; e < P; ++e) {
-        c[e] = k.ra ? row[k.ca * P + e] : 1.f;
-        s[e] = k.ra ? sign * row[half + k.ca * P + e] : 0.f;
-        c[P + e] = k.rb ? row[k.cb * P + e] : 1.f;
-        s[P + e] = k.rb ? sign * row[half + k.cb * P + e] : 0.f;
+      for (int h = 0; h < 2; ++h) {
+        const bool on = h ? k.rb : k.ra;
+        const int chunk = h ? k.cb : k.ca;
+        float cc[P], ss[P];
+#pragma unroll
+        for (int e = 0; e < P; e += 2) {
+          float2 u = make_float2(1.f, 1.f), v = make_float2(0.f, 0.f);
+          if (on) {
+            u = *reinterpret_cast<const float2*>(row + chunk * P + e);
+            v = *reinterpret_cast<const float2*>(row + half + chunk * P + e);
+          }
+          cc[e] = u.x; cc[e + 1] = u.y; ss[e] = sign * v.x; ss[e + 1] = sign * v.y;
+        }
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          c[h * P + e] = pk(cc[e], cc[e]);
+          s[h * P + e] = pk(-ss[e], ss[e]);
+        }
       }
     } else if (k.ra) {
 #pragma unroll
       for (int q = 0; q < V / 4; ++q) {
-        const float4 a = reinterpret_cast<const float4*>(row + k.ca * V)[q];
-        const float4 b = reinterpret_cast<const float4*>(row + half + k.ca * V)[q];
-        c[4 * q] = a.x; c[4 * q + 1] = a.y; c[4 * q + 2] = a.z; c[4 * q + 3] = a.w;
-        s[4 * q] = sign * b.x; s[4 * q + 1] = sign * b.y; s[4 * q + 2] = sign * b.z; s[4 * q + 3] = sign * b.w;
+        const float4 u = reinterpret_cast<const float4*>(row + k.ca * V)[q];
+        const float4 v = reinterpret_cast<const float4*>(row + half + k.ca * V)[q];
+        c[2 * q] = pk(u.x, u.y);
+        c[2 * q + 1] = pk(u.z, u.w);
+        s[2 * q] = pk(v.x, v.y);
+        s[2 * q + 1] = pk(v.z, v.w);
       }
     }
   }
-  // turns the lane's two chunks in place (values outside the rotated part are left alone)
-  __device__ __forceinline__ void apply(float (&a)[V], float (&b)[V], const Slot& k) const {
+  // turns the lane's two chunks in place (values outside the rotated part are left alone);
+  // BACK: the other way (interleaved pairs: the sines' sign says which)
+  template <bool BACK>
+  __device__ __forceinline__ void apply(Pair2<V>& x, const Slot& k) const {
     if constexpr (INTER) {
       constexpr int P = V / 2;
       if (k.ra) {
 #pragma unroll
-        for (int e = 0; e < P; ++e) {
-          const float x = a[2 * e], y = a[2 * e + 1];
-          a[2 * e] = __fmaf_rn(x, c[e], -__fmul_rn(y, s[e]));
-          a[2 * e + 1] = __fmaf_rn(y, c[e], __fmul_rn(x, s[e]));
-        }
+        for (int e = 0; e < P; ++e) x.a[e] = fma_x2(x.a[e], c[e], mul_x2(swap_x2(x.a[e]), s[e]));
       }
       if (k.rb) {
 #pragma unroll
-        for (int e = 0; e < P; ++e) {
-          const float x = b[2 * e], y = b[2 * e + 1];
-          b[2 * e] = __fmaf_rn(x, c[P + e], -__fmul_rn(y, s[P + e]));
-          b[2 * e + 1] = __fmaf_rn(y, c[P + e], __fmul_rn(x, s[P + e]));
-        }
+        for (int e = 0; e < P; ++e) x.b[e] = fma_x2(x.b[e], c[P + e], mul_x2(swap_x2(x.b[e]), s[P + e]));
       }
     } else if (k.ra) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float x = a[e], y = b[e];
-        a[e] = __fmaf_rn(x, c[e], -__fmul_rn(y, s[e]));
-        b[e] = __fmaf_rn(y, c[e], __fmul_rn(x, s[e]));
+      for (int e = 0; e < V / 2; ++e) {
+        const uint64_t u = x.a[e], v = x.b[e];
+        if constexpr (BACK) {
+          x.a[e] = fma_x2(u, c[e], mul_x2(v, s[e]));
+          x.b[e] = sub_x2(mul_x2(v, c[e]), mul_x2(u, s[e]));
+        } else {
+          x.a[e] = sub_x2(mul_x2(u, c[e]), mul_x2(v, s[e]));
+          x.b[e] = fma_x2(v, c[e], mul_x2(u, s[e]));
+        }
       }
     }
   }
 };
 
+// the weight's values of a lane's two chunks (zeros where there is none: the lane adds nothing)
 template <int ACT, int V>
-__device__ __forceinline__ void load_weights(const void* w, int w32, int chunk, float (&f)[V]) {
+__device__ __forceinline__ void load_weights(const void* w, int w32, const Slot& k, Pair2<V>& f) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) f[e] = chunk >= 0 ? load_w<ACT>(w, w32, chunk * V + e) : 0.f;
+  for (int e = 0; e < V / 2; ++e) {
+    const int a = k.ca * V + 2 * e, b = k.cb * V + 2 * e;
+    f.a[e] = k.ca >= 0 ? pk(load_w<ACT>(w, w32, a), load_w<ACT>(w, w32, a + 1)) : 0ull;
+    f.b[e] = k.cb >= 0 ? pk(load_w<ACT>(w, w32, b), load_w<ACT>(w, w32, b + 1)) : 0ull;
+  }
 }
 
-__device__ __forceinline__ uint4 load_chunk(const char* p, int chunk) {
-  return chunk >= 0 ? *reinterpret_cast<const uint4*>(p + 16 * chunk) : make_uint4(0u, 0u, 0u, 0u);
+// 16 bytes into this lane's place of the ring, without waiting
+__device__ __forceinline__ void async_chunk(uint32_t dst, const char* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-template <int ACT, int V> __device__ __forceinline__ void widen_chunk(const uint4& r, float (&f)[V]) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-  widen<ACT, V>(w, f);
+__device__ __forceinline__ uint4 take_chunk(uint32_t src) {
+  uint4 r;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(src) : "memory");
+  return r;
 }
-template <int ACT, int V> __device__ __forceinline__ void store_chunk(char* p, int chunk, const float (&f)[V]) {
-  if (chunk < 0) return;
-  uint32_t w[4];
-  narrow<ACT, V>(f, w);
-  store_bytes<16>(p + 16 * chunk, w);
+__device__ __forceinline__ void clear_chunk(uint32_t dst) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
 }
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// the sum over a head's lanes of what each lane holds in packed pairs
+__device__ __forceinline__ float head_sum(uint64_t v, int lanes) {
+  const float2 f = unpk(v);
+  return lanes_sum(__fadd_rn(f.x, f.y), lanes);
+}
+
+// A warp's walk over its items: `groups` neighbouring heads a step (one for each group of
+// lanes), nb steps an item.  What it points to moves along by additions.
+struct Walk {
+  int64_t item, t;
+  int h, end;  // this step's first head; the item's heads end
+  __device__ __forceinline__ bool done(int64_t items) const { return item >= items; }
+  __device__ __forceinline__ void start(int parts, int span, int heads) {
+    int part = 0;
+    t = item;
+    if (parts > 1) {
+      t = item / parts;
+      part = (int)(item - t * parts);
+    }
+    h = part * span;
+    end = min(heads, h + span);
+  }
+};
 
 template <int ACT, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kQkThreads, 2) qk_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const QkParams p) {
   constexpr int V = 16 / dtype_size<ACT>::value;
-  constexpr int U = 4;  // heads a lane holds at a time: 128 bytes of loads in flight a lane
+  extern __shared__ __align__(16) unsigned char ring[];  // [warps][kQkSteps][2][32 lanes] chunks
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int L = 1 << p.log_l, groups = 32 >> p.log_l, grp = lane >> p.log_l;
-  const bool is_k = (int)blockIdx.y >= p.units_q;
+  const bool is_k = (int)blockIdx.x >= p.blocks_q;
   const QkSeg& S = p.seg[is_k];
-  const int h0 = (is_k ? (int)blockIdx.y - p.units_q : (int)blockIdx.y) * p.hb;
-  const int h1 = min(S.heads, h0 + p.hb);
+  const int parts = p.parts_a_token[is_k], span = p.nb * groups, heads = S.heads;
+  const int64_t items = p.tokens * parts;
+  const int64_t stride = (int64_t)(is_k ? gridDim.x - p.blocks_q : p.blocks_q) * warps;
   const Slot k = slot_of<INTER>(lane & (L - 1), p.D / V, p.rot / V);
-  float wa[V], wb[V];
-  if constexpr (NORM) {
-    load_weights<ACT, V>(S.w, p.w32, k.ca, wa);
-    load_weights<ACT, V>(S.w, p.w32, k.cb, wb);
-  }
-  const int64_t step = (int64_t)gridDim.x * warps;
-  for (int64_t t = (int64_t)blockIdx.x * warps + warp; t < p.tokens; t += step) {
-    const int64_t pos = load_pos(p, t);
-    const bool ok = pos >= 0 && pos < p.table_rows;
-    if (pos >= p.table_rows && lane == 0) atomicOr(p.status, 1u << FAR_ERR_POSITION);
-    Turn<INTER, V> turn;
-    const char* xt = S.x + t * S.xt;
-    char* yt = S.y + t * S.yt;
-    bool first = true;
-    for (int hb = h0; hb < h1; hb += U * groups) {
-      uint4 xa[U], xb[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = hb + u * groups + grp;
-        const char* x = xt + h * S.xh;
-        xa[u] = load_chunk(x, h < h1 ? k.ca : -1);
-        xb[u] = load_chunk(x, h < h1 ? k.cb : -1);
+  const uint32_t mine = smem_addr(ring) + warp * (kQkSteps * 1024) + lane * 16;
+  const int oa = 16 * max(k.ca, 0), ob = 16 * max(k.cb, 0);
+  if (k.ca < 0 || k.cb < 0)  // chunks that never arrive add nothing to their head
+    for (int i = 0; i < 2 * kQkSteps; ++i) clear_chunk(mine + 512 * i);
+  Walk in{(int64_t)(is_k ? (int)blockIdx.x - p.blocks_q : (int)blockIdx.x) * warps + warp, 0, 0, 0};
+  Walk at = in;
+  const char* src = nullptr;
+  auto aim = [&]() {
+    in.start(parts, span, heads);
+    src = S.x + in.t * S.xt + (int64_t)(in.h + grp) * S.xh;
+  };
+  if (!in.done(items)) aim();
+  const int64_t xh = groups * S.xh, yh = groups * S.yh;
+  // one step's chunks of this lane on their way
+  auto fetch = [&](int slot) {
+    if (!in.done(items)) {
+      if (in.h + grp < in.end) {
+        if (k.ca >= 0) async_chunk(mine + slot * 1024, src + oa);
+        if (k.cb >= 0) async_chunk(mine + slot * 1024 + 512, src + ob);
       }
-      if (first) {
-        turn.load(p.table + (ok ? pos : 0) * p.rot, k, p.rot >> 1, p.sign);
-        first = false;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = hb + u * groups + grp;
-        if (hb + u * groups >= h1) break;  // uniform over the warp
-        float a[V], b[V];
-        widen_chunk<ACT, V>(xa[u], a);
-        widen_chunk<ACT, V>(xb[u], b);
-        if constexpr (NORM) {
-          float ss = 0.f, st = 0.f;
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            ss = __fmaf_rn(a[e], a[e], ss);
-            st = __fmaf_rn(b[e], b[e], st);
-          }
-          const float r = row_rstd(lanes_sum(__fadd_rn(ss, st), L), p.dim_f, p.eps);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            a[e] = __fmul_rn(__fmul_rn(a[e], r), wa[e]);
-            b[e] = __fmul_rn(__fmul_rn(b[e], r), wb[e]);
-          }
-        }
-        turn.apply(a, b, k);
-        if (!ok) {
-          const float v = pos < 0 ? 0.f : __uint_as_float(0x7fffffffu);
-#pragma unroll
-          for (int e = 0; e < V; ++e) a[e] = b[e] = v;
-        }
-        if (h < h1) {
-          char* y = yt + h * S.yh;
-          store_chunk<ACT, V>(y, k.ca, a);
-          store_chunk<ACT, V>(y, k.cb, b);
-        }
+      src += xh;
+      in.h += groups;
+      if (in.h >= in.end) {
+        in.item += stride;
+        if (!in.done(items)) aim();
       }
     }
+    async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kQkSteps - 1; ++i) fetch(i);
+  Pair2<V> w;
+  if constexpr (NORM) load_weights<ACT, V>(S.w, p.w32, k, w);
+  Turn<INTER, V> turn;
+  int slot = 0;
+  for (; !at.done(items); at.item += stride) {
+   at.start(parts, span, heads);
+   const int64_t pos = load_pos(p, at.t);
+   const bool ok = pos >= 0 && pos < p.table_rows;
+   if (pos >= p.table_rows && lane == 0) atomicOr(p.status, 1u << FAR_ERR_POSITION);
+   turn.load(p.table + (ok ? pos : 0) * p.rot, k, p.rot >> 1, p.sign);
+   char* y = S.y + at.t * S.yt + (int64_t)(at.h + grp) * S.yh;
+   for (; at.h < at.end; at.h += groups, y += yh) {
+    fetch(slot == 0 ? kQkSteps - 1 : slot - 1);
+    async_wait<kQkSteps - 1>();
+    Pair2<V> x;
+    widen2x<ACT, V>(take_chunk(mine + slot * 1024), x.a);
+    widen2x<ACT, V>(take_chunk(mine + slot * 1024 + 512), x.b);
+    if constexpr (NORM) {
+      uint64_t ss = 0ull, st = 0ull;
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        ss = fma_x2(x.a[e], x.a[e], ss);
+        st = fma_x2(x.b[e], x.b[e], st);
+      }
+      const float r = head_rstd(head_sum(add_x2(ss, st), L), p);
+      const uint64_t r2 = pk(r, r);
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        x.a[e] = mul_x2(mul_x2(x.a[e], r2), w.a[e]);
+        x.b[e] = mul_x2(mul_x2(x.b[e], r2), w.b[e]);
+      }
+    }
+    if (!NORM && p.sign < 0.f) turn.template apply<true>(x, k);
+    else turn.template apply<false>(x, k);
+    if (!ok) {
+      const float v = pos < 0 ? 0.f : __uint_as_float(0x7fffffffu);
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) x.a[e] = x.b[e] = pk(v, v);
+    }
+    if (at.h + grp < at.end) {
+      store_chunk<ACT, V>(y, k.ca, x.a);
+      store_chunk<ACT, V>(y, k.cb, x.b);
+    }
+    if (++slot == kQkSteps) slot = 0;
+   }
   }
 }
 
 // One partial row of the weights' gradient a block: the warps' sums, added in their order.
 template <int V>
-__device__ __forceinline__ void write_part(float* part, float* sm, const Slot& k, float (&da)[V], float (&db)[V],
-                                           int L, int lane, int warp, int warps, int D) {
+__device__ __forceinline__ void write_part(float* part, float* sm, const Slot& k, const Pair2<V>& d, int L, int lane,
+                                           int warp, int warps, int D) {
+  float da[V], db[V];
+#pragma unroll
+  for (int e = 0; e < V / 2; ++e) {
+    const float2 u = unpk(d.a[e]), v = unpk(d.b[e]);
+    da[2 * e] = u.x;
+    da[2 * e + 1] = u.y;
+    db[2 * e] = v.x;
+    db[2 * e + 1] = v.y;
+  }
 #pragma unroll
   for (int e = 0; e < V; ++e)
     for (int off = L; off < 32; off <<= 1) {
       da[e] = __fadd_rn(da[e], __shfl_xor_sync(0xffffffffu, da[e], off));
       db[e] = __fadd_rn(db[e], __shfl_xor_sync(0xffffffffu, db[e], off));
     }
+  __syncthreads();  // every warp is done with the ring, where the sums go
   if (lane < L) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -296,99 +411,124 @@ __device__ __forceinline__ void write_part(float* part, float* sm, const Slot& k
 }
 
 template <int ACT, bool INTER>
-__global__ void __launch_bounds__(kQkThreads, 2) qk_back_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_back_kernel(const QkParams p) {
   constexpr int V = 16 / dtype_size<ACT>::value;
-  constexpr int U = 2;  // heads a lane holds at a time: x and dy of two, 128 bytes a lane
-  extern __shared__ float sm_dw[];
+  extern __shared__ __align__(16) unsigned char ring[];  // [warps][kQkBackSteps][x, x, dy, dy][32 lanes] chunks
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int L = 1 << p.log_l, groups = 32 >> p.log_l, grp = lane >> p.log_l;
-  const bool is_k = (int)blockIdx.y >= p.units_q;
+  const bool is_k = (int)blockIdx.x >= p.blocks_q;
   const QkSeg& S = p.seg[is_k];
-  const int h0 = (is_k ? (int)blockIdx.y - p.units_q : (int)blockIdx.y) * p.hb;
-  const int h1 = min(S.heads, h0 + p.hb);
+  const int parts = p.parts_a_token[is_k], span = p.nb * groups, heads = S.heads;
+  const int64_t items = p.tokens * parts;
+  const int64_t stride = (int64_t)(is_k ? gridDim.x - p.blocks_q : p.blocks_q) * warps;
   const Slot k = slot_of<INTER>(lane & (L - 1), p.D / V, p.rot / V);
-  float wa[V], wb[V], da[V], db[V];
-  load_weights<ACT, V>(S.w, p.w32, k.ca, wa);
-  load_weights<ACT, V>(S.w, p.w32, k.cb, wb);
-#pragma unroll
-  for (int e = 0; e < V; ++e) da[e] = db[e] = 0.f;
-  const int64_t step = (int64_t)gridDim.x * warps;
-  for (int64_t t = (int64_t)blockIdx.x * warps + warp; t < p.tokens; t += step) {
-    const int64_t pos = load_pos(p, t);
-    const bool ok = pos >= 0 && pos < p.table_rows;
-    if (pos >= p.table_rows && lane == 0) atomicOr(p.status, 1u << FAR_ERR_POSITION);
-    Turn<INTER, V> turn;
-    bool first = true;
-    for (int hb = h0; hb < h1; hb += U * groups) {
-      uint4 xa[U], xb[U], ga[U], gb[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = hb + u * groups + grp;
-        const char* x = S.x + t * S.xt + h * S.xh;
-        const char* g = S.g + t * S.gt + h * S.gh;
-        xa[u] = load_chunk(x, h < h1 ? k.ca : -1);
-        xb[u] = load_chunk(x, h < h1 ? k.cb : -1);
-        ga[u] = load_chunk(g, h < h1 ? k.ca : -1);
-        gb[u] = load_chunk(g, h < h1 ? k.cb : -1);
+  const uint32_t mine = smem_addr(ring) + warp * (kQkBackSteps * 2048) + lane * 16;
+  const int oa = 16 * max(k.ca, 0), ob = 16 * max(k.cb, 0);
+  if (k.ca < 0 || k.cb < 0)
+    for (int i = 0; i < 4 * kQkBackSteps; ++i) clear_chunk(mine + 512 * i);
+  Walk in{(int64_t)(is_k ? (int)blockIdx.x - p.blocks_q : (int)blockIdx.x) * warps + warp, 0, 0, 0};
+  Walk at = in;
+  const char *src = nullptr, *grad = nullptr;
+  auto aim = [&]() {
+    in.start(parts, span, heads);
+    src = S.x + in.t * S.xt + (int64_t)(in.h + grp) * S.xh;
+    grad = S.g + in.t * S.gt + (int64_t)(in.h + grp) * S.gh;
+  };
+  if (!in.done(items)) aim();
+  const int64_t xh = groups * S.xh, gh = groups * S.gh, yh = groups * S.yh;
+  auto fetch = [&](int slot) {
+    if (!in.done(items)) {
+      if (in.h + grp < in.end) {
+        if (k.ca >= 0) {
+          async_chunk(mine + slot * 2048, src + oa);
+          async_chunk(mine + slot * 2048 + 1024, grad + oa);
+        }
+        if (k.cb >= 0) {
+          async_chunk(mine + slot * 2048 + 512, src + ob);
+          async_chunk(mine + slot * 2048 + 1536, grad + ob);
+        }
       }
-      if (first) {
-        turn.load(p.table + (ok ? pos : 0) * p.rot, k, p.rot >> 1, p.sign);
-        first = false;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = hb + u * groups + grp;
-        if (hb + u * groups >= h1) break;  // uniform over the warp
-        float a[V], b[V], c[V], d[V];
-        widen_chunk<ACT, V>(xa[u], a);
-        widen_chunk<ACT, V>(xb[u], b);
-        widen_chunk<ACT, V>(ga[u], c);
-        widen_chunk<ACT, V>(gb[u], d);
-        float ss = 0.f, st = 0.f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          ss = __fmaf_rn(a[e], a[e], ss);
-          st = __fmaf_rn(b[e], b[e], st);
-        }
-        const float r = row_rstd(lanes_sum(__fadd_rn(ss, st), L), p.dim_f, p.eps);
-        turn.apply(c, d, k);
-        float da1 = 0.f, db1 = 0.f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          a[e] = __fmul_rn(a[e], r);  // u = x r
-          b[e] = __fmul_rn(b[e], r);
-          if (ok && h < h1) {
-            da[e] = __fmaf_rn(c[e], a[e], da[e]);
-            db[e] = __fmaf_rn(d[e], b[e], db[e]);
-          }
-          c[e] = __fmul_rn(c[e], wa[e]);  // h = g w
-          d[e] = __fmul_rn(d[e], wb[e]);
-          da1 = __fmaf_rn(c[e], a[e], da1);
-          db1 = __fmaf_rn(d[e], b[e], db1);
-        }
-        const float m = __fdiv_rn(lanes_sum(__fadd_rn(da1, db1), L), p.dim_f);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          a[e] = __fmul_rn(r, __fmaf_rn(-a[e], m, c[e]));
-          b[e] = __fmul_rn(r, __fmaf_rn(-b[e], m, d[e]));
-        }
-        if (!ok) {
-          const float v = pos < 0 ? 0.f : __uint_as_float(0x7fffffffu);
-#pragma unroll
-          for (int e = 0; e < V; ++e) a[e] = b[e] = v;
-        }
-        if (h < h1) {
-          char* y = S.y + t * S.yt + h * S.yh;
-          store_chunk<ACT, V>(y, k.ca, a);
-          store_chunk<ACT, V>(y, k.cb, b);
-        }
+      src += xh;
+      grad += gh;
+      in.h += groups;
+      if (in.h >= in.end) {
+        in.item += stride;
+        if (!in.done(items)) aim();
       }
     }
+    async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kQkBackSteps - 1; ++i) fetch(i);
+  Pair2<V> w, dw;
+  load_weights<ACT, V>(S.w, p.w32, k, w);
+#pragma unroll
+  for (int e = 0; e < V / 2; ++e) dw.a[e] = dw.b[e] = 0ull;
+  Turn<INTER, V> turn;
+  int slot = 0;
+  for (; !at.done(items); at.item += stride) {
+   at.start(parts, span, heads);
+   const int64_t pos = load_pos(p, at.t);
+   const bool ok = pos >= 0 && pos < p.table_rows;
+   if (pos >= p.table_rows && lane == 0) atomicOr(p.status, 1u << FAR_ERR_POSITION);
+   turn.load(p.table + (ok ? pos : 0) * p.rot, k, p.rot >> 1, p.sign);
+   char* y = S.y + at.t * S.yt + (int64_t)(at.h + grp) * S.yh;
+   for (; at.h < at.end; at.h += groups, y += yh) {
+    fetch(slot == 0 ? kQkBackSteps - 1 : slot - 1);
+    async_wait<kQkBackSteps - 1>();
+    Pair2<V> x, g;
+    widen2x<ACT, V>(take_chunk(mine + slot * 2048), x.a);
+    widen2x<ACT, V>(take_chunk(mine + slot * 2048 + 512), x.b);
+    widen2x<ACT, V>(take_chunk(mine + slot * 2048 + 1024), g.a);
+    widen2x<ACT, V>(take_chunk(mine + slot * 2048 + 1536), g.b);
+    uint64_t ss = 0ull, st = 0ull;
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      ss = fma_x2(x.a[e], x.a[e], ss);
+      st = fma_x2(x.b[e], x.b[e], st);
+    }
+    const float r = head_rstd(head_sum(add_x2(ss, st), L), p);
+    const uint64_t r2 = pk(r, r);
+    turn.template apply<true>(g, k);
+    const bool here = ok && at.h + grp < at.end;
+    ss = st = 0ull;
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      x.a[e] = mul_x2(x.a[e], r2);  // u = x r
+      x.b[e] = mul_x2(x.b[e], r2);
+      if (here) {
+        dw.a[e] = fma_x2(g.a[e], x.a[e], dw.a[e]);
+        dw.b[e] = fma_x2(g.b[e], x.b[e], dw.b[e]);
+      }
+      g.a[e] = mul_x2(g.a[e], w.a[e]);  // h = g w
+      g.b[e] = mul_x2(g.b[e], w.b[e]);
+      ss = fma_x2(g.a[e], x.a[e], ss);
+      st = fma_x2(g.b[e], x.b[e], st);
+    }
+    const float m = -__fmul_rn(head_sum(add_x2(ss, st), L), p.inv_dim);
+    const uint64_t m2 = pk(m, m);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      x.a[e] = mul_x2(r2, fma_x2(x.a[e], m2, g.a[e]));
+      x.b[e] = mul_x2(r2, fma_x2(x.b[e], m2, g.b[e]));
+    }
+    if (!ok) {
+      const float v = pos < 0 ? 0.f : __uint_as_float(0x7fffffffu);
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) x.a[e] = x.b[e] = pk(v, v);
+    }
+    if (at.h + grp < at.end) {
+      store_chunk<ACT, V>(y, k.ca, x.a);
+      store_chunk<ACT, V>(y, k.cb, x.b);
+    }
+    if (++slot == kQkBackSteps) slot = 0;
+   }
   }
-  write_part<V>(p.parts + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * p.D, sm_dw, k, da, db, L, lane, warp, warps,
-                p.D);
+  async_wait<0>();
+  write_part<V>(p.parts + (int64_t)blockIdx.x * p.D, reinterpret_cast<float*>(ring), k, dw, L,
+                lane, warp, warps, p.D);
 }
 
 // ---------------------------------------------------------------------------
@@ -440,7 +580,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_any_kernel(const QkParams p, in
         const float v = load_one<ACT>(x, i);
         ss = __fmaf_rn(v, v, ss);
       }
-      r = row_rstd(lanes_sum(ss, 32), p.dim_f, p.eps);
+      r = head_rstd(lanes_sum(ss, 32), p);
     }
     if constexpr (!BACK) {
       for (int i = lane; i < items; i += 32) {
@@ -464,7 +604,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_any_kernel(const QkParams p, in
       float dot = 0.f;
       // two sweeps over the head: the mean of h u (and the weights' sums), then dx
       for (int sweep = 0; sweep < 2; ++sweep) {
-        const float m = sweep ? __fdiv_rn(lanes_sum(dot, 32), p.dim_f) : 0.f;
+        const float m = sweep ? __fmul_rn(lanes_sum(dot, 32), p.inv_dim) : 0.f;
         for (int i = lane; i < items; i += 32) {
           const Item it = item_of(i, p.rot, inter);
           float a = load_one<ACT>(g, it.a), b = 0.f;
@@ -680,7 +820,8 @@ int validate_qk(const QkCall& c) {
 
 struct QkPlan {
   bool vec;
-  int log_l, hb, units_q, units_k;
+  int log_l, nb, parts[2], blocks[2];
+  int units_q, units_k;
   dim3 grid, block;
   size_t smem;
 };
@@ -715,31 +856,32 @@ QkPlan plan_qk(const QkCall& c, int sms) {
   }
   while ((1 << g.log_l) < slots) ++g.log_l;
   const int groups = 32 >> g.log_l;
-  // Heads a warp takes of a token: as many as two sweeps hold, fewer (down to one a group of
-  // lanes) while that leaves SMs without 16 warps of work.
-  const int U = c.back ? 2 : 4;
-  int64_t hb = 2 * U * groups;
-  auto units = [&](int64_t h) { return (c.heads[0] + h - 1) / h + (c.heads[1] + h - 1) / h; };
-  while (hb > groups && c.tokens * units(hb) < (int64_t)sms * 16) hb /= 2;
-  while (units(hb) > (c.back ? 64 : 32768)) hb *= 2;  // gridDim.y's limit; backward: the partial rows'
-  g.hb = (int)(hb < INT32_MAX / 2 ? hb : INT32_MAX / 2);
-  g.units_q = (int)((c.heads[0] + hb - 1) / hb);
-  g.units_k = (int)((c.heads[1] + hb - 1) / hb);
-  const int u = g.units_q + g.units_k;
+  // Steps (of `groups` heads) a warp takes of a token at a time, with that token's cosines and
+  // sines in its registers: up to 8, fewer (down to one) while that leaves SMs without 16 warps
+  // of work.
+  const int64_t steps[2] = {(c.heads[0] + groups - 1) / groups, (c.heads[1] + groups - 1) / groups};
+  g.nb = 8;
+  auto items = [&](int i) { return c.tokens * ((steps[i] + g.nb - 1) / g.nb); };
+  while (g.nb > 1 && items(0) + items(1) < (int64_t)sms * 16) g.nb /= 2;
   int warps = 8;
-  while (warps > 1 && (c.tokens + warps - 1) / warps * u < sms) warps /= 2;
-  const int64_t blocks = (c.tokens + warps - 1) / warps;
-  int64_t cap;
-  if (c.back) {
-    cap = (2 * sms + u - 1) / u;  // two blocks an SM, one partial row each
-    if (cap * u > kQkParts) cap = kQkParts / u;
-  } else {
-    cap = (8 * sms + u - 1) / u;
+  while (warps > 1 && (items(0) + items(1)) / warps < sms) warps /= 2;
+  // one wave of blocks, shared between queries and keys as their steps are
+  const int64_t all = kQkCtas * sms < kQkParts ? kQkCtas * sms : kQkParts;
+  int64_t blocks[2];
+  for (int i = 0; i < 2; ++i) {
+    g.parts[i] = (int)((steps[i] + g.nb - 1) / g.nb);
+    const int64_t need = (items(i) + warps - 1) / warps;
+    int64_t share = (all * steps[i] + (steps[0] + steps[1]) / 2) / (steps[0] + steps[1]);
+    if (share < 1) share = 1;
+    if (share > all - 1) share = all - 1;  // (the other has at least one)
+    if (c.heads[1 - i] == 0) share = all;
+    blocks[i] = c.heads[i] == 0 ? 0 : need < share ? need : share;
   }
-  if (cap < 1) cap = 1;
-  g.grid = dim3((unsigned)(blocks < cap ? blocks : cap), u);
+  g.blocks[0] = (int)blocks[0];
+  g.blocks[1] = (int)blocks[1];
+  g.grid = dim3((unsigned)(blocks[0] + blocks[1]));
   g.block = dim3(32 * warps);
-  g.smem = c.back ? (size_t)warps * D * 4 : 0;
+  g.smem = (size_t)warps * (c.back ? kQkBackSteps * 2048 : kQkSteps * 1024);  // (the weights' sums fit: D <= 512)
   return g;
 }
 
@@ -800,7 +942,7 @@ int run_qk(const QkCall& c, void* stream) {
   p.tokens = c.tokens;
   p.status = status;
   p.eps = c.eps;
-  p.dim_f = (float)c.D;
+  p.inv_dim = 1.0f / (float)c.D;
   p.sign = (c.back || c.transpose) ? -1.f : 1.f;
   p.D = (int32_t)c.D;
   p.rot = (int32_t)c.rot;
@@ -808,14 +950,18 @@ int run_qk(const QkCall& c, void* stream) {
   p.w32 = c.wd == FAR_F32 ? 1 : c.wd == FAR_F16 ? 2 : 3;
   p.log_l = g.log_l;
   p.units_q = g.units_q;
-  p.hb = g.hb;
+  p.blocks_q = g.blocks[0];
+  p.nb = g.nb;
+  p.parts_a_token[0] = g.parts[0];
+  p.parts_a_token[1] = g.parts[1];
   cudaError_t e = c.act == FAR_F16    ? launch_qk<FAR_F16>(c, g, p, s)
                   : c.act == FAR_BF16 ? launch_qk<FAR_BF16>(c, g, p, s)
                                       : launch_qk<FAR_F32>(c, g, p, s);
   if (e == cudaSuccess && c.back) {
-    const int rows = (int)g.grid.x;
+    const int rows = (int)g.grid.x;  // scalar kernels: of either half
+    const int rows_q = g.vec ? g.blocks[0] : rows * g.units_q, rows_k = g.vec ? g.blocks[1] : rows * g.units_k;
     e = launch_k(qk_weight_grad_kernel, dim3((unsigned)((c.D + 31) / 32), 2), dim3(32, 32), 0, s,
-                 (const float*)p.parts, (int)c.D, rows * g.units_q, rows * g.units_k, c.heads[0] ? c.dw[0] : nullptr,
+                 (const float*)p.parts, (int)c.D, rows_q, rows_k, c.heads[0] ? c.dw[0] : nullptr,
                  c.heads[1] ? c.dw[1] : nullptr);
   }
   return e == cudaSuccess ? FAR_OK : cuda_error_status(e);

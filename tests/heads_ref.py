@@ -3,9 +3,9 @@ the error that binary32 steps may leave (the tests' tolerances).
 
 Bounds, with u = 2^-24: a sum of D squares by fused multiply-adds in any tree of the kernels
 (at most D/32 + 5 deep in the scalar kernel, V + 6 in the vector one; D/16 + 8 covers both)
-is within (D/16 + 8) u of itself, the root halves that, and the division, the sum with eps,
-the root, the reciprocal and the products after it are one u each.  So n is within
-(D/32 + 12) u |n|, and a turned pair within that of |a c| + |b s|, plus 2 u of the same for
+is within (D/16 + 8) u of itself, and the root halves that.  The product by 1/D and the sum
+with eps (3 u, halved), the reciprocal root (within two units in the last place: 4 u) and
+the two products after it make 7.5 u more.  So n is within (D/32 + 12) u |n|, and a turned pair within that of |a c| + |b s|, plus 2 u of the same for
 its two roundings.
 """
 import torch

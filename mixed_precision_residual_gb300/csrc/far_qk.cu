@@ -94,7 +94,9 @@ __device__ __forceinline__ float head_rstd(float S, const QkParams& p) {
 }
 
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
-  for (int off = lanes >> 1; off > 0; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    if (off < lanes) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));  // (the whole warp alike)
   return v;
 }
 
@@ -132,24 +134,38 @@ __device__ __forceinline__ Slot slot_of(int s, int C, int RC) {
   return r;
 }
 
-// Two chunks of V values each, as packed pairs: P pairs a chunk.
+// Two neighbouring values.  (As two registers: held as one 64-bit register for the packed
+// binary32 instructions, the backward kernel issued 386 instructions a step of four heads
+// against SCALARCOUNT.)
+struct X2 {
+  float x, y;
+};
+__device__ __forceinline__ X2 x2(float x, float y) { return X2{x, y}; }
+__device__ __forceinline__ float2 un2(X2 v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ X2 vfma(X2 a, X2 b, X2 c) { return X2{__fmaf_rn(a.x, b.x, c.x), __fmaf_rn(a.y, b.y, c.y)}; }
+// c - a b
+__device__ __forceinline__ X2 vnfma(X2 a, X2 b, X2 c) { return X2{__fmaf_rn(-a.x, b.x, c.x), __fmaf_rn(-a.y, b.y, c.y)}; }
+__device__ __forceinline__ X2 vmul(X2 a, X2 b) { return X2{__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y)}; }
+__device__ __forceinline__ X2 vadd(X2 a, X2 b) { return X2{__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)}; }
+
+// Two chunks of V values each, in pairs.
 template <int V>
 struct Pair2 {
-  uint64_t a[V / 2], b[V / 2];
+  X2 a[V / 2], b[V / 2];
 };
-template <int ACT, int V> __device__ __forceinline__ void widen2x(const uint4& r, uint64_t (&p)[V / 2]) {
+template <int ACT, int V> __device__ __forceinline__ void widen2x(const uint4& r, X2 (&p)[V / 2]) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
   float f[V];
   widen<ACT, V>(w, f);
 #pragma unroll
-  for (int e = 0; e < V / 2; ++e) p[e] = pk(f[2 * e], f[2 * e + 1]);
+  for (int e = 0; e < V / 2; ++e) p[e] = x2(f[2 * e], f[2 * e + 1]);
 }
-template <int ACT, int V> __device__ __forceinline__ void store_chunk(char* dst, int chunk, const uint64_t (&p)[V / 2]) {
+template <int ACT, int V> __device__ __forceinline__ void store_chunk(char* dst, int chunk, const X2 (&p)[V / 2]) {
   if (chunk < 0) return;
   float f[V];
 #pragma unroll
   for (int e = 0; e < V / 2; ++e) {
-    const float2 t = unpk(p[e]);
+    const float2 t = un2(p[e]);
     f[2 * e] = t.x;
     f[2 * e + 1] = t.y;
   }
@@ -158,7 +174,7 @@ template <int ACT, int V> __device__ __forceinline__ void store_chunk(char* dst,
   store_bytes<16>(dst + 16 * chunk, w);
 }
 
-__device__ __forceinline__ uint64_t swap_x2(uint64_t v) { return (v >> 32) | (v << 32); }
+__device__ __forceinline__ X2 swap_x2(X2 v) { return X2{v.y, v.x}; }
 
 // The cosines and sines a lane needs.  Half pairs: V of each, shared by its two chunks, packed
 // two neighbours a word: c and s.  Interleaved pairs: V/2 of each for either chunk, each
@@ -166,7 +182,7 @@ __device__ __forceinline__ uint64_t swap_x2(uint64_t v) { return (v >> 32) | (v 
 // (x, y) (c, c) + (y, x) (-s, s).
 template <bool INTER, int V>
 struct Turn {
-  uint64_t c[V / 2 * (INTER ? 2 : 1)], s[V / 2 * (INTER ? 2 : 1)];
+  X2 c[V / 2 * (INTER ? 2 : 1)], s[V / 2 * (INTER ? 2 : 1)];
   __device__ __forceinline__ void load(const float* row, const Slot& k, int half, float sign) {
     if constexpr (INTER) {
       constexpr int P = V / 2;
@@ -186,8 +202,8 @@ struct Turn {
         }
 #pragma unroll
         for (int e = 0; e < P; ++e) {
-          c[h * P + e] = pk(cc[e], cc[e]);
-          s[h * P + e] = pk(-ss[e], ss[e]);
+          c[h * P + e] = x2(cc[e], cc[e]);
+          s[h * P + e] = x2(-ss[e], ss[e]);
         }
       }
     } else if (k.ra) {
@@ -195,10 +211,10 @@ struct Turn {
       for (int q = 0; q < V / 4; ++q) {
         const float4 u = reinterpret_cast<const float4*>(row + k.ca * V)[q];
         const float4 v = reinterpret_cast<const float4*>(row + half + k.ca * V)[q];
-        c[2 * q] = pk(u.x, u.y);
-        c[2 * q + 1] = pk(u.z, u.w);
-        s[2 * q] = pk(v.x, v.y);
-        s[2 * q + 1] = pk(v.z, v.w);
+        c[2 * q] = x2(u.x, u.y);
+        c[2 * q + 1] = x2(u.z, u.w);
+        s[2 * q] = x2(v.x, v.y);
+        s[2 * q + 1] = x2(v.z, v.w);
       }
     }
   }
@@ -210,22 +226,22 @@ struct Turn {
       constexpr int P = V / 2;
       if (k.ra) {
 #pragma unroll
-        for (int e = 0; e < P; ++e) x.a[e] = fma_x2(x.a[e], c[e], mul_x2(swap_x2(x.a[e]), s[e]));
+        for (int e = 0; e < P; ++e) x.a[e] = vfma(x.a[e], c[e], vmul(swap_x2(x.a[e]), s[e]));
       }
       if (k.rb) {
 #pragma unroll
-        for (int e = 0; e < P; ++e) x.b[e] = fma_x2(x.b[e], c[P + e], mul_x2(swap_x2(x.b[e]), s[P + e]));
+        for (int e = 0; e < P; ++e) x.b[e] = vfma(x.b[e], c[P + e], vmul(swap_x2(x.b[e]), s[P + e]));
       }
     } else if (k.ra) {
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) {
-        const uint64_t u = x.a[e], v = x.b[e];
+        const X2 u = x.a[e], v = x.b[e];
         if constexpr (BACK) {
-          x.a[e] = fma_x2(u, c[e], mul_x2(v, s[e]));
-          x.b[e] = sub_x2(mul_x2(v, c[e]), mul_x2(u, s[e]));
+          x.a[e] = vfma(u, c[e], vmul(v, s[e]));
+          x.b[e] = vnfma(u, s[e], vmul(v, c[e]));
         } else {
-          x.a[e] = sub_x2(mul_x2(u, c[e]), mul_x2(v, s[e]));
-          x.b[e] = fma_x2(v, c[e], mul_x2(u, s[e]));
+          x.a[e] = vnfma(v, s[e], vmul(u, c[e]));
+          x.b[e] = vfma(v, c[e], vmul(u, s[e]));
         }
       }
     }
@@ -238,8 +254,8 @@ __device__ __forceinline__ void load_weights(const void* w, int w32, const Slot&
 #pragma unroll
   for (int e = 0; e < V / 2; ++e) {
     const int a = k.ca * V + 2 * e, b = k.cb * V + 2 * e;
-    f.a[e] = k.ca >= 0 ? pk(load_w<ACT>(w, w32, a), load_w<ACT>(w, w32, a + 1)) : 0ull;
-    f.b[e] = k.cb >= 0 ? pk(load_w<ACT>(w, w32, b), load_w<ACT>(w, w32, b + 1)) : 0ull;
+    f.a[e] = k.ca >= 0 ? x2(load_w<ACT>(w, w32, a), load_w<ACT>(w, w32, a + 1)) : X2{0.f, 0.f};
+    f.b[e] = k.cb >= 0 ? x2(load_w<ACT>(w, w32, b), load_w<ACT>(w, w32, b + 1)) : X2{0.f, 0.f};
   }
 }
 
@@ -259,9 +275,17 @@ __device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_g
 template <int N> __device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // the sum over a head's lanes of what each lane holds in packed pairs
-__device__ __forceinline__ float head_sum(uint64_t v, int lanes) {
-  const float2 f = unpk(v);
+__device__ __forceinline__ float head_sum(X2 v, int lanes) {
+  const float2 f = un2(v);
   return lanes_sum(__fadd_rn(f.x, f.y), lanes);
+}
+
+// What a token without a place in the table gets: zeros for padding, NaN past its end.
+__device__ __forceinline__ void store_bad(char* y, const Slot& k, int64_t pos) {
+  const uint32_t v = pos < 0 ? 0u : 0xffffffffu;  // all ones is a NaN in every type
+  const uint32_t w[4] = {v, v, v, v};
+  if (k.ca >= 0) store_bytes<16>(y + 16 * k.ca, w);
+  if (k.cb >= 0) store_bytes<16>(y + 16 * k.cb, w);
 }
 
 // A warp's walk over its items: `groups` neighbouring heads a step (one for each group of
@@ -291,7 +315,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const QkParams 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int L = 1 << p.log_l, groups = 32 >> p.log_l, grp = lane >> p.log_l;
   const bool is_k = (int)blockIdx.x >= p.blocks_q;
-  const QkSeg& S = p.seg[is_k];
+  const QkSeg S = is_k ? p.seg[1] : p.seg[0];
   const int parts = p.parts_a_token[is_k], span = p.nb * groups, heads = S.heads;
   const int64_t items = p.tokens * parts;
   const int64_t stride = (int64_t)(is_k ? gridDim.x - p.blocks_q : p.blocks_q) * warps;
@@ -341,32 +365,33 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const QkParams 
    for (; at.h < at.end; at.h += groups, y += yh) {
     fetch(slot == 0 ? kQkSteps - 1 : slot - 1);
     async_wait<kQkSteps - 1>();
+    const bool here = at.h + grp < at.end;
+    if (!ok) {  // (the whole warp)
+      if (here) store_bad(y, k, pos);
+      if (++slot == kQkSteps) slot = 0;
+      continue;
+    }
     Pair2<V> x;
     widen2x<ACT, V>(take_chunk(mine + slot * 1024), x.a);
     widen2x<ACT, V>(take_chunk(mine + slot * 1024 + 512), x.b);
     if constexpr (NORM) {
-      uint64_t ss = 0ull, st = 0ull;
+      X2 ss = X2{0.f, 0.f}, st = X2{0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) {
-        ss = fma_x2(x.a[e], x.a[e], ss);
-        st = fma_x2(x.b[e], x.b[e], st);
+        ss = vfma(x.a[e], x.a[e], ss);
+        st = vfma(x.b[e], x.b[e], st);
       }
-      const float r = head_rstd(head_sum(add_x2(ss, st), L), p);
-      const uint64_t r2 = pk(r, r);
+      const float r = head_rstd(head_sum(vadd(ss, st), L), p);
+      const X2 r2 = x2(r, r);
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) {
-        x.a[e] = mul_x2(mul_x2(x.a[e], r2), w.a[e]);
-        x.b[e] = mul_x2(mul_x2(x.b[e], r2), w.b[e]);
+        x.a[e] = vmul(vmul(x.a[e], r2), w.a[e]);
+        x.b[e] = vmul(vmul(x.b[e], r2), w.b[e]);
       }
     }
     if (!NORM && p.sign < 0.f) turn.template apply<true>(x, k);
     else turn.template apply<false>(x, k);
-    if (!ok) {
-      const float v = pos < 0 ? 0.f : __uint_as_float(0x7fffffffu);
-#pragma unroll
-      for (int e = 0; e < V / 2; ++e) x.a[e] = x.b[e] = pk(v, v);
-    }
-    if (at.h + grp < at.end) {
+    if (here) {
       store_chunk<ACT, V>(y, k.ca, x.a);
       store_chunk<ACT, V>(y, k.cb, x.b);
     }
@@ -382,7 +407,7 @@ __device__ __forceinline__ void write_part(float* part, float* sm, const Slot& k
   float da[V], db[V];
 #pragma unroll
   for (int e = 0; e < V / 2; ++e) {
-    const float2 u = unpk(d.a[e]), v = unpk(d.b[e]);
+    const float2 u = un2(d.a[e]), v = un2(d.b[e]);
     da[2 * e] = u.x;
     da[2 * e + 1] = u.y;
     db[2 * e] = v.x;
@@ -419,7 +444,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_back_kernel(const QkPa
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int L = 1 << p.log_l, groups = 32 >> p.log_l, grp = lane >> p.log_l;
   const bool is_k = (int)blockIdx.x >= p.blocks_q;
-  const QkSeg& S = p.seg[is_k];
+  const QkSeg S = is_k ? p.seg[1] : p.seg[0];
   const int parts = p.parts_a_token[is_k], span = p.nb * groups, heads = S.heads;
   const int64_t items = p.tokens * parts;
   const int64_t stride = (int64_t)(is_k ? gridDim.x - p.blocks_q : p.blocks_q) * warps;
@@ -465,7 +490,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_back_kernel(const QkPa
   Pair2<V> w, dw;
   load_weights<ACT, V>(S.w, p.w32, k, w);
 #pragma unroll
-  for (int e = 0; e < V / 2; ++e) dw.a[e] = dw.b[e] = 0ull;
+  for (int e = 0; e < V / 2; ++e) dw.a[e] = dw.b[e] = X2{0.f, 0.f};
   Turn<INTER, V> turn;
   int slot = 0;
   for (; !at.done(items); at.item += stride) {
@@ -478,48 +503,48 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_back_kernel(const QkPa
    for (; at.h < at.end; at.h += groups, y += yh) {
     fetch(slot == 0 ? kQkBackSteps - 1 : slot - 1);
     async_wait<kQkBackSteps - 1>();
+    const bool here = at.h + grp < at.end;
+    if (!ok) {
+      if (here) store_bad(y, k, pos);
+      if (++slot == kQkBackSteps) slot = 0;
+      continue;
+    }
     Pair2<V> x, g;
     widen2x<ACT, V>(take_chunk(mine + slot * 2048), x.a);
     widen2x<ACT, V>(take_chunk(mine + slot * 2048 + 512), x.b);
     widen2x<ACT, V>(take_chunk(mine + slot * 2048 + 1024), g.a);
     widen2x<ACT, V>(take_chunk(mine + slot * 2048 + 1536), g.b);
-    uint64_t ss = 0ull, st = 0ull;
+    X2 ss = X2{0.f, 0.f}, st = X2{0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) {
-      ss = fma_x2(x.a[e], x.a[e], ss);
-      st = fma_x2(x.b[e], x.b[e], st);
+      ss = vfma(x.a[e], x.a[e], ss);
+      st = vfma(x.b[e], x.b[e], st);
     }
-    const float r = head_rstd(head_sum(add_x2(ss, st), L), p);
-    const uint64_t r2 = pk(r, r);
+    const float r = head_rstd(head_sum(vadd(ss, st), L), p);
+    const X2 r2 = x2(r, r);
     turn.template apply<true>(g, k);
-    const bool here = ok && at.h + grp < at.end;
-    ss = st = 0ull;
+    ss = st = X2{0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) {
-      x.a[e] = mul_x2(x.a[e], r2);  // u = x r
-      x.b[e] = mul_x2(x.b[e], r2);
+      x.a[e] = vmul(x.a[e], r2);  // u = x r
+      x.b[e] = vmul(x.b[e], r2);
       if (here) {
-        dw.a[e] = fma_x2(g.a[e], x.a[e], dw.a[e]);
-        dw.b[e] = fma_x2(g.b[e], x.b[e], dw.b[e]);
+        dw.a[e] = vfma(g.a[e], x.a[e], dw.a[e]);
+        dw.b[e] = vfma(g.b[e], x.b[e], dw.b[e]);
       }
-      g.a[e] = mul_x2(g.a[e], w.a[e]);  // h = g w
-      g.b[e] = mul_x2(g.b[e], w.b[e]);
-      ss = fma_x2(g.a[e], x.a[e], ss);
-      st = fma_x2(g.b[e], x.b[e], st);
+      g.a[e] = vmul(g.a[e], w.a[e]);  // h = g w
+      g.b[e] = vmul(g.b[e], w.b[e]);
+      ss = vfma(g.a[e], x.a[e], ss);
+      st = vfma(g.b[e], x.b[e], st);
     }
-    const float m = -__fmul_rn(head_sum(add_x2(ss, st), L), p.inv_dim);
-    const uint64_t m2 = pk(m, m);
+    const float m = -__fmul_rn(head_sum(vadd(ss, st), L), p.inv_dim);
+    const X2 m2 = x2(m, m);
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) {
-      x.a[e] = mul_x2(r2, fma_x2(x.a[e], m2, g.a[e]));
-      x.b[e] = mul_x2(r2, fma_x2(x.b[e], m2, g.b[e]));
+      x.a[e] = vmul(r2, vfma(x.a[e], m2, g.a[e]));
+      x.b[e] = vmul(r2, vfma(x.b[e], m2, g.b[e]));
     }
-    if (!ok) {
-      const float v = pos < 0 ? 0.f : __uint_as_float(0x7fffffffu);
-#pragma unroll
-      for (int e = 0; e < V / 2; ++e) x.a[e] = x.b[e] = pk(v, v);
-    }
-    if (at.h + grp < at.end) {
+    if (here) {
       store_chunk<ACT, V>(y, k.ca, x.a);
       store_chunk<ACT, V>(y, k.cb, x.b);
     }
@@ -645,29 +670,28 @@ __global__ void __launch_bounds__(kQkThreads) qk_any_kernel(const QkParams p, in
   }
 }
 
-// The partial rows summed in a fixed order, in binary64: block (32 columns x 32 row lanes),
-// blockIdx.y = 0 the queries' weight, 1 the keys'.
+// The partial rows summed in a fixed order (every 32nd row by a lane of rows, then the lanes by
+// halves): block (32 columns x 32 row lanes), blockIdx.y = 0 the queries' weight, 1 the keys'.
 __global__ void __launch_bounds__(1024)
     qk_weight_grad_kernel(const float* parts, int D, int rows_q, int rows_k, float* dq_weight, float* dk_weight) {
-  __shared__ double sm[32][33];
+  __shared__ float sm[32][33];
   pdl_launch_dependents();
   pdl_wait();
   const int col = blockIdx.x * 32 + threadIdx.x;
   const int rows = blockIdx.y ? rows_k : rows_q;
   const float* base = parts + (blockIdx.y ? (int64_t)rows_q * D : 0);
   float* out = blockIdx.y ? dk_weight : dq_weight;
-  double v = 0.0;
+  float v = 0.f;
   if (col < D) {
 #pragma unroll 8
-    for (int r = threadIdx.y; r < rows; r += 32) v += (double)base[(int64_t)r * D + col];
+    for (int r = threadIdx.y; r < rows; r += 32) v = __fadd_rn(v, base[(int64_t)r * D + col]);
   }
   sm[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
-  if (threadIdx.y == 0 && col < D && out) {
-    double t = 0.0;
-    for (int i = 0; i < 32; ++i) t += sm[i][threadIdx.x];
-    out[col] = (float)t;
-  }
+  // turned: a warp adds the 32 row lanes of one column
+  const float t = lanes_sum(sm[threadIdx.x][threadIdx.y], 32);
+  const int c = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && c < D && out) out[c] = t;
 }
 
 struct Freqs {

@@ -306,14 +306,17 @@ struct Walk {
   }
 };
 
-template <int ACT, bool INTER, bool NORM>
+template <int ACT, bool INTER, bool NORM, int LOGL>
 __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const QkParams p) {
   constexpr int V = 16 / dtype_size<ACT>::value;
   extern __shared__ __align__(16) unsigned char ring[];  // [warps][kQkSteps][2][32 lanes] chunks
   pdl_launch_dependents();
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int L = 1 << p.log_l, groups = 32 >> p.log_l, grp = lane >> p.log_l;
+  // (broadcast, so that the compiler keeps the warp's walk in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int log_l = LOGL >= 0 ? LOGL : p.log_l;
+  const int L = 1 << log_l, groups = 32 >> log_l, grp = lane >> log_l;
   const bool is_k = (int)blockIdx.x >= p.blocks_q;
   const QkSeg S = is_k ? p.seg[1] : p.seg[0];
   const int parts = p.parts_a_token[is_k], span = p.nb * groups, heads = S.heads;
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const QkParams 
   const int64_t stride = (int64_t)(is_k ? gridDim.x - p.blocks_q : p.blocks_q) * warps;
   const Slot k = slot_of<INTER>(lane & (L - 1), p.D / V, p.rot / V);
   const uint32_t mine = smem_addr(ring) + warp * (kQkSteps * 1024) + lane * 16;
-  const int oa = 16 * max(k.ca, 0), ob = 16 * max(k.cb, 0);
+  const int64_t oa = grp * S.xh + 16 * max(k.ca, 0), ob = grp * S.xh + 16 * max(k.cb, 0);  // this lane's places
   if (k.ca < 0 || k.cb < 0)  // chunks that never arrive add nothing to their head
     for (int i = 0; i < 2 * kQkSteps; ++i) clear_chunk(mine + 512 * i);
   Walk in{(int64_t)(is_k ? (int)blockIdx.x - p.blocks_q : (int)blockIdx.x) * warps + warp, 0, 0, 0};
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const QkParams 
   const char* src = nullptr;
   auto aim = [&]() {
     in.start(parts, span, heads);
-    src = S.x + in.t * S.xt + (int64_t)(in.h + grp) * S.xh;
+    src = S.x + in.t * S.xt + (int64_t)in.h * S.xh;
   };
   if (!in.done(items)) aim();
   const int64_t xh = groups * S.xh, yh = groups * S.yh;
@@ -435,14 +438,17 @@ __device__ __forceinline__ void write_part(float* part, float* sm, const Slot& k
   }
 }
 
-template <int ACT, bool INTER>
+template <int ACT, bool INTER, int LOGL>
 __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_back_kernel(const QkParams p) {
   constexpr int V = 16 / dtype_size<ACT>::value;
   extern __shared__ __align__(16) unsigned char ring[];  // [warps][kQkBackSteps][x, x, dy, dy][32 lanes] chunks
   pdl_launch_dependents();
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int L = 1 << p.log_l, groups = 32 >> p.log_l, grp = lane >> p.log_l;
+  // (broadcast, so that the compiler keeps the warp's walk in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int log_l = LOGL >= 0 ? LOGL : p.log_l;
+  const int L = 1 << log_l, groups = 32 >> log_l, grp = lane >> log_l;
   const bool is_k = (int)blockIdx.x >= p.blocks_q;
   const QkSeg S = is_k ? p.seg[1] : p.seg[0];
   const int parts = p.parts_a_token[is_k], span = p.nb * groups, heads = S.heads;
@@ -450,7 +456,8 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_back_kernel(const QkPa
   const int64_t stride = (int64_t)(is_k ? gridDim.x - p.blocks_q : p.blocks_q) * warps;
   const Slot k = slot_of<INTER>(lane & (L - 1), p.D / V, p.rot / V);
   const uint32_t mine = smem_addr(ring) + warp * (kQkBackSteps * 2048) + lane * 16;
-  const int oa = 16 * max(k.ca, 0), ob = 16 * max(k.cb, 0);
+  const int64_t oa = grp * S.xh + 16 * max(k.ca, 0), ob = grp * S.xh + 16 * max(k.cb, 0);
+  const int64_t ga = grp * S.gh + 16 * max(k.ca, 0), gb = grp * S.gh + 16 * max(k.cb, 0);
   if (k.ca < 0 || k.cb < 0)
     for (int i = 0; i < 4 * kQkBackSteps; ++i) clear_chunk(mine + 512 * i);
   Walk in{(int64_t)(is_k ? (int)blockIdx.x - p.blocks_q : (int)blockIdx.x) * warps + warp, 0, 0, 0};
@@ -458,8 +465,8 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_back_kernel(const QkPa
   const char *src = nullptr, *grad = nullptr;
   auto aim = [&]() {
     in.start(parts, span, heads);
-    src = S.x + in.t * S.xt + (int64_t)(in.h + grp) * S.xh;
-    grad = S.g + in.t * S.gt + (int64_t)(in.h + grp) * S.gh;
+    src = S.x + in.t * S.xt + (int64_t)in.h * S.xh;
+    grad = S.g + in.t * S.gt + (int64_t)in.h * S.gh;
   };
   if (!in.done(items)) aim();
   const int64_t xh = groups * S.xh, gh = groups * S.gh, yh = groups * S.yh;
@@ -468,11 +475,11 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_back_kernel(const QkPa
       if (in.h + grp < in.end) {
         if (k.ca >= 0) {
           async_chunk(mine + slot * 2048, src + oa);
-          async_chunk(mine + slot * 2048 + 1024, grad + oa);
+          async_chunk(mine + slot * 2048 + 1024, grad + ga);
         }
         if (k.cb >= 0) {
           async_chunk(mine + slot * 2048 + 512, src + ob);
-          async_chunk(mine + slot * 2048 + 1536, grad + ob);
+          async_chunk(mine + slot * 2048 + 1536, grad + gb);
         }
       }
       src += xh;
@@ -909,6 +916,14 @@ QkPlan plan_qk(const QkCall& c, int sms) {
   return g;
 }
 
+template <int ACT, int LOGL>
+auto pick_qk(const QkCall& c) -> void (*)(QkParams) {
+  const bool inter = c.pairs == FAR_PAIRS_INTERLEAVED;
+  if (c.back) return inter ? qk_back_kernel<ACT, true, LOGL> : qk_back_kernel<ACT, false, LOGL>;
+  if (c.norm) return inter ? qk_kernel<ACT, true, true, LOGL> : qk_kernel<ACT, false, true, LOGL>;
+  return inter ? qk_kernel<ACT, true, false, LOGL> : qk_kernel<ACT, false, false, LOGL>;
+}
+
 template <int ACT>
 cudaError_t launch_qk(const QkCall& c, const QkPlan& g, const QkParams& p, cudaStream_t s) {
   const int inter = c.pairs == FAR_PAIRS_INTERLEAVED, norm = c.norm;
@@ -919,10 +934,11 @@ cudaError_t launch_qk(const QkCall& c, const QkPlan& g, const QkParams& p, cudaS
     }
     return launch_k(qk_any_kernel<ACT, false>, g.grid, g.block, g.smem, s, p, inter, norm);
   }
-  void (*k)(QkParams);
-  if (c.back) k = inter ? qk_back_kernel<ACT, true> : qk_back_kernel<ACT, false>;
-  else if (c.norm) k = inter ? qk_kernel<ACT, true, true> : qk_kernel<ACT, false, true>;
-  else k = inter ? qk_kernel<ACT, true, false> : qk_kernel<ACT, false, false>;
+  // the sums over a head's lanes are unrolled for the usual head sizes (64, 128 and 256 in 16 bits)
+  void (*k)(QkParams) = g.log_l == 2   ? pick_qk<ACT, 2>(c)
+                        : g.log_l == 3 ? pick_qk<ACT, 3>(c)
+                        : g.log_l == 4 ? pick_qk<ACT, 4>(c)
+                                       : pick_qk<ACT, -1>(c);
   return launch_k(k, g.grid, g.block, g.smem, s, p);
 }
 

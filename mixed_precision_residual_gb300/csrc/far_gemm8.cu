@@ -180,51 +180,15 @@ __device__ __forceinline__ bool fill_scales(float* ring, uint32_t full0, uint32_
   return true;
 }
 
-// 32 neighbouring outputs of one row
-__device__ __forceinline__ void store_row32(const Gemm8Params& p, int64_t row, int64_t col, const float* v) {
-  if (row >= p.M || col >= p.N) return;
-  if (col + 32 <= p.N && p.out_align >= 16) {
-    uint32_t w[32];
-    int words;
-    if (p.out_dtype == FAR_F32) {
-      narrow<FAR_F32, 32>(v, w);
-      words = 32;
-    } else {
-      if (p.out_dtype == FAR_F16) narrow<FAR_F16, 32>(v, w);
-      else narrow<FAR_BF16, 32>(v, w);
-      words = 16;
-    }
-    char* o = static_cast<char*>(p.out) + (row * p.ldo + col) * (p.out_dtype == FAR_F32 ? 4 : 2);
-    if (p.out_align >= 32) {
-      // a whole 32-byte sector a lane and instruction
-#pragma unroll
-      for (int i = 0; i < 32; i += 8)
-        if (i < words)
-          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + 4 * i), "r"(w[i]),
-                       "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
-                       "r"(w[i + 7])
-                       : "memory");
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; i += 4)
-        if (i < words) *reinterpret_cast<uint4*>(o + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (col + i < p.N) store_out(p, row, col + i, v[i]);
-  }
-}
-
 // ---------------------------------------------------------------------------
 // pair_kernel: 256 x 256 output tiles over a cluster of 2.  Each CTA holds its 128 rows of x
 // and half of the tile's rows of wt (up to 128) per block of k; one thread of the even CTA issues
 // tcgen05.mma.cta_group::2 over both, each CTA's TMEM receiving the sums of its 128 rows.
 //   warp 0      TMA producer (both CTAs), a ring of kPairStages blocks of k running across tiles
 //   warp 1      MMA issuer (even CTA); allocates TMEM: two halves of 256 columns
-//   warp 2      column scales (wt scaled by rows)
+//   warps 2, 3  where wt is scaled by rows: column and row factors, some blocks of k ahead
 //   warps 4-11  epilogue: warp w the TMEM lanes 32 (w % 4) .., columns 128 ((w - 4) / 4) ..; a
-//               thread keeps 128 outputs of one row in registers
+//               thread keeps 128 outputs in registers
 // The registers a thread: 384 threads are launched at 168; warps 0-3 give theirs up to 72 and
 // the epilogue's take 216 (128 x 72 + 256 x 216 = 384 x 168).
 // The last column of tiles runs at the width that is left (a multiple of 32).
@@ -235,7 +199,12 @@ constexpr uint32_t kPairABytes = 128 * kBlock, kPairBBytes = 128 * kBlock;
 constexpr uint32_t kPairRing = kPairStages * (kPairABytes + kPairBBytes);
 constexpr int kPairBars = 2 * kPairStages + 4 + 2 * kScaleSlots;
 constexpr uint32_t kPairOut = 8 * 4096;  // a box of 32 rows x 128 bytes of outputs an epilogue warp
-constexpr size_t kPairSmem = kPairRing + kPairOut + kScaleSlots * 256 * 4 + kPairBars * 8 + 16 + 1024;
+// A slot of the scale ring (wt scaled by rows): the 128 rows' factors, then for each half of the
+// columns 4 groups of 32 column factors, 36 apart (a fragment's thread reads one group, and
+// the four groups lie on different banks).
+constexpr int kRowFactors = 128, kColGroup = 36, kSlotFloats = kRowFactors + 2 * 4 * kColGroup;
+constexpr uint32_t kPairScales = kScaleSlots * kSlotFloats * 4;
+constexpr size_t kPairSmem = kPairRing + kPairOut + kPairScales + kPairBars * 8 + 16 + 1024;
 constexpr int kPairGroup = 8;  // tile rows that are walked together, so that CTAs at work share panels in L2
 
 struct PairTile {
@@ -263,7 +232,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t sbase = smem_addr(smem);
   const uint32_t a_base = sbase, b_base = sbase + kPairStages * kPairABytes;
   float* scales = reinterpret_cast<float*>(smem + kPairRing + kPairOut);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kPairRing + kPairOut + kScaleSlots * 256 * 4);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kPairRing + kPairOut + kPairScales);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kPairBars);
   const uint32_t full0 = smem_addr(&bars[0]), empty0 = smem_addr(&bars[kPairStages]);
   const uint32_t acc_full0 = smem_addr(&bars[2 * kPairStages]), acc_empty0 = acc_full0 + 16;
@@ -283,7 +252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(acc_empty0 + 8 * a, 16);  // even CTA: 8 epilogue warps in each CTA
     }
     for (int s = 0; s < kScaleSlots; ++s) {
-      mbar_init(sc_full0 + 8 * s, 1);   // the scale warp
+      mbar_init(sc_full0 + 8 * s, 2);  // the two scale warps
       mbar_init(sc_empty0 + 8 * s, 8);  // this CTA's epilogue warps
     }
     fence_barrier_init();
@@ -362,10 +331,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
         }
       }
-    } else if (COLS && warp == 2) {
+    } else if (COLS && warp == 3) {
+      // ---------------- row factors ----------------
       uint32_t g = 0;
-      for (int t = pair; t < p.num_tiles; t += pairs, g += p.KB)
-        if (!fill_scales<256>(scales, sc_full0, sc_empty0, p.ws, pair_tile(p, t).col0, p.N, 0, p.KB, p.KB, g, lane, p)) break;
+      bool ok = true;
+      for (int t = pair; ok && t < p.num_tiles; t += pairs) {
+        const int64_t row0 = pair_tile(p, t).row0 + (int)rank * 128 + lane;
+        for (int kb = 0; ok && kb < p.KB; kb += 4) {
+          Scale4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i].load(row0 + 32 * i < p.M ? p.xs + (row0 + 32 * i) * p.KB : nullptr, kb, p.KB, p.xs_vec);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (kb + j >= p.KB) break;
+            const uint32_t slot = g % kScaleSlots;
+            if (!mbar_wait(sc_empty0 + 8 * slot, ((g / kScaleSlots) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+              ok = false;
+              break;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) scales[slot * kSlotFloats + lane + 32 * i] = x[i].v[j];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sc_full0 + 8 * slot);
+            ++g;
+          }
+        }
+      }
+    } else if (COLS && warp == 2) {
+      // ---------------- column factors: a lane's 4 neighbouring columns of either half ----------------
+      uint32_t g = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < p.num_tiles; t += pairs) {
+        const int64_t col0 = pair_tile(p, t).col0 + 4 * lane;
+        for (int kb = 0; ok && kb < p.KB; kb += 4) {
+          Scale4 x[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int64_t c = col0 + 128 * h + i;
+              x[h][i].load(c < p.N ? p.ws + c * p.KB : nullptr, kb, p.KB, p.ws_vec);
+            }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (kb + j >= p.KB) break;
+            const uint32_t slot = g % kScaleSlots;
+            if (!mbar_wait(sc_empty0 + 8 * slot, ((g / kScaleSlots) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+              ok = false;
+              break;
+            }
+            // column 4 lane + i: pair (4 lane + i) % 8 / 2 of the 8 columns number lane / 2
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float* dst = scales + slot * kSlotFloats + kRowFactors + h * 4 * kColGroup + 2 * (lane >> 1);
+#pragma unroll
+              for (int i = 0; i < 4; i += 2)
+                *reinterpret_cast<float2*>(dst + ((lane & 1) * 2 + i / 2) * kColGroup) = make_float2(x[h][i].v[j], x[h][i + 1].v[j]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sc_full0 + 8 * slot);
+            ++g;
+          }
+        }
+      }
     }
   } else {
     // ---------------- epilogue ----------------
@@ -376,104 +404,197 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     unsigned char* box = smem + kPairRing + (warp - 4) * 4096;
     uint32_t g = 0;
     bool ok = true;
-    for (int t = pair; ok && t < p.num_tiles; t += pairs) {
-      const PairTile w = pair_tile(p, t);
-      const int64_t row = w.row0 + (int)rank * 128 + quarter * 32 + lane;
-      const int64_t col = w.col0 + half * 128;
-      const int mine = w.cols - half * 128;  // columns of this half (may be none)
-      const float* xrow = row < p.M ? p.xs + row * p.KB : nullptr;
-      const float* wrow = !COLS && col < p.N ? p.ws + col / kBlock * p.KB : nullptr;
-      Scale4 xn, wn;
-      xn.load(xrow, 0, p.KB, p.xs_vec);
-      if constexpr (!COLS) wn.load(wrow, 0, p.KB, p.ws_vec);
-      float acc[128];
-#pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      for (int kb4 = 0; ok && kb4 < p.KB; kb4 += 4) {
-        Scale4 sc;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sc.v[j] = COLS ? xn.v[j] : __fmul_rn(xn.v[j], wn.v[j]);
-        xn.load(xrow, kb4 + 4, p.KB, p.xs_vec);  // the next four blocks', while these are worked on
-        if constexpr (!COLS) wn.load(wrow, kb4 + 4, p.KB, p.ws_vec);
-#pragma unroll 1
-        for (int j = 0; j < 4 && kb4 + j < p.KB; ++j, ++g) {
+    if constexpr (COLS) {
+      // A thread keeps rows t, t + 8, t + 16, t + 24 of its warp's 32 (t = lane / 4) and the columns
+      // 8 i + 2 q, 8 i + 2 q + 1 (q = lane % 4) of its half: 4 row factors and 32 column factors for
+      // its 128 outputs.  (A row a thread instead takes 128 column factors a block from shared
+      // memory, whose bandwidth the MMA's operands already fill: scaled by rows on both sides,
+      // 8192^3 then took 799 us.)
+      const int t4 = lane >> 2, q = lane & 3;
+      const float* row_factors = scales + quarter * 32 + t4;
+      const float* col_factors = scales + kRowFactors + (half * 4 + q) * kColGroup;
+      for (int t = pair; ok && t < p.num_tiles; t += pairs) {
+        const PairTile w = pair_tile(p, t);
+        const int64_t row = w.row0 + (int)rank * 128 + quarter * 32;  // the warp's first
+        const int64_t col = w.col0 + half * 128;
+        const int mine = w.cols - half * 128;  // columns of this half (may be none)
+        float acc[128];
+  #pragma unroll
+        for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+  #pragma unroll 1
+        for (int kb = 0; kb < p.KB; ++kb, ++g) {
           const uint32_t buf = g & 1u, slot = g % kScaleSlots;
-          const float sr = sc.at(j);
-          if (!mbar_wait(acc_full0 + 8 * buf, (g >> 1) & 1u, p.timeout_ns, p.status) ||
-              (COLS && !mbar_wait(sc_full0 + 8 * slot, (g / kScaleSlots) & 1u, p.timeout_ns, p.status))) {
+          if (!mbar_wait(sc_full0 + 8 * slot, (g / kScaleSlots) & 1u, p.timeout_ns, p.status)) {
+            ok = false;
+            break;
+          }
+          const float* rf = row_factors + slot * kSlotFloats;
+          float sr[4];
+  #pragma unroll
+          for (int u = 0; u < 4; ++u) sr[u] = rf[8 * u];
+          if (!mbar_wait(acc_full0 + 8 * buf, (g >> 1) & 1u, p.timeout_ns, p.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const float4* cs = reinterpret_cast<const float4*>(scales + slot * 256 + half * 128);
+          const float4* cf = reinterpret_cast<const float4*>(col_factors + slot * kSlotFloats);
           // All 128 columns always: those past a narrow tile's hold what nobody stores.  (The
           // other warp of this SM quarter adds while this one loads.)
-#pragma unroll
+  #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t r[32];
-            tmem_ld32_sync(lanes + buf * 256 + 32 * c, r);
+            tmem_ld_frag_sync(lanes + buf * 256 + 32 * c, r);
             if (c == 3) {  // all read: this warp's share of the buffer is free
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
             }
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              float4 q;
-              if constexpr (COLS) q = cs[8 * c + i / 4];
-              else q = make_float4(1.f, 1.f, 1.f, 1.f);
-              float* a = &acc[32 * c + i];
-              const float v0 = __uint_as_float(r[i]), v1 = __uint_as_float(r[i + 1]), v2 = __uint_as_float(r[i + 2]),
-                          v3 = __uint_as_float(r[i + 3]);
-              a[0] = __fmaf_rn(COLS ? __fmul_rn(v0, q.x) : v0, sr, a[0]);
-              a[1] = __fmaf_rn(COLS ? __fmul_rn(v1, q.y) : v1, sr, a[1]);
-              a[2] = __fmaf_rn(COLS ? __fmul_rn(v2, q.z) : v2, sr, a[2]);
-              a[3] = __fmaf_rn(COLS ? __fmul_rn(v3, q.w) : v3, sr, a[3]);
+  #pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const float4 f = cf[2 * c + i / 2];
+  #pragma unroll
+              for (int u = 0; u < 4; ++u) {  // row t + 8 u
+                const int o = 16 * (u >> 1) + 2 * (u & 1) + 4 * i;
+                float* a = &acc[32 * c + o];
+                const float v0 = __uint_as_float(r[o]), v1 = __uint_as_float(r[o + 1]), v2 = __uint_as_float(r[o + 4]),
+                            v3 = __uint_as_float(r[o + 5]);
+                a[0] = __fmaf_rn(__fmul_rn(v0, f.x), sr[u], a[0]);
+                a[1] = __fmaf_rn(__fmul_rn(v1, f.y), sr[u], a[1]);
+                a[4] = __fmaf_rn(__fmul_rn(v2, f.z), sr[u], a[4]);
+                a[5] = __fmaf_rn(__fmul_rn(v3, f.w), sr[u], a[5]);
+              }
             }
           }
-          if constexpr (COLS) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sc_empty0 + 8 * slot);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sc_empty0 + 8 * slot);
+        }
+        if (!ok) break;
+        if (p.out_align >= 16) {
+          // through shared memory in boxes of 32 rows x 128 bytes (128-byte swizzle), copied out by TMA
+          // while the next tile's blocks arrive; the copy leaves out what lies past the edges
+          const bool f32 = p.out_dtype == FAR_F32;
+  #pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (mine <= 32 * c) break;
+            if (f32 || (c & 1) == 0) {  // a new box: the copy of the last one has read it
+              if (lane == 0) bulk_wait_read();
+              __syncwarp();
+            }
+  #pragma unroll
+            for (int i = 0; i < 4; ++i)
+  #pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float* a = &acc[32 * c + 16 * (u >> 1) + 2 * (u & 1) + 4 * i];
+                unsigned char* line = box + (t4 + 8 * u) * 128;  // row t4 + 8 u: its units are permuted by t4
+                if (f32) {
+                  *reinterpret_cast<float2*>(line + (((2 * i + (q >> 1)) ^ t4) * 16) + (q & 1) * 8) = make_float2(a[0], a[1]);
+                } else {
+                  const uint32_t v = p.out_dtype == FAR_F16 ? narrow2<FAR_F16>(a[0], a[1]) : narrow2<FAR_BF16>(a[0], a[1]);
+                  *reinterpret_cast<uint32_t*>(line + (((4 * (c & 1) + i) ^ t4) * 16) + q * 4) = v;
+                }
+              }
+            if (f32 || (c & 1) == 1 || mine <= 32 * (c + 1)) {
+              fence_async_shared();
+              __syncwarp();
+              const int64_t x = col + (f32 ? 32 * c : 64 * (c / 2));
+              if (lane == 0 && x < p.N && row < p.M) {
+                tma_store_2d(&map_out, smem_addr(box), (int)x, (int)row);
+                bulk_commit();
+              }
+            }
+          }
+        } else {
+  #pragma unroll
+          for (int i = 0; i < 128; ++i) {
+            const int64_t m = row + t4 + 8 * (((i >> 4) & 1) * 2 + ((i >> 1) & 1)), n = col + 32 * (i >> 5) + 8 * ((i >> 2) & 3) + 2 * q + (i & 1);
+            if (m < p.M && n < p.N) store_out(p, m, n, acc[i]);
           }
         }
       }
-      if (!ok) break;
-      if (p.out_align >= 16) {
-        // through shared memory in boxes of 32 rows x 128 bytes (128-byte swizzle), copied out by TMA
-        // while the next tile's blocks arrive; the copy leaves out what lies past the edges
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (mine <= 32 * c) break;
-          const bool f32 = p.out_dtype == FAR_F32;
-          if (f32 || (c & 1) == 0) {  // a new box: the copy of the last one has read it
-            if (lane == 0) bulk_wait_read();
-            __syncwarp();
-          }
-          uint32_t v[32];
-          if (f32) narrow<FAR_F32, 32>(acc + 32 * c, v);
-          else if (p.out_dtype == FAR_F16) narrow<FAR_F16, 32>(acc + 32 * c, v);
-          else narrow<FAR_BF16, 32>(acc + 32 * c, v);
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            if (u < 4 || f32) {
-              const int unit = (f32 || (c & 1) == 0 ? u : u + 4) ^ (lane & 7);
-              *reinterpret_cast<uint4*>(box + lane * 128 + unit * 16) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+    } else {
+      // Scaled by tiles: a thread keeps one row's 128 columns, its factors (xs times ws) in registers.
+      for (int t = pair; ok && t < p.num_tiles; t += pairs) {
+        const PairTile w = pair_tile(p, t);
+        const int64_t row = w.row0 + (int)rank * 128 + quarter * 32 + lane;
+        const int64_t col = w.col0 + half * 128;
+        const int mine = w.cols - half * 128;  // columns of this half (may be none)
+        const float* xrow = row < p.M ? p.xs + row * p.KB : nullptr;
+        const float* wrow = col < p.N ? p.ws + col / kBlock * p.KB : nullptr;
+        Scale4 xn, wn;
+        xn.load(xrow, 0, p.KB, p.xs_vec);
+        wn.load(wrow, 0, p.KB, p.ws_vec);
+        float acc[128];
+  #pragma unroll
+        for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+        for (int kb4 = 0; ok && kb4 < p.KB; kb4 += 4) {
+          Scale4 sc;
+  #pragma unroll
+          for (int j = 0; j < 4; ++j) sc.v[j] = __fmul_rn(xn.v[j], wn.v[j]);
+          xn.load(xrow, kb4 + 4, p.KB, p.xs_vec);  // the next four blocks', while these are worked on
+          wn.load(wrow, kb4 + 4, p.KB, p.ws_vec);
+  #pragma unroll 1
+          for (int j = 0; j < 4 && kb4 + j < p.KB; ++j, ++g) {
+            const uint32_t buf = g & 1u;
+            const float sr = sc.at(j);
+            if (!mbar_wait(acc_full0 + 8 * buf, (g >> 1) & 1u, p.timeout_ns, p.status)) {
+              ok = false;
+              break;
             }
-          }
-          if (f32 || (c & 1) == 1 || mine <= 32 * (c + 1)) {
-            fence_async_shared();
-            __syncwarp();
-            const int64_t x = col + (f32 ? 32 * c : 64 * (c / 2)), y = row - lane;
-            if (lane == 0 && x < p.N && y < p.M) {
-              tma_store_2d(&map_out, smem_addr(box), (int)x, (int)y);
-              bulk_commit();
+            tc_fence_after();
+            // All 128 columns always: those past a narrow tile's hold what nobody stores.  (The
+            // other warp of this SM quarter adds while this one loads.)
+  #pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t r[32];
+              tmem_ld32_sync(lanes + buf * 256 + 32 * c, r);
+              if (c == 3) {  // all read: this warp's share of the buffer is free
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
+              }
+  #pragma unroll
+              for (int i = 0; i < 32; ++i) acc[32 * c + i] = __fmaf_rn(__uint_as_float(r[i]), sr, acc[32 * c + i]);
             }
           }
         }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (mine > 32 * c) store_row32(p, row, col + 32 * c, acc + 32 * c);
+        if (!ok) break;
+        if (p.out_align >= 16) {
+          // through shared memory in boxes of 32 rows x 128 bytes (128-byte swizzle), copied out by TMA
+          // while the next tile's blocks arrive; the copy leaves out what lies past the edges
+  #pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (mine <= 32 * c) break;
+            const bool f32 = p.out_dtype == FAR_F32;
+            if (f32 || (c & 1) == 0) {  // a new box: the copy of the last one has read it
+              if (lane == 0) bulk_wait_read();
+              __syncwarp();
+            }
+            uint32_t v[32];
+            if (f32) narrow<FAR_F32, 32>(acc + 32 * c, v);
+            else if (p.out_dtype == FAR_F16) narrow<FAR_F16, 32>(acc + 32 * c, v);
+            else narrow<FAR_BF16, 32>(acc + 32 * c, v);
+  #pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              if (u < 4 || f32) {
+                const int unit = (f32 || (c & 1) == 0 ? u : u + 4) ^ (lane & 7);
+                *reinterpret_cast<uint4*>(box + lane * 128 + unit * 16) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+              }
+            }
+            if (f32 || (c & 1) == 1 || mine <= 32 * (c + 1)) {
+              fence_async_shared();
+              __syncwarp();
+              const int64_t x = col + (f32 ? 32 * c : 64 * (c / 2)), y = row - lane;
+              if (lane == 0 && x < p.N && y < p.M) {
+                tma_store_2d(&map_out, smem_addr(box), (int)x, (int)y);
+                bulk_commit();
+              }
+            }
+          }
+        } else {
+  #pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (row < p.M && col + i < p.N) store_out(p, row, col + i, acc[i]);
+        }
       }
     }
     if (lane == 0) bulk_wait_all();

@@ -9,7 +9,7 @@
 // block in the other half of TMEM; the register tile is what limits the tile's size.
 //
 // pair_kernel  -- many rows: 256 x 256 tiles over CTA pairs, x's rows on the TMEM lanes.
-// small_kernel -- few rows (a decode batch): wt's rows on the lanes, 16 to 128 rows of x as the
+// small_kernel -- few rows (a decode batch): wt's rows on the lanes, 16 to 64 rows of x as the
 //                 columns, k split over a cluster of CTAs that add their sums through
 //                 distributed shared memory.  Bound by reading wt once.
 // plain_kernel -- any shape, stride and alignment: 64 x 64 tiles in binary32.
@@ -620,10 +620,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 constexpr int kSmallThreads = 256;
 template <int NT>
 struct SmallShape {
-  static constexpr int ctas = NT <= 64 ? 2 : 1;    // CTAs an SM
-  static constexpr int bufs = NT <= 64 ? 4 : 2;    // TMEM accumulators
+  static constexpr int ctas = 2;  // an SM
+  static constexpr int bufs = 4;  // TMEM accumulators
   static constexpr uint32_t a_bytes = 128 * kBlock, b_bytes = NT * kBlock;
-  static constexpr int stages = NT == 16 ? 5 : NT == 32 ? 5 : NT == 64 ? 4 : 6;
+  static constexpr int stages = NT == 64 ? 4 : 5;
   static constexpr uint32_t ring = stages * (a_bytes + b_bytes);
   static constexpr uint32_t tmem_cols = bufs * NT < 32 ? 32 : bufs * NT;
   static constexpr int bars = 2 * stages + 2 * bufs + 2 * kScaleSlots;
@@ -651,6 +651,11 @@ __global__ void __launch_bounds__(kSmallThreads, SmallShape<NT>::ctas)
   const int kb0 = (int)((int64_t)p.KB * rank / split), kb1 = (int)((int64_t)p.KB * (rank + 1) / split);
 
   pdl_launch_dependents();
+  // The ring's first load of wt starts for L2 while the CTA is set up and the kernel ahead drains
+  // (m = 4, 8192 x 8192: 13.2 us against 13.8; 2048 x 8192: 6.7 against 7.3; the CTA's whole
+  // share instead: 13.6, and 24.3 against 20.7 on 28672 x 4096).
+  if (warp == 3 && lane == 0)
+    for (int kb = kb0; kb < kb1 && kb < kb0 + S::stages; ++kb) tma_prefetch_2d(&map_w, kb * kBlock, (int)n0);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::stages; ++s) {
       mbar_init(full0 + 8 * s, 1);
@@ -879,19 +884,22 @@ Gemm8Plan plan_gemm8(const Gemm8Params& p, int sms) {
   const bool tma = p.K > 0 && p.ldx % 16 == 0 && p.ldw % 16 == 0 && (((uintptr_t)p.x | (uintptr_t)p.wt) & 15) == 0;
   if (!tma) return g;
   const int64_t tiles_n = ((int64_t)p.N + 127) / 128;
-  g.nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-  const int64_t tiles_m = ((int64_t)p.M + g.nt - 1) / g.nt;
-  const int64_t slots = (int64_t)sms * (g.nt <= 64 ? 2 : 1);
+  g.nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64;
+  const int64_t tiles_m = ((int64_t)p.M + g.nt - 1) / g.nt, slots = 2ll * sms;
+  // k is shared out while there are free places for it, not below two blocks a CTA
   g.split = 1;
   while (g.split < 8 && tiles_n * tiles_m * g.split * 2 <= slots && p.KB >= 4 * g.split) g.split *= 2;
   const int64_t pair_tiles = (((int64_t)p.M + 255) / 256) * (((int64_t)p.N + 255) / 256);
-  // estimated time, in cycles: a block of k takes the pair kernel 540, the small kernel about
-  // 2.8 a column and no less than its 16 KB of wt take to arrive
+  // Estimated microseconds, fitted to both kernels on 32 shapes (64 to 768 rows, 1536 x 1536 to 8192 x
+  // 8192): a launch, then waves of CTAs at so much a block of k.  The faster of the two is taken
+  // on all but 512 rows x 1536 x 1536 (11.3 against 10.3 us).  E.g. (pair / small) 128 x 8192 x
+  // 8192 31.3 / 27.0, 192 rows 31.4 / 44.1; 256 x 4096 x 4096 18.4 / 17.7, 384 rows 18.3 / 25.8.
   const int64_t waves = (tiles_n * tiles_m * g.split + slots - 1) / slots;
-  const double small = (double)waves * ((p.KB + g.split - 1) / g.split) * (g.nt == 128 ? 360.0 : 700.0) + 1000.0;
-  const double pair = (double)((pair_tiles + sms / 2 - 1) / (sms / 2)) * p.KB * 540.0 + 3000.0;
+  const double small = 5.0 + 0.7 * (double)waves * (double)((p.KB + g.split - 1) / g.split);
+  const int64_t pair_waves = (pair_tiles + sms / 2 - 1) / (sms / 2);
+  const double pair = 4.8 + (p.tile_scales ? 0.42 : 0.8) * (double)pair_waves * p.KB;
   const bool fits = tiles_n <= 65535 && tiles_m <= 65535;
-  g.kind = fits && (p.M <= 64 || small <= pair) ? 2 : 1;
+  g.kind = fits && small <= pair ? 2 : 1;
   if (g.kind == 1 && pair_tiles > INT32_MAX) g.kind = 0;
   return g;
 }
@@ -966,8 +974,7 @@ int run_gemm8(Gemm8Params& p, void* stream) {
     } else {
       e = g.nt == 16   ? launch_small<16>(mx, mw, p, g.split, s)
           : g.nt == 32 ? launch_small<32>(mx, mw, p, g.split, s)
-          : g.nt == 64 ? launch_small<64>(mx, mw, p, g.split, s)
-                       : launch_small<128>(mx, mw, p, g.split, s);
+                       : launch_small<64>(mx, mw, p, g.split, s);
     }
   }
   return e == cudaSuccess ? FAR_OK : cuda_error_status(e);

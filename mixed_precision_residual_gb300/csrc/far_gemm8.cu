@@ -40,7 +40,7 @@ struct Gemm8Params {
   int32_t M, N, K, KB;    // KB: blocks of 128 along k
   int32_t tile_scales;    // ws: one a 128 rows of wt (1) or one a row (0)
   int32_t out_dtype;
-  int32_t out_align;      // bytes that out and its row stride are multiples of: 32, 16 or less
+  int32_t out_align;      // bytes that out and its row stride are multiples of: 16, 4 or 2
   int32_t xs_vec, ws_vec; // rows of scales start on 16-byte boundaries
   int32_t tiles_m, tiles_n, num_tiles;  // pair_kernel
   unsigned int* status;
@@ -178,6 +178,47 @@ __device__ __forceinline__ bool fill_scales(float* ring, uint32_t full0, uint32_
     }
   }
   return true;
+}
+
+// A warp's outputs leave in boxes of 32 rows x 128 bytes, put together in shared memory (16-byte
+// units of a row permuted by XOR with row % 8: the 128-byte swizzle).  Where out's rows allow, TMA
+// copies a box out while the next tile's blocks arrive, leaving out what lies past the edges;
+// else the warp stores it row by row, 32 neighbouring words (or half words) at a time.
+__device__ __forceinline__ void begin_box(const Gemm8Params& p, int lane) {
+  if (p.out_align >= 16) {
+    if (lane == 0) bulk_wait_read();  // the copy of the last box has read it
+    __syncwarp();
+  }
+}
+__device__ __forceinline__ void store_box(const Gemm8Params& p, const CUtensorMap* map, unsigned char* box, int lane,
+                                          int64_t row, int64_t col) {
+  if (p.out_align >= 16) {
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0 && col < p.N && row < p.M) {
+      tma_store_2d(map, smem_addr(box), (int)col, (int)row);
+      bulk_commit();
+    }
+    return;
+  }
+  __syncwarp();
+  const int rows = (int)min((int64_t)32, p.M - row);
+  for (int r = 0; r < rows; ++r) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4);
+    if (p.out_dtype == FAR_F32) {
+      if (col + lane < p.N) static_cast<uint32_t*>(p.out)[(row + r) * p.ldo + col + lane] = v;
+    } else {
+      const int64_t n = col + 2 * lane;
+      uint16_t* o = static_cast<uint16_t*>(p.out) + (row + r) * p.ldo + n;
+      if (p.out_align >= 4 && n + 1 < p.N) {
+        *reinterpret_cast<uint32_t*>(o) = v;
+      } else {
+        if (n < p.N) o[0] = (uint16_t)v;
+        if (n + 1 < p.N) o[1] = (uint16_t)(v >> 16);
+      }
+    }
+  }
+  __syncwarp();  // before the next box
 }
 
 // ---------------------------------------------------------------------------
@@ -469,46 +510,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (lane == 0) mbar_arrive(sc_empty0 + 8 * slot);
         }
         if (!ok) break;
-        if (p.out_align >= 16) {
-          // through shared memory in boxes of 32 rows x 128 bytes (128-byte swizzle), copied out by TMA
-          // while the next tile's blocks arrive; the copy leaves out what lies past the edges
-          const bool f32 = p.out_dtype == FAR_F32;
-  #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (mine <= 32 * c) break;
-            if (f32 || (c & 1) == 0) {  // a new box: the copy of the last one has read it
-              if (lane == 0) bulk_wait_read();
-              __syncwarp();
-            }
-  #pragma unroll
-            for (int i = 0; i < 4; ++i)
-  #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const float* a = &acc[32 * c + 16 * (u >> 1) + 2 * (u & 1) + 4 * i];
-                unsigned char* line = box + (t4 + 8 * u) * 128;  // row t4 + 8 u: its units are permuted by t4
-                if (f32) {
-                  *reinterpret_cast<float2*>(line + (((2 * i + (q >> 1)) ^ t4) * 16) + (q & 1) * 8) = make_float2(a[0], a[1]);
-                } else {
-                  const uint32_t v = p.out_dtype == FAR_F16 ? narrow2<FAR_F16>(a[0], a[1]) : narrow2<FAR_BF16>(a[0], a[1]);
-                  *reinterpret_cast<uint32_t*>(line + (((4 * (c & 1) + i) ^ t4) * 16) + q * 4) = v;
-                }
-              }
-            if (f32 || (c & 1) == 1 || mine <= 32 * (c + 1)) {
-              fence_async_shared();
-              __syncwarp();
-              const int64_t x = col + (f32 ? 32 * c : 64 * (c / 2));
-              if (lane == 0 && x < p.N && row < p.M) {
-                tma_store_2d(&map_out, smem_addr(box), (int)x, (int)row);
-                bulk_commit();
+        const bool f32 = p.out_dtype == FAR_F32;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (mine <= 32 * c) break;
+          if (f32 || (c & 1) == 0) begin_box(p, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float* a = &acc[32 * c + 16 * (u >> 1) + 2 * (u & 1) + 4 * i];
+              unsigned char* line = box + (t4 + 8 * u) * 128;  // row t4 + 8 u: its units are permuted by t4
+              if (f32) {
+                *reinterpret_cast<float2*>(line + (((2 * i + (q >> 1)) ^ t4) * 16) + (q & 1) * 8) = make_float2(a[0], a[1]);
+              } else {
+                const uint32_t v = p.out_dtype == FAR_F16 ? narrow2<FAR_F16>(a[0], a[1]) : narrow2<FAR_BF16>(a[0], a[1]);
+                *reinterpret_cast<uint32_t*>(line + (((4 * (c & 1) + i) ^ t4) * 16) + q * 4) = v;
               }
             }
-          }
-        } else {
-  #pragma unroll
-          for (int i = 0; i < 128; ++i) {
-            const int64_t m = row + t4 + 8 * (((i >> 4) & 1) * 2 + ((i >> 1) & 1)), n = col + 32 * (i >> 5) + 8 * ((i >> 2) & 3) + 2 * q + (i & 1);
-            if (m < p.M && n < p.N) store_out(p, m, n, acc[i]);
-          }
+          if (f32 || (c & 1) == 1 || mine <= 32 * (c + 1))
+            store_box(p, &map_out, box, lane, row, col + (f32 ? 32 * c : 64 * (c / 2)));
         }
       }
     } else {
@@ -558,42 +579,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
         }
         if (!ok) break;
-        if (p.out_align >= 16) {
-          // through shared memory in boxes of 32 rows x 128 bytes (128-byte swizzle), copied out by TMA
-          // while the next tile's blocks arrive; the copy leaves out what lies past the edges
-  #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (mine <= 32 * c) break;
-            const bool f32 = p.out_dtype == FAR_F32;
-            if (f32 || (c & 1) == 0) {  // a new box: the copy of the last one has read it
-              if (lane == 0) bulk_wait_read();
-              __syncwarp();
-            }
-            uint32_t v[32];
-            if (f32) narrow<FAR_F32, 32>(acc + 32 * c, v);
-            else if (p.out_dtype == FAR_F16) narrow<FAR_F16, 32>(acc + 32 * c, v);
-            else narrow<FAR_BF16, 32>(acc + 32 * c, v);
-  #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              if (u < 4 || f32) {
-                const int unit = (f32 || (c & 1) == 0 ? u : u + 4) ^ (lane & 7);
-                *reinterpret_cast<uint4*>(box + lane * 128 + unit * 16) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-              }
-            }
-            if (f32 || (c & 1) == 1 || mine <= 32 * (c + 1)) {
-              fence_async_shared();
-              __syncwarp();
-              const int64_t x = col + (f32 ? 32 * c : 64 * (c / 2)), y = row - lane;
-              if (lane == 0 && x < p.N && y < p.M) {
-                tma_store_2d(&map_out, smem_addr(box), (int)x, (int)y);
-                bulk_commit();
-              }
+        const bool f32 = p.out_dtype == FAR_F32;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (mine <= 32 * c) break;
+          if (f32 || (c & 1) == 0) begin_box(p, lane);
+          uint32_t v[32];
+          if (f32) narrow<FAR_F32, 32>(acc + 32 * c, v);
+          else if (p.out_dtype == FAR_F16) narrow<FAR_F16, 32>(acc + 32 * c, v);
+          else narrow<FAR_BF16, 32>(acc + 32 * c, v);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            if (u < 4 || f32) {
+              const int unit = (f32 || (c & 1) == 0 ? u : u + 4) ^ (lane & 7);
+              *reinterpret_cast<uint4*>(box + lane * 128 + unit * 16) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
             }
           }
-        } else {
-  #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (row < p.M && col + i < p.N) store_out(p, row, col + i, acc[i]);
+          if (f32 || (c & 1) == 1 || mine <= 32 * (c + 1))
+            store_box(p, &map_out, box, lane, row - lane, col + (f32 ? 32 * c : 64 * (c / 2)));
         }
       }
     }
@@ -944,7 +947,7 @@ int run_gemm8(Gemm8Params& p, void* stream) {
   p.timeout_ns = kWaitTimeoutNs;
   const int64_t so = p.out_dtype == FAR_F32 ? 4 : 2;
   const uint64_t bits = (uint64_t)(uintptr_t)p.out | (uint64_t)(p.ldo * so);
-  p.out_align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
+  p.out_align = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
   p.xs_vec = p.KB % 4 == 0 && ((uintptr_t)p.xs & 15) == 0;
   p.ws_vec = p.KB % 4 == 0 && ((uintptr_t)p.ws & 15) == 0;
   const Gemm8Plan g = plan_gemm8(p, sms);

@@ -407,6 +407,11 @@ int gemm_fp8_block(const void* x, int64_t x_row_stride, const float* x_scale, co
                    const float* wt_scale, int wt_block, void* out, int64_t out_row_stride, int64_t m, int64_t n,
                    int64_t k, int out_dtype, void* stream);
 
+/* the product's plan for a device with `sms` SMs (host logic only; aligned operands, rows of k
+   codes): out4 = {kind (0 plain, 1 tensor cores over CTA pairs, 2 tensor cores with few rows of x a
+   CTA), rows of x a CTA (kind 2), CTAs that share a tile's k (kind 2), grid} */
+int far_plan_gemm_fp8_for_sms(int64_t m, int64_t n, int64_t k, int wt_block, int sms, int* out4);
+
 /* the output dtype od of FAR_DTYPES(act, wd), or -status when the pair is rejected */
 int far_output_dtype(int dtype);
 

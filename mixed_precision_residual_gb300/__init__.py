@@ -542,6 +542,7 @@ def rmsnorm_quant_host(x, weight, eps, qtype, q, scale, workspace, stream=None) 
                                   _stream_handle(stream)))
 
 
-from .block import fused_add_rmsnorm_quant_block, gemm_fp8_block, quant_block_fp8, rmsnorm_quant_block  # noqa: E402
+from .block import (fused_add_rmsnorm_quant_block, gemm_fp8_block, plan_gemm_fp8_for_sms, quant_block_fp8,  # noqa: E402
+                    rmsnorm_quant_block)
 from .heads import (qk_backward_workspace_bytes, qk_norm_rope, qk_norm_rope_backward, rope, rope_backward,  # noqa: E402
                     rope_frequencies, rope_table)

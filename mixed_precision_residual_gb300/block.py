@@ -19,7 +19,7 @@ import ctypes
 
 import torch
 
-from . import lib
+from . import _check, lib
 from ._launch import native, on_stream
 
 _vp, _f32, _i64, _int = ctypes.c_void_p, ctypes.c_float, ctypes.c_int64, ctypes.c_int
@@ -31,6 +31,8 @@ lib.quant_block_fp8.argtypes = [_vp, _i64, _vp, _vp, _i64, _i64, _int, _int, _in
 lib.quant_block_fp8.restype = _int
 lib.gemm_fp8_block.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _int, _vp, _i64, _i64, _i64, _i64, _int, _vp]
 lib.gemm_fp8_block.restype = _int
+lib.far_plan_gemm_fp8_for_sms.argtypes = [_i64, _i64, _i64, _int, _int, _vp]
+lib.far_plan_gemm_fp8_for_sms.restype = _int
 
 BLOCKS = {"row": 0, "tile": 1}
 
@@ -82,3 +84,10 @@ def gemm_fp8_block(x: torch.Tensor, x_scale: torch.Tensor, wt: torch.Tensor, wt_
     if stream is None:
         return native.gemm_fp8_block(x, x_scale, wt, wt_scale, out_dtype, out)
     return on_stream(stream, native.gemm_fp8_block, x, x_scale, wt, wt_scale, out_dtype, out)
+
+
+def plan_gemm_fp8_for_sms(m: int, n: int, k: int, block: str, sms: int) -> dict:
+    """gemm_fp8_block's plan for aligned operands on a device with `sms` SMs (host logic only)."""
+    buf = (ctypes.c_int * 4)()
+    _check(lib.far_plan_gemm_fp8_for_sms(m, n, k, BLOCKS[block], sms, ctypes.addressof(buf)))
+    return dict(zip(("kind", "rows", "split", "grid"), list(buf)))

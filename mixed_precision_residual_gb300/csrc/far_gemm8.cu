@@ -460,9 +460,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int64_t col = w.col0 + half * 128;
         const int mine = w.cols - half * 128;  // columns of this half (may be none)
         float acc[128];
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-  #pragma unroll 1
+#pragma unroll 1
         for (int kb = 0; kb < p.KB; ++kb, ++g) {
           const uint32_t buf = g & 1u, slot = g % kScaleSlots;
           if (!mbar_wait(sc_full0 + 8 * slot, (g / kScaleSlots) & 1u, p.timeout_ns, p.status)) {
@@ -471,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
           const float* rf = row_factors + slot * kSlotFloats;
           float sr[4];
-  #pragma unroll
+#pragma unroll
           for (int u = 0; u < 4; ++u) sr[u] = rf[8 * u];
           if (!mbar_wait(acc_full0 + 8 * buf, (g >> 1) & 1u, p.timeout_ns, p.status)) {
             ok = false;
@@ -481,7 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           const float4* cf = reinterpret_cast<const float4*>(col_factors + slot * kSlotFloats);
           // All 128 columns always: those past a narrow tile's hold what nobody stores.  (The
           // other warp of this SM quarter adds while this one loads.)
-  #pragma unroll
+#pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t r[32];
             tmem_ld_frag_sync(lanes + buf * 256 + 32 * c, r);
@@ -490,10 +490,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
             }
-  #pragma unroll
+#pragma unroll
             for (int i = 0; i < 4; i += 2) {
               const float4 f = cf[2 * c + i / 2];
-  #pragma unroll
+#pragma unroll
               for (int u = 0; u < 4; ++u) {  // row t + 8 u
                 const int o = 16 * (u >> 1) + 2 * (u & 1) + 4 * i;
                 float* a = &acc[32 * c + o];
@@ -545,15 +545,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         xn.load(xrow, 0, p.KB, p.xs_vec);
         wn.load(wrow, 0, p.KB, p.ws_vec);
         float acc[128];
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < 128; ++i) acc[i] = 0.f;
         for (int kb4 = 0; ok && kb4 < p.KB; kb4 += 4) {
           Scale4 sc;
-  #pragma unroll
+#pragma unroll
           for (int j = 0; j < 4; ++j) sc.v[j] = __fmul_rn(xn.v[j], wn.v[j]);
           xn.load(xrow, kb4 + 4, p.KB, p.xs_vec);  // the next four blocks', while these are worked on
           wn.load(wrow, kb4 + 4, p.KB, p.ws_vec);
-  #pragma unroll 1
+#pragma unroll 1
           for (int j = 0; j < 4 && kb4 + j < p.KB; ++j, ++g) {
             const uint32_t buf = g & 1u;
             const float sr = sc.at(j);
@@ -564,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             tc_fence_after();
             // All 128 columns always: those past a narrow tile's hold what nobody stores.  (The
             // other warp of this SM quarter adds while this one loads.)
-  #pragma unroll
+#pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t r[32];
               tmem_ld32_sync(lanes + buf * 256 + 32 * c, r);
@@ -573,7 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
               }
-  #pragma unroll
+#pragma unroll
               for (int i = 0; i < 32; ++i) acc[32 * c + i] = __fmaf_rn(__uint_as_float(r[i]), sr, acc[32 * c + i]);
             }
           }
@@ -893,12 +893,13 @@ Gemm8Plan plan_gemm8(const Gemm8Params& p, int sms) {
   g.split = 1;
   while (g.split < 8 && tiles_n * tiles_m * g.split * 2 <= slots && p.KB >= 4 * g.split) g.split *= 2;
   const int64_t pair_tiles = (((int64_t)p.M + 255) / 256) * (((int64_t)p.N + 255) / 256);
-  // Estimated microseconds, fitted to both kernels on 32 shapes (64 to 768 rows, 1536 x 1536 to 8192 x
-  // 8192): a launch, then waves of CTAs at so much a block of k.  The faster of the two is taken
-  // on all but 512 rows x 1536 x 1536 (11.3 against 10.3 us).  E.g. (pair / small) 128 x 8192 x
-  // 8192 31.3 / 27.0, 192 rows 31.4 / 44.1; 256 x 4096 x 4096 18.4 / 17.7, 384 rows 18.3 / 25.8.
+  // Estimated microseconds, fitted to both kernels on 44 shapes (4 to 768 rows, 128 x 384 to 8192 x
+  // 8192): a launch, then waves of CTAs at so much a block of k.  E.g. (pair / small) 4 x 8192 x
+  // 384 6.5 / 4.6; 64 x 2048 x 512 6.7 / 7.8, 64 x 8192 x 1024 8.9 / 7.7; 128 x 8192 x 8192 31.3 /
+  // 27.0, 192 rows 31.4 / 44.1; 256 x 4096 x 4096 18.4 / 17.7, 384 rows 18.3 / 25.8.
   const int64_t waves = (tiles_n * tiles_m * g.split + slots - 1) / slots;
-  const double small = 5.0 + 0.7 * (double)waves * (double)((p.KB + g.split - 1) / g.split);
+  const double depth = (double)waves * (double)((p.KB + g.split - 1) / g.split);
+  const double small = g.nt == 16 ? 3.4 + 0.55 * depth : g.nt == 32 ? 4.5 + 0.6 * depth : 6.3 + 0.66 * depth;
   const int64_t pair_waves = (pair_tiles + sms / 2 - 1) / (sms / 2);
   const double pair = 4.8 + (p.tile_scales ? 0.42 : 0.8) * (double)pair_waves * p.KB;
   const bool fits = tiles_n <= 65535 && tiles_m <= 65535;
@@ -1010,4 +1011,31 @@ extern "C" int gemm_fp8_block(const void* x, int64_t x_row_stride, const float* 
   p.K = (int32_t)k;
   p.KB = (int32_t)((k + kBlock - 1) / kBlock);
   return run_gemm8(p, stream);
+}
+
+extern "C" int far_plan_gemm_fp8_for_sms(int64_t m, int64_t n, int64_t k, int wt_block, int sms, int* out4) {
+  if (!out4) return FAR_ERR_NULL;
+  if (wt_block != FAR_BLOCK_ROW && wt_block != FAR_BLOCK_TILE) return FAR_ERR_DTYPE;
+  if (m < 1 || n < 1 || k < 1 || m > INT32_MAX || n > INT32_MAX || k > INT32_MAX || sms < 2) return FAR_ERR_SHAPE;
+  Gemm8Params p{};  // (16-byte aligned operands with rows of k codes)
+  p.M = (int32_t)m;
+  p.N = (int32_t)n;
+  p.K = (int32_t)k;
+  p.KB = (int32_t)((k + kBlock - 1) / kBlock);
+  p.ldx = p.ldw = k;
+  p.tile_scales = wt_block == FAR_BLOCK_TILE;
+  const Gemm8Plan g = plan_gemm8(p, sms);
+  int64_t ctas = 0;
+  if (g.kind == 1) {
+    const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
+    ctas = 2 * (tiles < sms / 2 ? tiles : sms / 2);
+  } else if (g.kind == 2) {
+    ctas = g.split * ((n + 127) / 128) * ((m + g.nt - 1) / g.nt);
+  } else {
+    const int64_t tiles = ((m + 63) / 64) * ((n + 63) / 64);
+    ctas = tiles < 8ll * sms ? tiles : 8ll * sms;
+  }
+  const int v[4] = {g.kind, g.kind == 2 ? g.nt : 0, g.kind == 2 ? g.split : 0, (int)(ctas < INT32_MAX ? ctas : INT32_MAX)};
+  for (int i = 0; i < 4; ++i) out4[i] = v[i];
+  return FAR_OK;
 }

@@ -96,3 +96,26 @@ def test_binding_refusals(far):
         far.quant_block_fp8(x.double())
     with pytest.raises(far.FarError):
         far.gemm_fp8_block(q, s, q, s, out_dtype=torch.float64)
+
+
+def test_gemm_plans(far):
+    """Decode batches and few rows take the small kernel with k shared out while SMs are free, large
+    products CTA pairs, k that TMA cannot step over the plain kernel."""
+    plan = far.plan_gemm_fp8_for_sms
+    assert plan(1, 8192, 8192, "tile", 152) == {"kind": 2, "rows": 16, "split": 4, "grid": 256}
+    assert plan(17, 8192, 8192, "row", 152)["rows"] == 32 and plan(33, 8192, 8192, "tile", 152)["rows"] == 64
+    assert plan(4, 1024, 8192, "tile", 152)["split"] == 8
+    assert plan(4, 128, 384, "tile", 152)["split"] == 1  # three blocks of k are not shared out
+    assert plan(128, 8192, 8192, "tile", 152)["kind"] == 2 and plan(192, 8192, 8192, "tile", 152)["kind"] == 1
+    assert plan(16384, 8192, 8192, "tile", 152) == {"kind": 1, "rows": 0, "split": 0, "grid": 152}
+    assert plan(600, 777, 640, "tile", 152)["kind"] == 1 and plan(3000, 1102, 256, "row", 152)["kind"] == 1
+    assert plan(4, 128, 1000, "tile", 152)["kind"] == 0 and plan(16384, 8192, 100, "tile", 152)["kind"] == 0
+    assert plan(1 << 30, 1 << 30, 128, "tile", 152)["kind"] == 0  # more tiles than are counted
+    for m, n, k in ((1, 1, 16), (64, 100000, 128), (2000000, 128, 4096), (1, 1 << 23, 256)):
+        p = plan(m, n, k, "tile", 152)
+        assert p["kind"] in (1, 2) and p["grid"] >= 1
+        if p["kind"] == 2:  # no CTA without a block of k, clusters of a portable size
+            assert p["split"] <= 8 and p["split"] <= -(-k // 128)
+    for bad in ((0, 8, 8), (8, 0, 8), (8, 8, 0), (1 << 31, 8, 8)):
+        with pytest.raises(far.FarError):
+            plan(*bad, "tile", 152)

@@ -231,7 +231,8 @@ def check_gemm(far, xq, xs, wq, ws, dtype, where, out=None):
 
 GEMM = [(1, 1, 16), (1, 8, 128), (1, 130, 256), (2, 128, 144), (3, 300, 1040), (7, 256, 512), (16, 384, 2048), (17, 1000, 640),
         (33, 129, 128), (64, 512, 1024), (65, 257, 272), (100, 640, 384), (128, 128, 128), (129, 385, 528), (200, 2056, 512),
-        (256, 512, 4096), (300, 300, 304), (513, 768, 256), (1000, 1544, 784), (2048, 2048, 512)]
+        (256, 512, 4096), (300, 300, 304), (513, 768, 256), (1000, 1544, 784), (2048, 2048, 512),
+        (600, 777, 640), (3000, 1102, 256), (1025, 2049, 128), (3000, 520, 2064)]
 
 
 @pytest.mark.parametrize("rows", ["tile", "row"])

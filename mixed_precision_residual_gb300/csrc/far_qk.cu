@@ -19,7 +19,10 @@
 // waits for another), several steps ahead: the registers hold one step's values, and what is
 // in flight does not depend on how many warps they leave room for.  With loads into
 // registers instead, 128 bytes a lane and 16 warps an SM, the forward pass over 16384 tokens
-// of 32 + 8 heads of 128 bf16 values took 70.4 us and the backward pass over 8192 77.9.
+// of 32 + 8 heads of 128 bf16 values took 70.4 us and the backward pass over 8192 77.9; now 63.7 us
+// (5.4 TB/s, 81 % of a copy's rate) and 48.8 us (5.2 TB/s).  About 210 and 400 instructions a step
+// of four heads keep the schedulers 60 % busy beside DRAM at 61 %; three CTAs an SM, or the
+// table's rows fetched ahead through the ring too, took longer (66.0; 64.4 and 52.1 us).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -134,9 +137,9 @@ __device__ __forceinline__ Slot slot_of(int s, int C, int RC) {
   return r;
 }
 
-// Two neighbouring values.  (As two registers: held as one 64-bit register for the packed
-// binary32 instructions, the backward kernel issued 386 instructions a step of four heads
-// against SCALARCOUNT.)
+// Two neighbouring values, in two registers.  (In one 64-bit register, for the packed binary32
+// instructions, the backward pass of 8192 tokens took 55.5 us against 55.0: what the packed
+// forms saved went into moves.)
 struct X2 {
   float x, y;
 };
@@ -765,6 +768,27 @@ bool distinct(const Heads& t, int64_t tokens, int64_t heads, int64_t D) {
   return th || ht;
 }
 
+// Do two [tokens, heads, D] tensors share a byte?  Exact for equal strides (queries and keys
+// interleaved in one buffer in whatever way), else whether the bytes they span meet.
+bool heads_meet(const Heads& a, int64_t ha, const Heads& b, int64_t hb, int64_t tokens, int64_t D, int64_t es) {
+  const bool same = (tokens == 1 || a.ts == b.ts) && (a.hs == b.hs || (ha == 1 && hb == 1));
+  if (!regions_overlap(heads_region(a, tokens, ha, D, es), heads_region(b, tokens, hb, D, es))) return false;
+  if (!same || ha + hb > 8192) return true;
+  // head i of token t of a and head j of token u of b meet iff |d + (u - t) ts + (j - i) hs| < D, in
+  // elements where the bases differ by whole ones, in bytes to be exact
+  const int64_t d = (int64_t)((uint64_t)(uintptr_t)b.p - (uint64_t)(uintptr_t)a.p), w = D * es, ts = tokens == 1 ? 0 : a.ts * es;
+  for (int64_t dh = -(ha - 1); dh <= hb - 1; ++dh) {
+    const int64_t at = d + dh * a.hs * es;
+    if (ts == 0) {
+      if (at > -w && at < w) return true;
+      continue;
+    }
+    const int64_t lo = floor_div(-w - at, ts) + 1, hi = -floor_div(at - w, ts) - 1;  // -w < at + k ts < w
+    if (lo <= hi && lo <= tokens - 1 && hi >= -(tokens - 1)) return true;
+  }
+  return false;
+}
+
 bool same_heads(const Heads& a, const Heads& b, int64_t tokens, int64_t heads) {
   return a.p == b.p && (tokens == 1 || a.ts == b.ts) && (heads == 1 || a.hs == b.hs);
 }
@@ -811,12 +835,9 @@ int validate_qk(const QkCall& c) {
   if ((uintptr_t)c.table % 4 || (uintptr_t)c.pos % c.pos_bytes) return FAR_ERR_SHAPE;
   if (c.back && (!c.ws || c.ws_bytes < far_qk_backward_workspace_bytes(c.D) || ((uintptr_t)c.ws & 15)))
     return FAR_ERR_WORKSPACE;
-  // overlaps: the written regions against everything else
-  Region wr[5], rd[10];
+  // overlaps: every written buffer against every other
+  Region wr[3], rd[4];
   int nw = 0, nr = 0;
-  for (int i = 0; i < 2; ++i)
-    if (c.heads[i]) wr[nw++] = heads_region(c.y[i], c.tokens, c.heads[i], c.D, es);
-  const int ny = nw;
   if (c.back) {
     for (int i = 0; i < 2; ++i)
       if (c.heads[i]) wr[nw++] = region(c.dw[i], 1, c.D * 4, 0);
@@ -832,19 +853,26 @@ int validate_qk(const QkCall& c) {
     for (int b = 0; b < nr; ++b)
       if (regions_overlap(wr[a], rd[b])) return FAR_ERR_ALIAS;
   }
-  for (int i = 0, a = 0; i < 2; ++i) {
+  for (int i = 0; i < 2; ++i) {
     if (!c.heads[i]) continue;
+    const Region Y = heads_region(c.y[i], c.tokens, c.heads[i], c.D, es);
+    for (int b = 0; b < nr; ++b)
+      if (regions_overlap(Y, rd[b])) return FAR_ERR_ALIAS;
+    for (int b = 0; b < nw; ++b)
+      if (regions_overlap(Y, wr[b])) return FAR_ERR_ALIAS;
+    if (i == 0 && c.heads[1] && heads_meet(c.y[0], c.heads[0], c.y[1], c.heads[1], c.tokens, c.D, es)) return FAR_ERR_ALIAS;
     for (int j = 0; j < 2; ++j) {
       if (!c.heads[j]) continue;
       for (const Heads* t : {&c.x[j], &c.g[j]}) {
         if (t == &c.g[j] && !c.back) continue;
-        const Region R = heads_region(*t, c.tokens, c.heads[j], c.D, es);
-        if (regions_overlap(wr[a], R) && !(i == j && same_heads(c.y[i], *t, c.tokens, c.heads[i]))) return FAR_ERR_ALIAS;
-        for (int b = ny; b < nw; ++b)
-          if (regions_overlap(wr[b], R)) return FAR_ERR_ALIAS;
+        if (!(i == j && same_heads(c.y[i], *t, c.tokens, c.heads[i])) &&
+            heads_meet(c.y[i], c.heads[i], *t, c.heads[j], c.tokens, c.D, es))
+          return FAR_ERR_ALIAS;
+        const Region X = heads_region(*t, c.tokens, c.heads[j], c.D, es);
+        for (int b = 0; b < nw; ++b)
+          if (regions_overlap(wr[b], X)) return FAR_ERR_ALIAS;
       }
     }
-    ++a;
   }
   return FAR_OK;
 }

@@ -319,6 +319,29 @@ def test_gemm_same_bits_every_run(far):
             assert torch.equal(far.gemm_fp8_block(*a), first)
 
 
+def test_plain_launches_give_the_same_bits(far):
+    """With programmatic dependent launch off (far_set_programmatic_launch), a run of dependent calls is the same."""
+    x, r = torch.randn(40, 1024, device="cuda").bfloat16(), torch.randn(40, 1024, device="cuda").bfloat16()
+    w, nw = torch.randn(768, 1024, device="cuda").bfloat16(), torch.ones(1024, device="cuda").bfloat16()
+    table, pos, one = far.rope_table(64, 128), torch.arange(40, device="cuda"), torch.ones(128, device="cuda").bfloat16()
+
+    def run():
+        wq, ws = far.quant_block_fp8(w, block="tile")
+        xq, xs, res = far.fused_add_rmsnorm_quant_block(x, r, nw, 1e-6)
+        qkv = far.gemm_fp8_block(xq, xs, wq, ws).view(40, 6, 128)
+        y = far.qk_norm_rope(qkv[:, :4], qkv[:, 4:], one, one, 1e-6, table, pos)
+        return (res, qkv, *y, *far.qk_norm_rope_backward(*y, qkv[:, :4], qkv[:, 4:], one, one, 1e-6, table, pos))
+
+    want = [run() for _ in range(3)]
+    try:
+        far.set_programmatic_launch(False)
+        got = run()
+    finally:
+        far.set_programmatic_launch(True)
+    for other in want[1:] + [got]:
+        assert all(torch.equal(a, b) for a, b in zip(other, want[0]))
+
+
 def test_gemm_streams_and_graphs(far):
     """Calls on three streams at once, and two captured graphs replayed on new values."""
     sets = [operands(m, 1024, 1024, "tile", seed=m) for m in (3, 130, 512)]

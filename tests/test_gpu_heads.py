@@ -170,6 +170,20 @@ def test_packed_projection_in_place(far):
         assert torch.equal(qkv.view(37, 10, d)[:, 8:], v)
 
 
+def test_interleaved_projection_in_place(far):
+    """q, k and v interleaved head by head, [tokens, heads, 3, d]: in place, values untouched; one token too."""
+    for tokens in (19, 1):
+        s = make(tokens, 4, 4, 64, 64, "bf16")
+        v = torch.randn(tokens, 4, 64, device="cuda").bfloat16()
+        buf = torch.stack([s["q"], s["k"], v], 2).contiguous()
+        q, k = buf[:, :, 0], buf[:, :, 1]
+        far.qk_norm_rope(q, k, s["qw"], s["kw"], s["eps"], s["table"], s["pos"], q_out=q, k_out=k)
+        assert far.device_status() == 0
+        for x, w, y in ((s["q"], s["qw"], q), (s["k"], s["kw"], k)):
+            within(y, *forward(x, w, s["eps"], s["table"], s["pos"], "half"), f"interleaved {tokens}")
+        assert torch.equal(buf[:, :, 2], v)
+
+
 def test_layouts_give_the_same_bits(far):
     """Head-major buffers, token strides with gaps, four axes, int32 positions: the contiguous call's bits."""
     s = make(24, 4, 2, 128, 128, "bf16")

@@ -75,6 +75,15 @@ def test_rope_refusals(far):
     assert rope(transpose=2) == 2 and rope(act=3) == 2 and rope(q=None) == 3 and rope(y=A + 64) == 5
 
 
+def test_interleaved_views_in_place(far):
+    """q and k interleaved head by head in one buffer: in place is allowed, a value's overlap is not."""
+    il = dict(q=A, qts=768, qhs=192, k=A + 128, kts=768, khs=192, hk=2, yq=A, yqts=768, yqhs=192, yk=A + 128, ykts=768, ykhs=192)
+    assert call(far, **{**il, "yk": A + 126}) == 5  # k_out one value into q's head
+    assert call(far, **{**il, "yk": A + 128 + 64}) == 5  # between its own heads: shares bytes with k
+    assert call(far, **{**il, "k": A + 128 + 768 * 2 * 3, "yk": A + 128 + 768 * 2 * 3 - 2}) == 5
+    # (the allowed calls run on the GPU: test_gpu_heads.py)
+
+
 def test_nothing_to_do(far):
     """No tokens, or no heads: accepted without touching anything."""
     assert call(far, tokens=0, q=None, k=None, yq=None, yk=None, pos=None, table=None, rows=0) == 0

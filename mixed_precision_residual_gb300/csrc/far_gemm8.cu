@@ -203,6 +203,7 @@ __device__ __forceinline__ void store_box(const Gemm8Params& p, const CUtensorMa
   }
   __syncwarp();
   const int rows = (int)min((int64_t)32, p.M - row);
+#pragma unroll 8
   for (int r = 0; r < rows; ++r) {
     const uint32_t v = *reinterpret_cast<const uint32_t*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4);
     if (p.out_dtype == FAR_F32) {

@@ -137,6 +137,19 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const QbParams p) {
   }
 }
 
+// Writes n codes that lie in shared memory as 32 words, one a lane, to dst at any alignment: whole
+// aligned words put together from two neighbours, the up to 3 codes before and behind them alone.
+__device__ __forceinline__ void store_codes(unsigned char* dst, uint32_t word, int n, int lane) {
+  const int s = (int)((4 - ((uintptr_t)dst & 3)) & 3);
+  const uint32_t next = __shfl_down_sync(0xffffffffu, word, 1);
+  const uint32_t first = __shfl_sync(0xffffffffu, word, 0);
+  const int t = s + ((n - s) & ~3) + lane;  // (behind the last whole word; n < s: nothing whole)
+  const uint32_t tail = __shfl_sync(0xffffffffu, word, (t >> 2) & 31);
+  if (s + 4 * lane + 4 <= n) *reinterpret_cast<uint32_t*>(dst + s + 4 * lane) = __funnelshift_r(word, next, 8 * s);
+  if (lane < s && lane < n) dst[lane] = (unsigned char)(first >> (8 * lane));
+  if (lane < 3 && n > s && t < n) dst[t] = (unsigned char)(tail >> (8 * (t & 3)));
+}
+
 // One 128 x 128 tile a CTA (blockIdx.x over the columns, .y and .z over the rows).  A thread holds RPT
 // neighbouring rows of one chunk of V columns: RPT * V = 64 values, so that the codes of a column
 // it holds are RPT neighbouring bytes of the transposed row.
@@ -157,6 +170,9 @@ __global__ void __launch_bounds__(kThreads, ACT == FAR_F32 ? 2 : (TRANS || !VEC)
   const int64_t r0 = tr * kBlock, c0 = tc * kBlock;
   if (r0 >= p.rows) return;  // the whole CTA
   const int ch = threadIdx.x % CH, rg = threadIdx.x / CH;  // rg: this thread's group of RPT rows
+  // value e of a thread's chunk: neighbouring columns, or (without 16-byte loads) columns CH apart,
+  // so that neighbouring lanes read neighbouring values
+  auto at = [&](int e) { return VEC ? ch * V + e : ch + CH * e; };
   const int64_t col = c0 + ch * V;
   const int nr = (int)(p.rows - r0 < kBlock ? p.rows - r0 : kBlock);  // rows, columns of x in this tile
   const int nc = (int)(p.cols - c0 < kBlock ? p.cols - c0 : kBlock);
@@ -171,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, ACT == FAR_F32 ? 2 : (TRANS || !VEC)
     } else {
       float f[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) f[e] = r < nr && ch * V + e < nc ? elem<ACT>(xr, col + e) : 0.f;
+      for (int e = 0; e < V; ++e) f[e] = r < nr && at(e) < nc ? elem<ACT>(xr, c0 + at(e)) : 0.f;
       narrow<ACT, V>(f, raw[i]);  // exact: back to where it came from
     }
   }
@@ -218,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, ACT == FAR_F32 ? 2 : (TRANS || !VEC)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       if constexpr (CH == 16) cm[e] = max_nan(cm[e], __shfl_xor_sync(0xffffffffu, cm[e], 16));
-      if (lane < CH) part[warp * kBlock + ch * V + e] = cm[e];
+      if (lane < CH) part[warp * kBlock + at(e)] = cm[e];
     }
     __syncthreads();
     if (threadIdx.x < kBlock) {
@@ -230,27 +246,29 @@ __global__ void __launch_bounds__(kThreads, ACT == FAR_F32 ? 2 : (TRANS || !VEC)
     }
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < V; ++e) cm[e] = invs[ch * V + e];
+    for (int e = 0; e < V; ++e) cm[e] = invs[at(e)];
   }
 
   if constexpr (!TRANS) {
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int r = rg * RPT + i;
-      if (r < nr && ch * V < nc) {
+      if (r < nr) {
         float f[V];
         widen<ACT, V>(raw[i], f);
         uint32_t qw[V / 4];
 #pragma unroll
         for (int e = 0; e < V / 4; ++e) qw[e] = codes4(f + 4 * e, cm[0]);
-        unsigned char* q = p.q + (r0 + r) * p.cols + col;
+        unsigned char* q = p.q + (r0 + r) * p.cols + c0;
         if constexpr (VEC) {
+          q += ch * V;
+          if (ch * V >= nc) continue;
           if constexpr (V == 8) *reinterpret_cast<uint2*>(q) = make_uint2(qw[0], qw[1]);
           else *reinterpret_cast<uint32_t*>(q) = qw[0];
         } else {
 #pragma unroll
           for (int e = 0; e < V; ++e)
-            if (ch * V + e < nc) q[e] = (unsigned char)(qw[e >> 2] >> (8 * (e & 3)));
+            if (at(e) < nc) q[at(e)] = (unsigned char)(qw[e >> 2] >> (8 * (e & 3)));
         }
       }
     }
@@ -270,36 +288,38 @@ __global__ void __launch_bounds__(kThreads, ACT == FAR_F32 ? 2 : (TRANS || !VEC)
         qc[e][i4] = quantise4<kQuantFp8>(__fmul_rn(f[0][e], cm[e]), __fmul_rn(f[1][e], cm[e]), __fmul_rn(f[2][e], cm[e]),
                                          __fmul_rn(f[3][e], cm[e]));
     }
-    const int unit = rg ^ (ch & (UNITS - 1));
+    auto turn = [](int c) { return (VEC ? c / V : c) & (UNITS - 1); };  // (a lane's own in either layout)
+    const int unit = rg ^ turn(at(0));
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      unsigned char* s = sm + (ch * V + e) * kBlock + unit * RPT;
+      unsigned char* s = sm + at(e) * kBlock + unit * RPT;
       if constexpr (RPT == 8) *reinterpret_cast<uint2*>(s) = make_uint2(qc[e][0], qc[e][1]);
       else *reinterpret_cast<uint4*>(s) = make_uint4(qc[e][0], qc[e][1], qc[e][2], qc[e][3]);
     }
     __syncthreads();
-    // rows of q: 8 lanes of 16 bytes each, where its rows start on 16-byte boundaries
-    const bool wide = p.rows % 16 == 0 && ((uintptr_t)p.q & 15) == 0;
+    if (p.rows % 16 == 0 && ((uintptr_t)p.q & 15) == 0) {
+      // rows of q start on 16-byte boundaries: 8 lanes of 16 bytes each
 #pragma unroll
-    for (int j = 0; j < kBlock * 8 / kThreads; ++j) {
-      const int c = j * (kThreads / 8) + threadIdx.x / 8, k = threadIdx.x % 8;
-      const int swz = (c / V) & (UNITS - 1);
-      if (c >= nc) break;
-      unsigned char* q = p.q + (c0 + c) * p.rows + r0;
-      uint4 v;
-      if constexpr (RPT == 8) {  // the two 8-byte units of 16 rows share a 16-byte place, in either order
-        v = *reinterpret_cast<const uint4*>(sm + c * kBlock + ((2 * k) ^ (swz & ~1)) * 8);
-        if (swz & 1) v = make_uint4(v.z, v.w, v.x, v.y);
-      } else {
-        v = *reinterpret_cast<const uint4*>(sm + c * kBlock + (k ^ swz) * 16);
+      for (int j = 0; j < kBlock * 8 / kThreads; ++j) {
+        const int c = j * (kThreads / 8) + threadIdx.x / 8, k = threadIdx.x % 8;
+        const int swz = turn(c);
+        if (c >= nc) break;
+        unsigned char* q = p.q + (c0 + c) * p.rows + r0;
+        uint4 v;
+        if constexpr (RPT == 8) {  // the two 8-byte units of 16 rows share a 16-byte place, in either order
+          v = *reinterpret_cast<const uint4*>(sm + c * kBlock + ((2 * k) ^ (swz & ~1)) * 8);
+          if (swz & 1) v = make_uint4(v.z, v.w, v.x, v.y);
+        } else {
+          v = *reinterpret_cast<const uint4*>(sm + c * kBlock + (k ^ swz) * 16);
+        }
+        if (k * 16 < nr) *reinterpret_cast<uint4*>(q + k * 16) = v;  // (whole 16 bytes)
       }
-      if (wide) {
-        if (k * 16 < nr) *reinterpret_cast<uint4*>(q + k * 16) = v;  // rows % 16 == 0: whole 16 bytes
-      } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int b = 0; b < 16; ++b)
-          if (k * 16 + b < nr) q[k * 16 + b] = (unsigned char)(w[b >> 2] >> (8 * (b & 3)));
+    } else {
+      // a warp a row of q, a word a lane
+      for (int c = warp; c < nc; c += WARPS) {
+        constexpr int W = RPT / 4;  // words a unit
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(sm + c * kBlock + ((lane / W) ^ turn(c)) * RPT + lane % W * 4);
+        store_codes(p.q + (c0 + c) * p.rows + r0, v, nr, lane);
       }
     }
   }

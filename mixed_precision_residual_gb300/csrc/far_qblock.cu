@@ -32,12 +32,6 @@ struct QbParams {
   int32_t segs;      // rows_kernel: warp tasks a row
 };
 
-template <int DT> __device__ __forceinline__ float elem(const void* base, int64_t i) {
-  if constexpr (DT == FAR_F16) return __half2float(static_cast<const __half*>(base)[i]);
-  else if constexpr (DT == FAR_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
-  else return static_cast<const float*>(base)[i];
-}
-
 // 16 bytes, or zeros where `on` is false.  Volatile and without a branch: a thread's loads then
 // all leave before the first is waited for (a bf16 weight of 8192 x 8192 by tiles: 32.5 us, 6.2
 // TB/s; with each load under its branch 42.6).
@@ -47,6 +41,27 @@ __device__ __forceinline__ void load16(uint32_t (&w)[4], const void* src, bool o
       "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
       : "=&r"(w[0]), "=&r"(w[1]), "=&r"(w[2]), "=&r"(w[3])
       : "l"(src), "r"((int)on));
+}
+
+// one value's bits (zeros where `on` is false), as load16
+template <int DT> __device__ __forceinline__ uint32_t load_bits(const void* base, int64_t i, bool on) {
+  uint32_t v;
+  if constexpr (DT == FAR_F32) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
+                 : "=&r"(v)
+                 : "l"(static_cast<const float*>(base) + i), "r"((int)on));
+  } else {
+    uint16_t h;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t@p ld.global.nc.b16 %0, [%1];\n\t}"
+                 : "=&h"(h)
+                 : "l"(static_cast<const uint16_t*>(base) + i), "r"((int)on));
+    v = h;
+  }
+  return v;
+}
+template <int DT> __device__ __forceinline__ float value_of(uint32_t bits) {
+  if constexpr (DT == FAR_F32) return __uint_as_float(bits);
+  else return widen2<DT>(bits).x;
 }
 
 __device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
@@ -80,27 +95,39 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const QbParams p) {
       uint32_t raw[U][4];
 #pragma unroll
       for (int u = 0; u < U; ++u) load16(raw[u], xr + (int64_t)(c0 + 32 * u) * 16, c0 + 32 * u < chunks);
+      float m[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int c = c0 + 32 * u;
-        const uint32_t(&w)[4] = raw[u];
-        float f[V];
-        widen<ACT, V>(w, f);
-        float m = 0.f;
+        m[u] = 0.f;
         if constexpr (ACT == FAR_F32) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) m = max_nan(m, fabsf(f[e]));
+          for (int e = 0; e < V; ++e) m[u] = max_nan(m[u], fabsf(__uint_as_float(raw[u][e])));
         } else {
           uint32_t m2 = 0u;
 #pragma unroll
-          for (int e = 0; e < V / 2; ++e) m2 = habs_max2<ACT>(m2, w[e]);
+          for (int e = 0; e < V / 2; ++e) m2 = habs_max2<ACT>(m2, raw[u][e]);
           const float2 h = widen2<ACT>(m2);
-          m = max_nan(h.x, h.y);
+          m[u] = max_nan(h.x, h.y);
         }
-        m = lanes_max(m, LANES);
-        const float inv = block_inverse(m);
+        m[u] = lanes_max(m[u], LANES);
+      }
+      // The divisions of the U blocks, shared out: of a block's lanes, number u < 4 takes the u-th
+      // factor, number 4 + u the u-th scale (each lane all eight: 38.0 us for 8192 x 8192 bf16)
+      static_assert(U == 4, "");
+      const int j = lane & (LANES - 1), pick = j & 3;
+      const float mine = pick == 0 ? m[0] : pick == 1 ? m[1] : pick == 2 ? m[2] : m[3];
+      const bool scales = j & 4;
+      const float quotient = __fdiv_rn(scales ? mine : 448.0f, scales ? 448.0f : mine);
+      const float val = mine < kBlockTiny ? 0.f : quotient;
+      const int first = c0 - j + 32 * pick;  // the block's first chunk
+      if (j >= 4 && j < 8 && first < chunks) sr[first / LANES] = val;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float inv = __shfl_sync(0xffffffffu, val, (lane - j) + u);
+        const int c = c0 + 32 * u;
         if (c < chunks) {
-          if ((lane & (LANES - 1)) == 0) sr[c / LANES] = block_scale(m);
+          float f[V];
+          widen<ACT, V>(raw[u], f);
           uint32_t qw[V / 4];
 #pragma unroll
           for (int e = 0; e < V / 4; ++e) qw[e] = codes4(f + 4 * e, inv);
@@ -109,28 +136,31 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const QbParams p) {
         }
       }
     } else {
-      float f[U][4];
+      uint32_t bits[U][4];
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int64_t i = (int64_t)(seg * U + u) * kBlock + e * 32 + lane;
-          f[u][e] = i < p.cols ? elem<ACT>(xr, i) : 0.f;
+          bits[u][e] = load_bits<ACT>(xr, i, i < p.cols);
         }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t b = (int64_t)seg * U + u;
         if (b >= nblk) break;
-        float m = 0.f;
+        float m = 0.f, f[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) m = max_nan(m, fabsf(f[u][e]));
+        for (int e = 0; e < 4; ++e) {
+          f[e] = value_of<ACT>(bits[u][e]);
+          m = max_nan(m, fabsf(f[e]));
+        }
         m = warp_max_allreduce(m);
         const float inv = block_inverse(m);
         if (lane == 0) sr[b] = block_scale(m);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int64_t i = b * kBlock + e * 32 + lane;
-          if (i < p.cols) qr[i] = code1(f[u][e], inv);
+          if (i < p.cols) qr[i] = code1(f[e], inv);
         }
       }
     }
@@ -185,10 +215,11 @@ __global__ void __launch_bounds__(kThreads, ACT == FAR_F32 ? 2 : (TRANS || !VEC)
     if constexpr (VEC) {
       load16(raw[i], xr + col * (16 / V), r < nr && ch * V < nc);
     } else {
-      float f[V];
+      uint32_t v[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) f[e] = r < nr && at(e) < nc ? elem<ACT>(xr, c0 + at(e)) : 0.f;
-      narrow<ACT, V>(f, raw[i]);  // exact: back to where it came from
+      for (int e = 0; e < V; ++e) v[e] = load_bits<ACT>(xr, c0 + at(e), r < nr && at(e) < nc);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) raw[i][e] = ACT == FAR_F32 ? v[e] : v[(2 * e) % V] | v[(2 * e + 1) % V] << 16;
     }
   }
 

@@ -229,24 +229,29 @@ __device__ __forceinline__ void store_box(const Gemm8Params& p, const CUtensorMa
 //   warp 0      TMA producer (both CTAs), a ring of kPairStages blocks of k running across tiles
 //   warp 1      MMA issuer (even CTA); allocates TMEM: two halves of 256 columns
 //   warps 2, 3  where wt is scaled by rows: column and row factors, some blocks of k ahead
-//   warps 4-11  epilogue: warp w the TMEM lanes 32 (w % 4) .., columns 128 ((w - 4) / 4) ..; a
-//               thread keeps 128 outputs in registers
+//   warps 4-    epilogue: warp w the TMEM lanes 32 (w % 4) .. and 128 or (row-scaled wt) 64 of the
+//               columns, so that a thread keeps 128 or 64 outputs in registers
 // The registers a thread: 384 threads are launched at 168; warps 0-3 give theirs up to 72 and
-// the epilogue's take 216 (128 x 72 + 256 x 216 = 384 x 168).
+// the 8 epilogue warps take 216 (128 x 72 + 256 x 216 = 384 x 168).  With 16 epilogue warps
+// 640 at 96, then 56 and 104 (128 x 56 + 512 x 104 = 60416 of 61440).
 // The last column of tiles runs at the width that is left (a multiple of 32).
 // ---------------------------------------------------------------------------
-constexpr int kPairThreads = 384;
-constexpr int kPairStages = 5;
 constexpr uint32_t kPairABytes = 128 * kBlock, kPairBBytes = 128 * kBlock;
-constexpr uint32_t kPairRing = kPairStages * (kPairABytes + kPairBBytes);
-constexpr int kPairBars = 2 * kPairStages + 4 + 2 * kScaleSlots;
-constexpr uint32_t kPairOut = 8 * 4096;  // a box of 32 rows x 128 bytes of outputs an epilogue warp
-// A slot of the scale ring (wt scaled by rows): the 128 rows' factors, then for each half of the
-// columns 4 groups of 32 column factors, 36 apart (a fragment's thread reads one group, and
-// the four groups lie on different banks).
-constexpr int kRowFactors = 128, kColGroup = 36, kSlotFloats = kRowFactors + 2 * 4 * kColGroup;
-constexpr uint32_t kPairScales = kScaleSlots * kSlotFloats * 4;
-constexpr size_t kPairSmem = kPairRing + kPairOut + kPairScales + kPairBars * 8 + 16 + 1024;
+// A slot of the scale ring (wt scaled by rows): the 128 rows' factors, then for each 64 columns
+// 4 groups of 16 column factors, 20 apart (a fragment's thread reads one group, and the four
+// groups lie on different banks).
+constexpr int kRowFactors = 128, kColGroup = 20, kSlotFloats = kRowFactors + 4 * 4 * kColGroup;
+template <bool COLS>
+struct PairShape8 {
+  static constexpr int warps = COLS ? 16 : 8;  // of the epilogue
+  static constexpr int threads = 128 + 32 * warps;
+  static constexpr int stages = COLS ? 4 : 5;
+  static constexpr uint32_t ring = stages * (kPairABytes + kPairBBytes);
+  static constexpr uint32_t out = warps * 4096;  // a box of 32 rows x 128 bytes of outputs a warp
+  static constexpr uint32_t scales = COLS ? kScaleSlots * kSlotFloats * 4 : 0;
+  static constexpr int bars = 2 * stages + 4 + 2 * kScaleSlots;
+  static constexpr size_t smem = ring + out + scales + bars * 8 + 16 + 1024;
+};
 constexpr int kPairGroup = 8;  // tile rows that are walked together, so that CTAs at work share panels in L2
 
 struct PairTile {
@@ -265,19 +270,20 @@ __device__ __forceinline__ PairTile pair_tile(const Gemm8Params& p, int t) {
 }
 
 template <bool COLS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::threads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                 const __grid_constant__ CUtensorMap map_out, const Gemm8Params p) {
+  using S = PairShape8<COLS>;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   unsigned char* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);  // the same offset in both CTAs
   const uint32_t sbase = smem_addr(smem);
-  const uint32_t a_base = sbase, b_base = sbase + kPairStages * kPairABytes;
-  float* scales = reinterpret_cast<float*>(smem + kPairRing + kPairOut);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kPairRing + kPairOut + kPairScales);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kPairBars);
-  const uint32_t full0 = smem_addr(&bars[0]), empty0 = smem_addr(&bars[kPairStages]);
-  const uint32_t acc_full0 = smem_addr(&bars[2 * kPairStages]), acc_empty0 = acc_full0 + 16;
+  const uint32_t a_base = sbase, b_base = sbase + S::stages * kPairABytes;
+  float* scales = reinterpret_cast<float*>(smem + S::ring + S::out);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::ring + S::out + S::scales);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + S::bars);
+  const uint32_t full0 = smem_addr(&bars[0]), empty0 = smem_addr(&bars[S::stages]);
+  const uint32_t acc_full0 = smem_addr(&bars[2 * S::stages]), acc_empty0 = acc_full0 + 16;
   const uint32_t sc_full0 = acc_full0 + 32, sc_empty0 = sc_full0 + 8 * kScaleSlots;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_cta_rank();
@@ -285,17 +291,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairStages; ++s) {
+    for (int s = 0; s < S::stages; ++s) {
       mbar_init(full0 + 8 * s, 1);   // even CTA: its producer's arrive + both CTAs' bytes
       mbar_init(empty0 + 8 * s, 1);  // one multicast commit
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(acc_full0 + 8 * a, 1);    // one multicast commit
-      mbar_init(acc_empty0 + 8 * a, 16);  // even CTA: 8 epilogue warps in each CTA
+      mbar_init(acc_empty0 + 8 * a, 2 * S::warps);  // even CTA: the epilogue warps of both CTAs
     }
     for (int s = 0; s < kScaleSlots; ++s) {
       mbar_init(sc_full0 + 8 * s, 2);  // the two scale warps
-      mbar_init(sc_empty0 + 8 * s, 8);  // this CTA's epilogue warps
+      mbar_init(sc_empty0 + 8 * s, S::warps);  // this CTA's epilogue warps
     }
     fence_barrier_init();
     tma_prefetch_map(&map_x);
@@ -313,7 +319,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   pdl_wait();
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (COLS) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0 && lane == 0) {
       // ---------------- TMA producer (both CTAs) ----------------
       uint32_t g = 0;
@@ -322,8 +329,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const PairTile w = pair_tile(p, t);
         const int x_row = (int)w.row0 + (int)rank * 128, w_row = (int)w.col0 + (int)rank * (w.cols / 2);
         for (int kb = 0; kb < p.KB; ++kb, ++g) {
-          const uint32_t s = g % kPairStages;
-          if (!mbar_wait(empty0 + 8 * s, ((g / kPairStages) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+          const uint32_t s = g % S::stages;
+          if (!mbar_wait(empty0 + 8 * s, ((g / S::stages) & 1u) ^ 1u, p.timeout_ns, p.status)) {
             ok = false;
             break;
           }
@@ -334,8 +341,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       }
       if (rank == 0)  // the pair's copies of the last blocks must have landed before exit
-        for (uint32_t j = (g > (uint32_t)kPairStages ? g - kPairStages : 0u); j < g; ++j)
-          mbar_wait(full0 + 8 * (j % kPairStages), (j / kPairStages) & 1u, p.timeout_ns, p.status);
+        for (uint32_t j = (g > (uint32_t)S::stages ? g - S::stages : 0u); j < g; ++j)
+          mbar_wait(full0 + 8 * (j % S::stages), (j / S::stages) & 1u, p.timeout_ns, p.status);
     } else if (warp == 1 && rank == 0) {
       // ---------------- MMA issuer (even CTA) ----------------
       // One warp issues everything, so what it does for a block of k is kept short: ring
@@ -367,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           __syncwarp();
           acc ^= 1;
           acc_phase ^= acc == 0;
-          if (++s == kPairStages) {
+          if (++s == S::stages) {
             s = 0;
             s_phase ^= 1;
           }
@@ -422,10 +429,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               ok = false;
               break;
             }
-            // column 4 lane + i: pair (4 lane + i) % 8 / 2 of the 8 columns number lane / 2
+            // column 4 lane + i of a half: pair (4 lane + i) % 8 / 2 of 8 columns
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              float* dst = scales + slot * kSlotFloats + kRowFactors + h * 4 * kColGroup + 2 * (lane >> 1);
+              float* dst = scales + slot * kSlotFloats + kRowFactors + (2 * h + (lane >> 4)) * 4 * kColGroup + 2 * ((lane & 15) >> 1);
 #pragma unroll
               for (int i = 0; i < 4; i += 2)
                 *reinterpret_cast<float2*>(dst + ((lane & 1) * 2 + i / 2) * kColGroup) = make_float2(x[h][i].v[j], x[h][i + 1].v[j]);
@@ -439,30 +446,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else {
     // ---------------- epilogue ----------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * 128);
+    if constexpr (COLS) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    constexpr int WIDE = COLS ? 64 : 128;  // columns a warp
+    const int quarter = warp & 3, part = (warp - 4) >> 2;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(part * WIDE);
     const uint32_t acc_empty_even = map_to_cta(acc_empty0, 0);
-    unsigned char* box = smem + kPairRing + (warp - 4) * 4096;
+    unsigned char* box = smem + S::ring + (warp - 4) * 4096;
     uint32_t g = 0;
     bool ok = true;
     if constexpr (COLS) {
       // A thread keeps rows t, t + 8, t + 16, t + 24 of its warp's 32 (t = lane / 4) and the columns
-      // 8 i + 2 q, 8 i + 2 q + 1 (q = lane % 4) of its half: 4 row factors and 32 column factors for
-      // its 128 outputs.  (A row a thread instead takes 128 column factors a block from shared
-      // memory, whose bandwidth the MMA's operands already fill: scaled by rows on both sides,
-      // 8192^3 then took 799 us.)
+      // 8 i + 2 q, 8 i + 2 q + 1 (q = lane % 4) of its 64: 4 row factors and 16 column factors for its
+      // 64 outputs.  (8192^3 with both sides scaled by rows: a row of 128 columns a thread, each
+      // column factor read by every lane of every warp, 799 us: shared memory's bandwidth is what
+      // the MMA's operands already take; fragments of 128 columns on 8 warps 730.)
       const int t4 = lane >> 2, q = lane & 3;
       const float* row_factors = scales + quarter * 32 + t4;
-      const float* col_factors = scales + kRowFactors + (half * 4 + q) * kColGroup;
+      const float* col_factors = scales + kRowFactors + (part * 4 + q) * kColGroup;
       for (int t = pair; ok && t < p.num_tiles; t += pairs) {
         const PairTile w = pair_tile(p, t);
         const int64_t row = w.row0 + (int)rank * 128 + quarter * 32;  // the warp's first
-        const int64_t col = w.col0 + half * 128;
-        const int mine = w.cols - half * 128;  // columns of this half (may be none)
-        float acc[128];
+        const int64_t col = w.col0 + part * WIDE;
+        const int mine = w.cols - part * WIDE;  // columns of this warp (may be none)
+        float acc[64];
 #pragma unroll
-        for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+        for (int i = 0; i < 64; ++i) acc[i] = 0.f;
 #pragma unroll 1
         for (int kb = 0; kb < p.KB; ++kb, ++g) {
           const uint32_t buf = g & 1u, slot = g % kScaleSlots;
@@ -480,31 +489,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
           tc_fence_after();
           const float4* cf = reinterpret_cast<const float4*>(col_factors + slot * kSlotFloats);
-          // All 128 columns always: those past a narrow tile's hold what nobody stores.  (The
-          // other warp of this SM quarter adds while this one loads.)
+          // All 64 columns always: those past a narrow tile's hold what nobody stores.  (The other
+          // warps of this SM quarter add while this one loads.)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t r[32];
-            tmem_ld_frag_sync(lanes + buf * 256 + 32 * c, r);
+            uint32_t r[16];
+            tmem_ld_frag_sync(lanes + buf * 256 + 16 * c, r);
             if (c == 3) {  // all read: this warp's share of the buffer is free
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
             }
+            const float4 f = cf[c];
 #pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              const float4 f = cf[2 * c + i / 2];
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {  // row t + 8 u
-                const int o = 16 * (u >> 1) + 2 * (u & 1) + 4 * i;
-                float* a = &acc[32 * c + o];
-                const float v0 = __uint_as_float(r[o]), v1 = __uint_as_float(r[o + 1]), v2 = __uint_as_float(r[o + 4]),
-                            v3 = __uint_as_float(r[o + 5]);
-                a[0] = __fmaf_rn(__fmul_rn(v0, f.x), sr[u], a[0]);
-                a[1] = __fmaf_rn(__fmul_rn(v1, f.y), sr[u], a[1]);
-                a[4] = __fmaf_rn(__fmul_rn(v2, f.z), sr[u], a[4]);
-                a[5] = __fmaf_rn(__fmul_rn(v3, f.w), sr[u], a[5]);
-              }
+            for (int u = 0; u < 4; ++u) {  // row t + 8 u
+              const int o = 8 * (u >> 1) + 2 * (u & 1);
+              float* a = &acc[16 * c + o];
+              a[0] = __fmaf_rn(__fmul_rn(__uint_as_float(r[o]), f.x), sr[u], a[0]);
+              a[1] = __fmaf_rn(__fmul_rn(__uint_as_float(r[o + 1]), f.y), sr[u], a[1]);
+              a[4] = __fmaf_rn(__fmul_rn(__uint_as_float(r[o + 4]), f.z), sr[u], a[4]);
+              a[5] = __fmaf_rn(__fmul_rn(__uint_as_float(r[o + 5]), f.w), sr[u], a[5]);
             }
           }
           __syncwarp();
@@ -513,24 +517,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (!ok) break;
         const bool f32 = p.out_dtype == FAR_F32;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (mine <= 32 * c) break;
-          if (f32 || (c & 1) == 0) begin_box(p, lane);
+        for (int c = 0; c < 4; ++c) {  // 16 columns
+          if (mine <= 16 * c) break;
+          if (c == 0 || (f32 && c == 2)) begin_box(p, lane);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              const float* a = &acc[32 * c + 16 * (u >> 1) + 2 * (u & 1) + 4 * i];
+              const float* a = &acc[16 * c + 8 * (u >> 1) + 2 * (u & 1) + 4 * i];
               unsigned char* line = box + (t4 + 8 * u) * 128;  // row t4 + 8 u: its units are permuted by t4
               if (f32) {
-                *reinterpret_cast<float2*>(line + (((2 * i + (q >> 1)) ^ t4) * 16) + (q & 1) * 8) = make_float2(a[0], a[1]);
+                *reinterpret_cast<float2*>(line + (((4 * (c & 1) + 2 * i + (q >> 1)) ^ t4) * 16) + (q & 1) * 8) = make_float2(a[0], a[1]);
               } else {
                 const uint32_t v = p.out_dtype == FAR_F16 ? narrow2<FAR_F16>(a[0], a[1]) : narrow2<FAR_BF16>(a[0], a[1]);
-                *reinterpret_cast<uint32_t*>(line + (((4 * (c & 1) + i) ^ t4) * 16) + q * 4) = v;
+                *reinterpret_cast<uint32_t*>(line + (((2 * c + i) ^ t4) * 16) + q * 4) = v;
               }
             }
-          if (f32 || (c & 1) == 1 || mine <= 32 * (c + 1))
-            store_box(p, &map_out, box, lane, row, col + (f32 ? 32 * c : 64 * (c / 2)));
+          if (c == 3 || (f32 && c == 1) || mine <= 16 * (c + 1))
+            store_box(p, &map_out, box, lane, row, col + (f32 ? 32 * (c / 2) : 0));
         }
       }
     } else {
@@ -538,8 +542,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int t = pair; ok && t < p.num_tiles; t += pairs) {
         const PairTile w = pair_tile(p, t);
         const int64_t row = w.row0 + (int)rank * 128 + quarter * 32 + lane;
-        const int64_t col = w.col0 + half * 128;
-        const int mine = w.cols - half * 128;  // columns of this half (may be none)
+        const int64_t col = w.col0 + part * WIDE;
+        const int mine = w.cols - part * WIDE;  // columns of this half (may be none)
         const float* xrow = row < p.M ? p.xs + row * p.KB : nullptr;
         const float* wrow = col < p.N ? p.ws + col / kBlock * p.KB : nullptr;
         Scale4 xn, wn;
@@ -933,10 +937,10 @@ cudaError_t launch_small(const CUtensorMap& mx, const CUtensorMap& mw, const Gem
 template <bool COLS>
 cudaError_t launch_pair(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& mo, const Gemm8Params& p, int sms,
                         cudaStream_t s) {
-  cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(pair_kernel<COLS>), kPairSmem);
+  cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(pair_kernel<COLS>), PairShape8<COLS>::smem);
   if (e != cudaSuccess) return e;
   const int pairs = p.num_tiles < sms / 2 ? p.num_tiles : sms / 2;
-  return launch_k(pair_kernel<COLS>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, s, mx, mw, mo, p);
+  return launch_k(pair_kernel<COLS>, dim3(2 * pairs), dim3(PairShape8<COLS>::threads), PairShape8<COLS>::smem, s, mx, mw, mo, p);
 }
 
 int run_gemm8(Gemm8Params& p, void* stream) {

@@ -181,20 +181,16 @@ __device__ __forceinline__ void tmem_ld32_sync(uint32_t taddr, uint32_t (&r)[32]
       : "r"(taddr)
       : "memory");
 }
-// All 32 lanes x 32 columns in the layout of a matrix fragment: with q = lane % 4 and
-// t = lane / 4, register 16 h + 4 i + 2 u + e holds TMEM lane (base + 16 h + 8 u + t), column
-// 8 i + 2 q + e: a thread gets 8 columns of 4 rows instead of 32 of one.
-__device__ __forceinline__ void tmem_ld_frag_sync(uint32_t taddr, uint32_t (&r)[32]) {
+// All 32 lanes x 16 columns in the layout of a matrix fragment: with q = lane % 4 and
+// t = lane / 4, register 8 h + 4 i + 2 u + e holds TMEM lane (base + 16 h + 8 u + t), column
+// 8 i + 2 q + e: a thread gets 4 columns of 4 rows instead of 16 of one.
+__device__ __forceinline__ void tmem_ld_frag_sync(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15}, [%32];\n\t"
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%33];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr), "r"(taddr + (16u << 16))
       : "memory");
 }

@@ -479,16 +479,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::th
             ok = false;
             break;
           }
+          // Every trip to shared memory takes ~300 cycles here, behind the MMA's operands: the factors
+          // are read before the sums are waited for, the column factors two chunks ahead.
           const float* rf = row_factors + slot * kSlotFloats;
+          const float4* cf = reinterpret_cast<const float4*>(col_factors + slot * kSlotFloats);
           float sr[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) sr[u] = rf[8 * u];
+          float4 f = cf[0], f1 = cf[1];
           if (!mbar_wait(acc_full0 + 8 * buf, (g >> 1) & 1u, p.timeout_ns, p.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const float4* cf = reinterpret_cast<const float4*>(col_factors + slot * kSlotFloats);
           // All 64 columns always: those past a narrow tile's hold what nobody stores.  (The other
           // warps of this SM quarter add while this one loads.)
 #pragma unroll
@@ -500,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::th
               __syncwarp();
               if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
             }
-            const float4 f = cf[c];
+            const float4 f2 = c < 2 ? cf[c + 2] : f1;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {  // row t + 8 u
               const int o = 8 * (u >> 1) + 2 * (u & 1);
@@ -510,6 +513,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::th
               a[4] = __fmaf_rn(__fmul_rn(__uint_as_float(r[o + 4]), f.z), sr[u], a[4]);
               a[5] = __fmaf_rn(__fmul_rn(__uint_as_float(r[o + 5]), f.w), sr[u], a[5]);
             }
+            f = f1;
+            f1 = f2;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(sc_empty0 + 8 * slot);

@@ -226,7 +226,7 @@ __device__ __forceinline__ void store_box(const Gemm8Params& p, const CUtensorMa
 // pair_kernel: 256 x 256 output tiles over a cluster of 2.  Each CTA holds its 128 rows of x
 // and half of the tile's rows of wt (up to 128) per block of k; one thread of the even CTA issues
 // tcgen05.mma.cta_group::2 over both, each CTA's TMEM receiving the sums of its 128 rows.
-//   warp 0      TMA producer (both CTAs), a ring of kPairStages blocks of k running across tiles
+//   warp 0      TMA producer (both CTAs), a ring of 4 or 5 blocks of k running across tiles
 //   warp 1      MMA issuer (even CTA); allocates TMEM: two halves of 256 columns
 //   warps 2, 3  where wt is scaled by rows: column and row factors, some blocks of k ahead
 //   warps 4-    epilogue: warp w the TMEM lanes 32 (w % 4) .. and 128 or (row-scaled wt) 64 of the
@@ -235,6 +235,13 @@ __device__ __forceinline__ void store_box(const Gemm8Params& p, const CUtensorMa
 // the 8 epilogue warps take 216 (128 x 72 + 256 x 216 = 384 x 168).  With 16 epilogue warps
 // 640 at 96, then 56 and 104 (128 x 56 + 512 x 104 = 60416 of 61440).
 // The last column of tiles runs at the width that is left (a multiple of 32).
+// Measured: 16384 x 8192 x 8192, tile-scaled wt, bf16 out 760 to 870 us with the codes' power draw
+// (2.5 to 2.9 PFLOP/s; the same pipeline without promotion 3.7 on 8192^3), 5120 x 2056 x 4112
+// row-scaled 84 us.  Bound by the MMA (750 cycles a block beside the epilogue's TMEM loads,
+// 512 alone) and by the two hand-overs of a TMEM half, of which a block hides only the other half's
+// MMA: two halves of 256 columns are all of TMEM.  Row-scaled also by two FMA-pipe operations
+// an output and block, and TMEM loads in fragments, which run at half rate (32 cycles for 32
+// columns against 16.5).
 // ---------------------------------------------------------------------------
 constexpr uint32_t kPairABytes = 128 * kBlock, kPairBBytes = 128 * kBlock;
 // A slot of the scale ring (wt scaled by rows): the 128 rows' factors, then for each 64 columns
@@ -548,7 +555,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::th
         const PairTile w = pair_tile(p, t);
         const int64_t row = w.row0 + (int)rank * 128 + quarter * 32 + lane;
         const int64_t col = w.col0 + part * WIDE;
-        const int mine = w.cols - part * WIDE;  // columns of this half (may be none)
+        const int mine = w.cols - part * WIDE;  // columns of this warp (may be none)
         const float* xrow = row < p.M ? p.xs + row * p.KB : nullptr;
         const float* wrow = col < p.N ? p.ws + col / kBlock * p.KB : nullptr;
         Scale4 xn, wn;
@@ -629,6 +636,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::th
 //   sums of one row of wt.
 // Then each CTA leaves its sums in its shared memory and adds up every S-th row of x over the
 // cluster's CTAs, in the order of k.
+// Bound by reading wt: m = 4, 8192 x 8192 13.0 us (5.2 TB/s), 28672 x 4096 20.7 us (5.7 TB/s); the
+// rest is the launch, the set-up and the sum over the cluster (about 3 us).  Two CTAs an SM with
+// five blocks in flight each and as many CTAs as fit: 1 CTA an SM with 6 or 11 blocks 15.5 and
+// 14.9 us, 8192 x 8192 shared out over 2 or 8 CTAs instead of 4 15.6 and 17.4.
 // ---------------------------------------------------------------------------
 constexpr int kSmallThreads = 256;
 template <int NT>

@@ -73,6 +73,26 @@ def test_norm_plans(far, act, tokens, hidden):
     check_norm(far, far_gen.custom_inputs(act, act, tokens, hidden, seed=tokens, scale_lo=1e-2, scale_hi=50), f"{act} {tokens}x{hidden}")
 
 
+def test_norm_schedules_and_plans(far):
+    """Claimed rows (modes 0 and 2) and forced plans give the fixed stride's bits."""
+    d = far_gen.custom_inputs("bf16", "bf16", 2500, 4096, seed=3)
+    x, r, w = d["x"].cuda(), d["r"].cuda(), d["w"].cuda()
+    want = far.fused_add_rmsnorm_quant_block(x, r, w, 1e-6) + far.rmsnorm_quant_block(x, w, 1e-6)
+    same = lambda got: all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))  # noqa: E731
+    run = lambda: far.fused_add_rmsnorm_quant_block(x, r, w, 1e-6) + far.rmsnorm_quant_block(x, w, 1e-6)  # noqa: E731
+    try:
+        for mode in (0, 2):
+            far.set_row_schedule(mode)
+            assert same(run()), f"schedule {mode}"
+        far.set_row_schedule(1)
+        for plan in [(1, 0, 0, 0), (0, 4, 1, 2), (0, 8, 1, 0), (0, 2, 0, 0)]:
+            far.set_launch_override(*plan)
+            assert same(run()), f"plan {plan}"
+    finally:
+        far.set_row_schedule(1)
+        far.set_launch_override()
+
+
 def test_norm_against_the_oracle(far):
     """The oracle's out quantised: residual_out and, wherever out agrees over a block, the block bit for bit."""
     d = far_gen.custom_inputs("bf16", "bf16", 64, 2048, seed=4)

@@ -132,6 +132,8 @@ def rope_table(rows: int, rot_dim: int, base: float = 10000.0, scaling: dict | N
     host = (ctypes.c_double * len(freq))(*freq)
     if torch.device(device).type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
+    if stream is not None and torch.device(device).index not in (None, stream.device.index):
+        raise ValueError("the stream belongs to another device than the tensors")
     with torch.cuda.device(device), torch.cuda.stream(stream):
         here = torch.cuda.current_stream()
         table = torch.empty((rows, rot_dim), dtype=torch.float32, device=here.device)

@@ -197,3 +197,12 @@ def test_table_refusals(far):
     f[3] = math.inf
     assert far.lib.rope_table(A, 8, 64, 0, a, 1.0, None) == 6
     assert far.lib.rope_table(None, 0, 64, 0, ctypes.addressof((ctypes.c_double * 32)()), 1.0, None) == 0
+
+
+def test_table_on_another_devices_stream(far):
+    """refused before anything is made: a table asked for on one device, with a stream of another"""
+    from types import SimpleNamespace
+
+    stream = SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="another device"):
+        far.rope_table(8, 64, device="cuda:0", stream=stream)

@@ -255,13 +255,15 @@ int rmsnorm_quant_strided(const void* x, int64_t x_row_stride, const void* weigh
  *               at or past table_rows is a caller error found on the device: its rows are
  *               written as NaN and far_device_status reports FAR_ERR_POSITION.
  *   q_out, k_out  as q and k, act, strides of their own; no two values may share a place
- *   tokens >= 0 (0 is a no-op), 1 <= head_dim <= 2048, 2 <= rot_dim <= head_dim (even)
+ *   0 <= tokens < 2^31 (0 is a no-op), 0 <= q_heads, k_heads <= 2^30, 1 <= head_dim <= 2048,
+ *               2 <= rot_dim <= head_dim (even)
  *   dtype       FAR_DTYPES(act, wd) for qk_norm_rope, the activations' dtype code for rope
  * In place (q_out exactly q: pointer and strides; likewise k) is allowed; otherwise an
  * output shares no byte with any other buffer (FAR_ERR_ALIAS).  FAR_ERR_SHAPE for sizes or
- * strides outside the above.  16-byte aligned heads of whole 16-byte chunks whose pairs
- * fall in whole chunks take the vector kernel, anything else a scalar one; the order of
- * the sums differs between the two, so their results may differ in the last place.
+ * strides outside the above and for a pointer off its elements' alignment.  16-byte aligned
+ * heads of whole 16-byte chunks whose pairs fall in whole chunks take the vector kernel,
+ * anything else a scalar one; the order of the sums differs between the two, so their
+ * results may differ in the last place.
  */
 #define FAR_PAIRS_HALF 0
 #define FAR_PAIRS_INTERLEAVED 1
@@ -355,7 +357,7 @@ int rope_table(float* table, int64_t rows, int64_t rot_dim, int64_t first_positi
  *   scale  [tokens, ceil(hidden / 128)] binary32, contiguous, device; dequantise a block as
  *          q * scale: the operand form of gemm_fp8_block's x
  * Row strides, aliasing and everything else as for the strided quantised forms (pass hidden
- * for contiguous rows).
+ * for contiguous rows); FAR_ERR_SHAPE also for a pointer off its elements' alignment.
  */
 int fused_add_rmsnorm_quant_block(const void* x, int64_t x_row_stride, const void* residual,
                                   int64_t residual_row_stride, const void* weight, float eps, void* q, float* scale,

@@ -334,6 +334,8 @@ int validate_quant(const void* x, const void* r, const void* w, float eps, void*
     return FAR_OK;
   }
   const int64_t sa = dsize(c.act);
+  if (block && (((uintptr_t)x | (uintptr_t)r | (uintptr_t)res_out) % sa || (uintptr_t)w % dsize(c.wd) || ((uintptr_t)scale & 3)))
+    return FAR_ERR_SHAPE;  // (r and res_out null without a residual)
   const Region Q = region(q, tokens, hidden, hidden);
   const int64_t scales = tokens * (block ? (hidden + kBlock - 1) / kBlock : 1);
   const Region S = region(scale, 1, scales * 4, scales * 4);

@@ -362,47 +362,47 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const QkParams 
   Turn<INTER, V> turn;
   int slot = 0;
   for (; !at.done(items); at.item += stride) {
-   at.start(parts, span, heads);
-   const int64_t pos = load_pos(p, at.t);
-   const bool ok = pos >= 0 && pos < p.table_rows;
-   if (pos >= p.table_rows && lane == 0) atomicOr(p.status, 1u << FAR_ERR_POSITION);
-   turn.load(p.table + (ok ? pos : 0) * p.rot, k, p.rot >> 1, p.sign);
-   char* y = S.y + at.t * S.yt + (int64_t)(at.h + grp) * S.yh;
-   for (; at.h < at.end; at.h += groups, y += yh) {
-    fetch(slot == 0 ? kQkSteps - 1 : slot - 1);
-    async_wait<kQkSteps - 1>();
-    const bool here = at.h + grp < at.end;
-    if (!ok) {  // (the whole warp)
-      if (here) store_bad(y, k, pos);
+    at.start(parts, span, heads);
+    const int64_t pos = load_pos(p, at.t);
+    const bool ok = pos >= 0 && pos < p.table_rows;
+    if (pos >= p.table_rows && lane == 0) atomicOr(p.status, 1u << FAR_ERR_POSITION);
+    turn.load(p.table + (ok ? pos : 0) * p.rot, k, p.rot >> 1, p.sign);
+    char* y = S.y + at.t * S.yt + (int64_t)(at.h + grp) * S.yh;
+    for (; at.h < at.end; at.h += groups, y += yh) {
+      fetch(slot == 0 ? kQkSteps - 1 : slot - 1);
+      async_wait<kQkSteps - 1>();
+      const bool here = at.h + grp < at.end;
+      if (!ok) {  // (the whole warp)
+        if (here) store_bad(y, k, pos);
+        if (++slot == kQkSteps) slot = 0;
+        continue;
+      }
+      Pair2<V> x;
+      widen2x<ACT, V>(take_chunk(mine + slot * 1024), x.a);
+      widen2x<ACT, V>(take_chunk(mine + slot * 1024 + 512), x.b);
+      if constexpr (NORM) {
+        X2 ss = X2{0.f, 0.f}, st = X2{0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+          ss = vfma(x.a[e], x.a[e], ss);
+          st = vfma(x.b[e], x.b[e], st);
+        }
+        const float r = head_rstd(head_sum(vadd(ss, st), L), p);
+        const X2 r2 = x2(r, r);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+          x.a[e] = vmul(vmul(x.a[e], r2), w.a[e]);
+          x.b[e] = vmul(vmul(x.b[e], r2), w.b[e]);
+        }
+      }
+      if (!NORM && p.sign < 0.f) turn.template apply<true>(x, k);
+      else turn.template apply<false>(x, k);
+      if (here) {
+        store_chunk<ACT, V>(y, k.ca, x.a);
+        store_chunk<ACT, V>(y, k.cb, x.b);
+      }
       if (++slot == kQkSteps) slot = 0;
-      continue;
     }
-    Pair2<V> x;
-    widen2x<ACT, V>(take_chunk(mine + slot * 1024), x.a);
-    widen2x<ACT, V>(take_chunk(mine + slot * 1024 + 512), x.b);
-    if constexpr (NORM) {
-      X2 ss = X2{0.f, 0.f}, st = X2{0.f, 0.f};
-#pragma unroll
-      for (int e = 0; e < V / 2; ++e) {
-        ss = vfma(x.a[e], x.a[e], ss);
-        st = vfma(x.b[e], x.b[e], st);
-      }
-      const float r = head_rstd(head_sum(vadd(ss, st), L), p);
-      const X2 r2 = x2(r, r);
-#pragma unroll
-      for (int e = 0; e < V / 2; ++e) {
-        x.a[e] = vmul(vmul(x.a[e], r2), w.a[e]);
-        x.b[e] = vmul(vmul(x.b[e], r2), w.b[e]);
-      }
-    }
-    if (!NORM && p.sign < 0.f) turn.template apply<true>(x, k);
-    else turn.template apply<false>(x, k);
-    if (here) {
-      store_chunk<ACT, V>(y, k.ca, x.a);
-      store_chunk<ACT, V>(y, k.cb, x.b);
-    }
-    if (++slot == kQkSteps) slot = 0;
-   }
   }
 }
 
@@ -504,62 +504,62 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_back_kernel(const QkPa
   Turn<INTER, V> turn;
   int slot = 0;
   for (; !at.done(items); at.item += stride) {
-   at.start(parts, span, heads);
-   const int64_t pos = load_pos(p, at.t);
-   const bool ok = pos >= 0 && pos < p.table_rows;
-   if (pos >= p.table_rows && lane == 0) atomicOr(p.status, 1u << FAR_ERR_POSITION);
-   turn.load(p.table + (ok ? pos : 0) * p.rot, k, p.rot >> 1, p.sign);
-   char* y = S.y + at.t * S.yt + (int64_t)(at.h + grp) * S.yh;
-   for (; at.h < at.end; at.h += groups, y += yh) {
-    fetch(slot == 0 ? kQkBackSteps - 1 : slot - 1);
-    async_wait<kQkBackSteps - 1>();
-    const bool here = at.h + grp < at.end;
-    if (!ok) {
-      if (here) store_bad(y, k, pos);
-      if (++slot == kQkBackSteps) slot = 0;
-      continue;
-    }
-    Pair2<V> x, g;
-    widen2x<ACT, V>(take_chunk(mine + slot * 2048), x.a);
-    widen2x<ACT, V>(take_chunk(mine + slot * 2048 + 512), x.b);
-    widen2x<ACT, V>(take_chunk(mine + slot * 2048 + 1024), g.a);
-    widen2x<ACT, V>(take_chunk(mine + slot * 2048 + 1536), g.b);
-    X2 ss = X2{0.f, 0.f}, st = X2{0.f, 0.f};
-#pragma unroll
-    for (int e = 0; e < V / 2; ++e) {
-      ss = vfma(x.a[e], x.a[e], ss);
-      st = vfma(x.b[e], x.b[e], st);
-    }
-    const float r = head_rstd(head_sum(vadd(ss, st), L), p);
-    const X2 r2 = x2(r, r);
-    turn.template apply<true>(g, k);
-    ss = st = X2{0.f, 0.f};
-#pragma unroll
-    for (int e = 0; e < V / 2; ++e) {
-      x.a[e] = vmul(x.a[e], r2);  // u = x r
-      x.b[e] = vmul(x.b[e], r2);
-      if (here) {
-        dw.a[e] = vfma(g.a[e], x.a[e], dw.a[e]);
-        dw.b[e] = vfma(g.b[e], x.b[e], dw.b[e]);
+    at.start(parts, span, heads);
+    const int64_t pos = load_pos(p, at.t);
+    const bool ok = pos >= 0 && pos < p.table_rows;
+    if (pos >= p.table_rows && lane == 0) atomicOr(p.status, 1u << FAR_ERR_POSITION);
+    turn.load(p.table + (ok ? pos : 0) * p.rot, k, p.rot >> 1, p.sign);
+    char* y = S.y + at.t * S.yt + (int64_t)(at.h + grp) * S.yh;
+    for (; at.h < at.end; at.h += groups, y += yh) {
+      fetch(slot == 0 ? kQkBackSteps - 1 : slot - 1);
+      async_wait<kQkBackSteps - 1>();
+      const bool here = at.h + grp < at.end;
+      if (!ok) {
+        if (here) store_bad(y, k, pos);
+        if (++slot == kQkBackSteps) slot = 0;
+        continue;
       }
-      g.a[e] = vmul(g.a[e], w.a[e]);  // h = g w
-      g.b[e] = vmul(g.b[e], w.b[e]);
-      ss = vfma(g.a[e], x.a[e], ss);
-      st = vfma(g.b[e], x.b[e], st);
-    }
-    const float m = -__fmul_rn(head_sum(vadd(ss, st), L), p.inv_dim);
-    const X2 m2 = x2(m, m);
+      Pair2<V> x, g;
+      widen2x<ACT, V>(take_chunk(mine + slot * 2048), x.a);
+      widen2x<ACT, V>(take_chunk(mine + slot * 2048 + 512), x.b);
+      widen2x<ACT, V>(take_chunk(mine + slot * 2048 + 1024), g.a);
+      widen2x<ACT, V>(take_chunk(mine + slot * 2048 + 1536), g.b);
+      X2 ss = X2{0.f, 0.f}, st = X2{0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < V / 2; ++e) {
-      x.a[e] = vmul(r2, vfma(x.a[e], m2, g.a[e]));
-      x.b[e] = vmul(r2, vfma(x.b[e], m2, g.b[e]));
+      for (int e = 0; e < V / 2; ++e) {
+        ss = vfma(x.a[e], x.a[e], ss);
+        st = vfma(x.b[e], x.b[e], st);
+      }
+      const float r = head_rstd(head_sum(vadd(ss, st), L), p);
+      const X2 r2 = x2(r, r);
+      turn.template apply<true>(g, k);
+      ss = st = X2{0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        x.a[e] = vmul(x.a[e], r2);  // u = x r
+        x.b[e] = vmul(x.b[e], r2);
+        if (here) {
+          dw.a[e] = vfma(g.a[e], x.a[e], dw.a[e]);
+          dw.b[e] = vfma(g.b[e], x.b[e], dw.b[e]);
+        }
+        g.a[e] = vmul(g.a[e], w.a[e]);  // h = g w
+        g.b[e] = vmul(g.b[e], w.b[e]);
+        ss = vfma(g.a[e], x.a[e], ss);
+        st = vfma(g.b[e], x.b[e], st);
+      }
+      const float m = -__fmul_rn(head_sum(vadd(ss, st), L), p.inv_dim);
+      const X2 m2 = x2(m, m);
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        x.a[e] = vmul(r2, vfma(x.a[e], m2, g.a[e]));
+        x.b[e] = vmul(r2, vfma(x.b[e], m2, g.b[e]));
+      }
+      if (here) {
+        store_chunk<ACT, V>(y, k.ca, x.a);
+        store_chunk<ACT, V>(y, k.cb, x.b);
+      }
+      if (++slot == kQkBackSteps) slot = 0;
     }
-    if (here) {
-      store_chunk<ACT, V>(y, k.ca, x.a);
-      store_chunk<ACT, V>(y, k.cb, x.b);
-    }
-    if (++slot == kQkBackSteps) slot = 0;
-   }
   }
   async_wait<0>();
   write_part<V>(p.parts + (int64_t)blockIdx.x * p.D, reinterpret_cast<float*>(ring), k, dw, L,
@@ -793,6 +793,7 @@ bool same_heads(const Heads& a, const Heads& b, int64_t tokens, int64_t heads) {
   return a.p == b.p && (tokens == 1 || a.ts == b.ts) && (heads == 1 || a.hs == b.hs);
 }
 
+constexpr int64_t kQkMaxHeads = int64_t(1) << 30;  // (a head's number, and the next steps', in 32 bits)
 constexpr int64_t kQkLimit = int64_t(1) << 40;  // strides and sizes: byte offsets stay far inside int64
 
 int validate_qk(const QkCall& c) {
@@ -805,7 +806,7 @@ int validate_qk(const QkCall& c) {
   if (c.tokens < 0 || c.heads[0] < 0 || c.heads[1] < 0 || c.D < 1 || c.D > kQkMaxDim || c.rot < 2 || c.rot > c.D ||
       c.rot % 2 != 0 || c.table_rows < 0)
     return FAR_ERR_SHAPE;
-  if (c.tokens > INT32_MAX || c.heads[0] > INT32_MAX || c.heads[1] > INT32_MAX || c.table_rows > kQkLimit)
+  if (c.tokens > INT32_MAX || c.heads[0] > kQkMaxHeads || c.heads[1] > kQkMaxHeads || c.table_rows > kQkLimit)
     return FAR_ERR_SHAPE;
   const int64_t es = esize(c.act);
   bool any = false;
@@ -829,9 +830,11 @@ int validate_qk(const QkCall& c) {
   if (c.table_rows == 0) return FAR_ERR_SHAPE;
   // element alignment of every pointer
   for (int i = 0; i < 2; ++i)
-    if (c.heads[i])
+    if (c.heads[i]) {
       for (const void* q : {c.x[i].p, (const void*)c.y[i].p, c.back ? c.g[i].p : nullptr})
         if ((uintptr_t)q % es) return FAR_ERR_SHAPE;
+      if ((c.norm && (uintptr_t)c.w[i] % esize(c.wd)) || (c.back && (uintptr_t)c.dw[i] % 4)) return FAR_ERR_SHAPE;
+    }
   if ((uintptr_t)c.table % 4 || (uintptr_t)c.pos % c.pos_bytes) return FAR_ERR_SHAPE;
   if (c.back && (!c.ws || c.ws_bytes < far_qk_backward_workspace_bytes(c.D) || ((uintptr_t)c.ws & 15)))
     return FAR_ERR_WORKSPACE;

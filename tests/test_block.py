@@ -35,6 +35,12 @@ def test_norm_refusals(far, kw, status):
     assert norm(far, **kw) == status
 
 
+@pytest.mark.parametrize("kw", [dict(x=A + 1), dict(r=A + MB + 1), dict(w=A + 2 * MB + 1), dict(ro=A + 5 * MB + 1),
+                                dict(s=A + 4 * MB + 2), dict(w=A + 2 * MB + 2, dt=0x02)])
+def test_norm_misaligned_elements(far, kw):
+    assert norm(far, **kw) == 4
+
+
 def test_norm_nothing_to_do(far):
     assert norm(far, n=0, x=None, r=None, q=None, s=None, ro=None) == 0
     assert far.lib.rmsnorm_quant_block(A, 512, A + MB, 1e-6, A + 2 * MB, None, 4, 512, 0x22, None) == 3

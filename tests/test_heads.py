@@ -67,6 +67,19 @@ def test_backward_refusals(far, kw, status):
     assert call(far, back=True, **kw) == status
 
 
+def test_misaligned_weights(far):
+    for back in (False, True):
+        assert call(far, back=back, qw=A + 2 * MB + 1) == 4 and call(far, back=back, kw=A + 3 * MB + 1) == 4
+        assert call(far, back=back, kw=A + 3 * MB + 2, dtype=0x02) == 4
+    assert call(far, back=True, dqw=A + 10 * MB + 2) == 4 and call(far, back=True, dkw=A + 11 * MB + 1) == 4
+
+
+def test_head_count_refusals(far):
+    for back in (False, True):
+        assert call(far, back=back, tokens=0, h=(1 << 30) + 1) == 4 and call(far, back=back, tokens=0, hk=(1 << 30) + 1) == 4
+    assert call(far, tokens=0, h=1 << 30, hk=1 << 30) == 0
+
+
 def test_rope_refusals(far):
     def rope(transpose=0, act=2, q=A, y=A + MB):
         return far.lib.rope(q, 64, 64, None, 0, 0, A + 4 * MB, 16, A + 5 * MB, 8, y, 64, 64, None, 0, 0, 4, 1, 0, 64, 64,

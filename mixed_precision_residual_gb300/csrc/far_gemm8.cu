@@ -125,19 +125,20 @@ __device__ __forceinline__ uint64_t pk_bits(uint32_t lo, uint32_t hi) {
 struct Scale4 {
   float v[4];
   // (volatile: the compiler would otherwise move the loads down to their use, four blocks of k
-  // later, and their latency with them)
+  // later, and their latency with them; plain, not ld.global.nc: the kernel ahead may write the
+  // scales while this grid is already resident, so they are not read-only for its lifetime)
   __device__ __forceinline__ void load(const float* row, int kb, int KB, bool vec) {
     if (row == nullptr || kb >= KB) {
       v[0] = v[1] = v[2] = v[3] = 0.f;
     } else if (vec) {
-      asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
+      asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
                    : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
                    : "l"(row + kb));
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         v[j] = 0.f;
-        if (kb + j < KB) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v[j]) : "l"(row + kb + j));
+        if (kb + j < KB) asm volatile("ld.global.f32 %0, [%1];" : "=f"(v[j]) : "l"(row + kb + j));
       }
     }
   }
@@ -145,6 +146,16 @@ struct Scale4 {
     return j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3];
   }
 };
+
+// one scale, or 0 where `on` is false: without a branch, so that a lane's loads leave together (volatile
+// and plain as Scale4's)
+__device__ __forceinline__ float load_scale(const float* src, bool on) {
+  float v;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.f32 %0, [%1];\n\t}"
+               : "=&f"(v)
+               : "l"(src), "r"((int)on));
+  return v;
+}
 
 // A ring of column scales in shared memory: slot kb % kScaleSlots holds the scales of block kb for
 // the tile's columns.  One warp fills it four blocks at a time (their values are neighbours
@@ -163,7 +174,7 @@ __device__ __forceinline__ bool fill_scales(float* ring, uint32_t full0, uint32_
       const bool in = c < COLS && first + c < rows;
       const float* src = scales + (first + c) * KB;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[i][j] = in && kb + j < kb1 ? __ldg(src + kb + j) : 0.f;
+      for (int j = 0; j < 4; ++j) v[i][j] = load_scale(src + kb + j, in && kb + j < kb1);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {

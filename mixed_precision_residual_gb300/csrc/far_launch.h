@@ -1,6 +1,8 @@
 // What the per-head and block-scaled operators' host code shares: a kernel launch with the
 // process's choice of programmatic dependent launch.  (Every such kernel waits for the
-// kernels ahead of it, griddepcontrol.wait, before it touches global memory.)
+// kernels ahead of it, griddepcontrol.wait, before it reads or writes global memory; the
+// product's small kernel only has lines of wt brought into L2 earlier.  No kernel reads
+// through the read-only path, ld.global.nc: what the kernel ahead writes is not read-only.)
 #pragma once
 
 #include <cuda_runtime.h>

@@ -34,11 +34,13 @@ struct QbParams {
 
 // 16 bytes, or zeros where `on` is false.  Volatile and without a branch: a thread's loads then
 // all leave before the first is waited for (a bf16 weight of 8192 x 8192 by tiles: 32.5 us, 6.2
-// TB/s; with each load under its branch 42.6).
+// TB/s; with each load under its branch 42.6).  Plain loads, not read-only ones (ld.global.nc): x may be
+// what the kernel ahead writes while this grid is already resident, so it is not read-only for the
+// grid's lifetime.
 __device__ __forceinline__ void load16(uint32_t (&w)[4], const void* src, bool on) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
-      "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      "mov.b32 %3, 0;\n\t@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
       : "=&r"(w[0]), "=&r"(w[1]), "=&r"(w[2]), "=&r"(w[3])
       : "l"(src), "r"((int)on));
 }
@@ -47,12 +49,12 @@ __device__ __forceinline__ void load16(uint32_t (&w)[4], const void* src, bool o
 template <int DT> __device__ __forceinline__ uint32_t load_bits(const void* base, int64_t i, bool on) {
   uint32_t v;
   if constexpr (DT == FAR_F32) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.b32 %0, [%1];\n\t}"
                  : "=&r"(v)
                  : "l"(static_cast<const float*>(base) + i), "r"((int)on));
   } else {
     uint16_t h;
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t@p ld.global.nc.b16 %0, [%1];\n\t}"
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t@p ld.global.b16 %0, [%1];\n\t}"
                  : "=&h"(h)
                  : "l"(static_cast<const uint16_t*>(base) + i), "r"((int)on));
     v = h;

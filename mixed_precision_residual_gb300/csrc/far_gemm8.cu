@@ -307,7 +307,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::th
   const uint32_t rank = cluster_cta_rank();
   const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
 
-  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::stages; ++s) {
       mbar_init(full0 + 8 * s, 1);   // even CTA: its producer's arrive + both CTAs' bytes
@@ -334,6 +333,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::th
   cluster_sync();  // both CTAs' barriers exist before any remote arrive or copy
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // Not before this CTA has its TMEM columns: a dependent kernel of any library that allocated them first
+  // and then waited for this grid would leave the allocation here, which has no time limit, waiting for it.
+  pdl_launch_dependents();
   pdl_wait();
 
   if (warp < 4) {
@@ -685,7 +687,6 @@ __global__ void __launch_bounds__(kSmallThreads, SmallShape<NT>::ctas)
   const int64_t n0 = (int64_t)blockIdx.y * 128, m0 = (int64_t)blockIdx.z * NT;
   const int kb0 = (int)((int64_t)p.KB * rank / split), kb1 = (int)((int64_t)p.KB * (rank + 1) / split);
 
-  pdl_launch_dependents();
   // The ring's first load of wt starts for L2 while the CTA is set up and the kernel ahead drains
   // (m = 4, 8192 x 8192: 13.2 us against 13.8; 2048 x 8192: 6.7 against 7.3; the CTA's whole
   // share instead: 13.6, and 24.3 against 20.7 on 28672 x 4096).
@@ -716,6 +717,7 @@ __global__ void __launch_bounds__(kSmallThreads, SmallShape<NT>::ctas)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();  // (not before the TMEM columns are this CTA's, as in pair_kernel)
   pdl_wait();
 
   bool ok = true;

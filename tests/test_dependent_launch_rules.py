@@ -22,3 +22,41 @@ def test_no_read_only_loads(name):
     pointer lets the compiler choose them: what the kernel ahead writes is not that."""
     found = re.findall(r"ld\.global\.nc|__ldg|ld\.global\.[a-z:.]*nc|__restrict__", code(SOURCES[name]))
     assert not found, f"{name}: {found}"
+
+
+def bodies(text):
+    """(name, body) of each kernel."""
+    text = code(text)
+    for m in re.finditer(r"__global__[^;{]*?\b(\w*_kernel)\s*\([^{;]*\)\s*\{", text):
+        depth, i = 1, m.end()
+        while depth:
+            depth += {"{": 1, "}": -1}.get(text[i], 0)
+            i += 1
+        yield m.group(1), text[m.end():i]
+
+
+def test_tensor_memory_is_taken_before_dependents_start():
+    """tcgen05.alloc waits without a limit for free columns.  A dependent kernel let in before this one has its own could
+    take them and then wait for this one to end: each CTA lets dependents go only behind its allocation and the
+    barrier that publishes it."""
+    met = []
+    for name, text in SOURCES.items():
+        for kernel, body in bodies(text):
+            alloc, go = re.search(r"tmem_alloc\w*\(", body), body.find("pdl_launch_dependents")
+            if alloc and go >= 0:
+                met.append(kernel)
+                between = body[alloc.end():go] if go > alloc.end() else ""
+                assert "__syncthreads" in between, f"{name}: {kernel} lets dependents go before its TMEM columns are its own"
+    assert {"pair_kernel", "small_kernel"} <= set(met)
+
+
+def test_every_kernel_waits_before_it_lets_its_results_be_read():
+    """A kernel that lets dependents go waits, itself, for the kernels ahead: else its dependents, which wait for it alone,
+    could run beside those."""
+    met = 0
+    for name, text in SOURCES.items():
+        for kernel, body in bodies(text):
+            if "pdl_launch_dependents" in body:
+                met += 1
+                assert "pdl_wait()" in body, f"{name}: {kernel}"
+    assert met >= 8

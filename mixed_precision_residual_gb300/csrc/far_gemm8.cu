@@ -360,9 +360,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::th
           tma_load_2d_pair(b_base + s * kPairBBytes, &map_w, kb * kBlock, w_row, full_even);
         }
       }
-      if (rank == 0)  // the pair's copies of the last blocks must have landed before exit
-        for (uint32_t j = (g > (uint32_t)S::stages ? g - S::stages : 0u); j < g; ++j)
+      // Before exit the pair's copies of the last blocks must have landed, and the commits that free their
+      // slots, which the MMA issuer multicasts last, must have arrived in both CTAs.
+      const uint32_t last = g > (uint32_t)S::stages ? g - S::stages : 0u;
+      if (rank == 0)
+        for (uint32_t j = last; j < g; ++j)
           mbar_wait(full0 + 8 * (j % S::stages), (j / S::stages) & 1u, p.timeout_ns, p.status);
+      for (uint32_t j = last; ok && j < g; ++j)
+        ok = mbar_wait(empty0 + 8 * (j % S::stages), (j / S::stages) & 1u, p.timeout_ns, p.status);
     } else if (warp == 1 && rank == 0) {
       // ---------------- MMA issuer (even CTA) ----------------
       // One warp issues everything, so what it does for a block of k is kept short: ring
@@ -725,15 +730,24 @@ __global__ void __launch_bounds__(kSmallThreads, SmallShape<NT>::ctas)
   if (warp == 0) {
     if (lane == 0) {
       uint32_t g = 0;
+      bool running = true;
       for (int kb = kb0; kb < kb1; ++kb, ++g) {
         const uint32_t s = g % S::stages;
-        if (!mbar_wait(empty0 + 8 * s, ((g / S::stages) & 1u) ^ 1u, p.timeout_ns, p.status)) break;
+        if (!mbar_wait(empty0 + 8 * s, ((g / S::stages) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+          running = false;
+          break;
+        }
         mbar_arrive_expect_tx(full0 + 8 * s, S::a_bytes + S::b_bytes);
         tma_load_2d(a_base + s * S::a_bytes, &map_w, kb * kBlock, (int)n0, full0 + 8 * s);
         tma_load_2d(b_base + s * S::b_bytes, &map_x, kb * kBlock, (int)m0, full0 + 8 * s);
       }
-      for (uint32_t j = (g > (uint32_t)S::stages ? g - S::stages : 0u); j < g; ++j)  // landed before anything else lies there
+      // Before anything else lies there the last blocks must have landed and their slots been freed by the
+      // MMA issuer's last commits (the barriers they arrive on go with the CTA).
+      const uint32_t last = g > (uint32_t)S::stages ? g - S::stages : 0u;
+      for (uint32_t j = last; j < g; ++j)
         mbar_wait(full0 + 8 * (j % S::stages), (j / S::stages) & 1u, p.timeout_ns, p.status);
+      for (uint32_t j = last; running && j < g; ++j)
+        running = mbar_wait(empty0 + 8 * (j % S::stages), (j / S::stages) & 1u, p.timeout_ns, p.status);
     }
   } else if (warp == 1) {
     constexpr uint32_t IDESC = umma_idesc_e4m3_f32(128, NT);

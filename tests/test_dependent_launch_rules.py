@@ -60,3 +60,16 @@ def test_every_kernel_waits_before_it_lets_its_results_be_read():
                 met += 1
                 assert "pdl_wait()" in body, f"{name}: {kernel}"
     assert met >= 8
+
+
+def test_commits_of_the_last_blocks_are_awaited():
+    """gemm_fp8_block's MMA issuer commits a block's sums first and its ring slot last.  Nobody needs the last slots again,
+    but a commit that arrives after its CTA (or its peer) has left would fall on another CTA's shared memory: the
+    producer, behind its loop over the blocks, waits for the slots that the loop left occupied."""
+    kernels = dict(bodies(SOURCES["far_gemm8.cu"]))
+    for name in ("pair_kernel", "small_kernel"):
+        body = kernels[name]
+        assert body.count("umma_commit") == 2
+        loop = body.index("mbar_arrive_expect_tx(full0")
+        issuer = body.index("elect_one()")
+        assert re.search(r"mbar_wait\(empty0 \+ 8 \* \(j % S::stages\), \(j / S::stages\) & 1u", body[loop:issuer]), name

@@ -398,7 +398,11 @@ int quant_block_fp8(const void* x, int64_t x_row_stride, void* q, float* scale, 
  *   out      [m, n] out_dtype (FAR_F32, FAR_F16, FAR_BF16), row stride >= n, device
  * Products of two codes are exact; a block's sum is taken by the tensor cores in binary32,
  * scaled and added to the others in binary32, in an order that is not specified but the
- * same every run.  NaN codes and scales give NaN; a zero scale with finite codes gives 0.
+ * same every run.  NaN codes and scales give NaN; a zero scale with finite codes (and a finite
+ * scale beside it) gives 0.  Scales may have any size: a block's term is right to a few units of
+ * 2^-24 wherever it lies in binary32's range, on every kernel.  (A scale other than 0 below
+ * 2^-108 or from 2^103 on, or a product of two outside binary32's normal numbers, costs the
+ * tiles beside it a second pass, with up to 64 rows of x one on the FMA pipe.)
  * Tensor cores (tcgen05) are used when the row strides of x and wt are multiples of 16 and
  * x and wt lie on 16-byte boundaries; any other call takes a plain kernel with the same
  * contract.  out shares no byte with another buffer.  k = 0 gives zeros; m = 0 or n = 0 is a

@@ -16,6 +16,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "far.h"
 #include "far_device.cuh"
 #include "far_launch.h"
@@ -59,6 +61,33 @@ __device__ __forceinline__ void store_out(const Gemm8Params& p, int64_t row, int
   else static_cast<__nv_bfloat16*>(p.out)[i] = __float2bfloat16_rn(v);
 }
 
+// A block's sum is 0 or of a magnitude between 2^-18 (two of the smallest codes) and 2^25 (128 x 448 x 448), and its
+// term is to be right wherever the term itself lies in binary32's range, whatever the two scales.
+// Multiplied by one scale and then by the other it is, if the first is 0 or within 2^-108 .. 2^103: that
+// product is then a normal number.  Multiplied by the scales' product it is, if that is a normal number,
+// or 0 because a scale is.  The kernels' loops take one of these ways; scales for which it fails, which
+// no quantiser makes of values that a model has, send a product through scaled().
+__device__ __forceinline__ bool first_factor(float s) {
+  const float m = fabsf(s);
+  return m == 0.f || (m >= 0x1p-108f && m < 0x1p103f);
+}
+__device__ __forceinline__ bool one_factor(float a, float b) {
+  const float m = fabsf(__fmul_rn(a, b));
+  return (m >= 0x1p-126f && m <= 0x1.fffffep127f) || a == 0.f || b == 0.f;
+}
+// The factors that a sum is multiplied by one after the other: the scales' product and 1 where that is
+// right; else the larger scale first.  (Product too small: the larger scale lies below 2^23, and where
+// it lies below 2^-108 the term is below half of binary32's smallest number; too large: neither scale
+// is below 1.  Infinite and NaN scales: the same as in any order.)
+__device__ __forceinline__ float2 factors(float a, float b) {
+  if (one_factor(a, b)) return make_float2(__fmul_rn(a, b), 1.f);
+  return fabsf(a) > fabsf(b) ? make_float2(a, b) : make_float2(b, a);
+}
+__device__ __forceinline__ float scaled(float sum, float a, float b) {
+  const float2 f = factors(a, b);
+  return __fmul_rn(__fmul_rn(sum, f.x), f.y);
+}
+
 // 64 x 64 outputs a CTA of 256 threads, 4 x 4 a thread (16 apart), slices of 32 along k through
 // shared memory as binary32.  Bound by the FMA pipe; there for the shapes TMA cannot read.
 __global__ void __launch_bounds__(256) plain_kernel(const Gemm8Params p) {
@@ -92,16 +121,25 @@ __global__ void __launch_bounds__(256) plain_kernel(const Gemm8Params p) {
             for (int j = 0; j < 4; ++j) part[i][j] = __fmaf_rn(a[i], c[j], part[i][j]);
         }
       }
+      float sx[4], sw[4];
+      bool usual = true;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + ty + 16 * i;
-        const float sx = m < p.M ? p.xs[m * p.KB + b] : 0.f;
+        const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * i;
+        sx[i] = m < p.M ? p.xs[m * p.KB + b] : 0.f;
+        sw[i] = n < p.N ? p.ws[(p.tile_scales ? n / kBlock : n) * p.KB + b] : 0.f;
+        usual = usual && first_factor(sx[i]);
+      }
+      if (usual) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t n = n0 + tx + 16 * j;
-          const float sw = n < p.N ? p.ws[(p.tile_scales ? n / kBlock : n) * p.KB + b] : 0.f;
-          acc[i][j] = __fmaf_rn(__fmul_rn(part[i][j], sx), sw, acc[i][j]);
-        }
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = __fmaf_rn(__fmul_rn(part[i][j], sx[i]), sw[j], acc[i][j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = __fadd_rn(acc[i][j], scaled(part[i][j], sx[i], sw[j]));
       }
     }
 #pragma unroll
@@ -156,6 +194,31 @@ __device__ __forceinline__ float load_scale(const float* src, bool on) {
                : "l"(src), "r"((int)on));
   return v;
 }
+
+// Words in shared memory behind a kernel's barriers: scales were met that its loop does not serve, so that its
+// tiles are done once more with scaled(), after the loop and at no cost to it; and a role's wait ran out, so
+// that nothing is done again.
+constexpr int kRare = 0, kGaveUp = 1, kFlags = 2;
+
+// The least (zeros aside) and the largest magnitude of scales, three operations each.
+struct Extent {
+  float least = 1.f, most = 0.f;
+  __device__ __forceinline__ void add(float s) {
+    const float m = fabsf(s);
+    least = fminf(least, m == 0.f ? 1.f : m);
+    most = fmaxf(most, m);
+  }
+  // n scales at p, a warp's lanes side by side
+  __device__ __forceinline__ void add(const float* p, int64_t n, int lane) {
+#pragma unroll 8
+    for (int64_t i = lane; i < n; i += 32) add(p[i]);
+  }
+  // of all lanes (the bits of magnitudes are in their order)
+  __device__ __forceinline__ void join() {
+    least = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(least)));
+    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+  }
+};
 
 // A ring of column scales in shared memory: slot kb % kScaleSlots holds the scales of block kb for
 // the tile's columns.  One warp fills it four blocks at a time (their values are neighbours
@@ -240,6 +303,8 @@ __device__ __forceinline__ void store_box(const Gemm8Params& p, const CUtensorMa
 //   warp 0      TMA producer (both CTAs), a ring of 4 or 5 blocks of k running across tiles
 //   warp 1      MMA issuer (even CTA); allocates TMEM: two halves of 256 columns
 //   warps 2, 3  where wt is scaled by rows: column and row factors, some blocks of k ahead
+//   warp 2 (wt scaled by tiles) or the odd CTA's warp 1 (by rows) looks for scales that the epilogue's loop does
+//               not serve (kRare); where it finds one, the pair does its tiles once more, with scaled()
 //   warps 4-    epilogue: warp w the TMEM lanes 32 (w % 4) .. and 128 or (row-scaled wt) 64 of the
 //               columns, so that a thread keeps 128 or 64 outputs in registers
 // The registers a thread: 384 threads are launched at 168; warps 0-3 give theirs up to 72 and
@@ -300,6 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::th
   float* scales = reinterpret_cast<float*>(smem + S::ring + S::out);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::ring + S::out + S::scales);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + S::bars);
+  volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t full0 = smem_addr(&bars[0]), empty0 = smem_addr(&bars[S::stages]);
   const uint32_t acc_full0 = smem_addr(&bars[2 * S::stages]), acc_empty0 = acc_full0 + 16;
   const uint32_t sc_full0 = acc_full0 + 32, sc_empty0 = sc_full0 + 8 * kScaleSlots;
@@ -308,6 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::th
   const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
+    for (int i = 0; i < kFlags; ++i) flags[i] = 0;
     for (int s = 0; s < S::stages; ++s) {
       mbar_init(full0 + 8 * s, 1);   // even CTA: its producer's arrive + both CTAs' bytes
       mbar_init(empty0 + 8 * s, 1);  // one multicast commit
@@ -338,136 +405,183 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::th
   pdl_launch_dependents();
   pdl_wait();
 
+  // a flag of both CTAs
+  auto tell = [&](int flag) {
+    const uint32_t at = smem_addr(const_cast<int*>(&flags[flag]));
+    for (uint32_t r = 0; r < 2; ++r)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_cta(at, r)), "r"(1) : "memory");
+  };
+  // The end of a role's pass over the pair's tiles: all of the pair are done with theirs (no CTA leaves while
+  // its peer may still signal its barriers).  Is there to be another?
+  auto again = [&]() {
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    return flags[kRare] != 0 && flags[kGaveUp] == 0;
+  };
+  // blocks of k behind the barriers before the second pass
+  const uint32_t done = pair < p.num_tiles ? (uint32_t)((p.num_tiles - pair + pairs - 1) / pairs) * (uint32_t)p.KB : 0u;
+
   if (warp < 4) {
     if constexpr (COLS) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 0 && lane == 0) {
-      // ---------------- TMA producer (both CTAs) ----------------
-      uint32_t g = 0;
+    auto role = [&](auto second) {
+      constexpr bool SECOND = decltype(second)::value;
       bool ok = true;
-      for (int t = pair; ok && t < p.num_tiles; t += pairs) {
-        const PairTile w = pair_tile(p, t);
-        const int x_row = (int)w.row0 + (int)rank * 128, w_row = (int)w.col0 + (int)rank * (w.cols / 2);
-        for (int kb = 0; kb < p.KB; ++kb, ++g) {
-          const uint32_t s = g % S::stages;
-          if (!mbar_wait(empty0 + 8 * s, ((g / S::stages) & 1u) ^ 1u, p.timeout_ns, p.status)) {
-            ok = false;
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * (kPairABytes + kPairBBytes));
-          const uint32_t full_even = map_to_cta(full0 + 8 * s, 0);
-          tma_load_2d_pair(a_base + s * kPairABytes, &map_x, kb * kBlock, x_row, full_even);
-          tma_load_2d_pair(b_base + s * kPairBBytes, &map_w, kb * kBlock, w_row, full_even);
-        }
-      }
-      // Before exit the pair's copies of the last blocks must have landed, and the commits that free their
-      // slots, which the MMA issuer multicasts last, must have arrived in both CTAs.
-      const uint32_t last = g > (uint32_t)S::stages ? g - S::stages : 0u;
-      if (rank == 0)
-        for (uint32_t j = last; j < g; ++j)
-          mbar_wait(full0 + 8 * (j % S::stages), (j / S::stages) & 1u, p.timeout_ns, p.status);
-      for (uint32_t j = last; ok && j < g; ++j)
-        ok = mbar_wait(empty0 + 8 * (j % S::stages), (j / S::stages) & 1u, p.timeout_ns, p.status);
-    } else if (warp == 1 && rank == 0) {
-      // ---------------- MMA issuer (even CTA) ----------------
-      // One warp issues everything, so what it does for a block of k is kept short: ring
-      // positions by counters, descriptors by adding to those of the first slot (16-byte units)
-      const bool leader = elect_one();
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint64_t a0 = sw128_kmajor_desc(a_base), b0 = sw128_kmajor_desc(b_base);
-      uint32_t s = 0, s_phase = 0, acc = 0, acc_phase = 1;
-      bool ok = true;
-      for (int t = pair; ok && t < p.num_tiles; t += pairs) {
-        const uint32_t idesc = umma_idesc_e4m3_f32(256, pair_tile(p, t).cols);
-        for (int kb = 0; kb < p.KB; ++kb) {
-          if (!mbar_wait(acc_empty0 + 8 * acc, acc_phase, p.timeout_ns, p.status) ||
-              !mbar_wait(full0 + 8 * s, s_phase, p.timeout_ns, p.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t a = a0 + s * (kPairABytes >> 4), b = b0 + s * (kPairBBytes >> 4);
-          const uint32_t d = tm + acc * 256;
-          if (leader) {
-            umma_e4m3_pair<false>(d, a, b, idesc);
-            umma_e4m3_pair<true>(d, a + 2, b + 2, idesc);
-            umma_e4m3_pair<true>(d, a + 4, b + 4, idesc);
-            umma_e4m3_pair<true>(d, a + 6, b + 6, idesc);
-            umma_commit_pair(acc_full0 + 8 * acc, 0x3);  // the block's sums are there
-            umma_commit_pair(empty0 + 8 * s, 0x3);       // both CTAs' slots are free once read
-          }
-          __syncwarp();
-          acc ^= 1;
-          acc_phase ^= acc == 0;
-          if (++s == S::stages) {
-            s = 0;
-            s_phase ^= 1;
-          }
-        }
-      }
-    } else if (COLS && warp == 3) {
-      // ---------------- row factors ----------------
-      uint32_t g = 0;
-      bool ok = true;
-      for (int t = pair; ok && t < p.num_tiles; t += pairs) {
-        const int64_t row0 = pair_tile(p, t).row0 + (int)rank * 128 + lane;
-        for (int kb = 0; ok && kb < p.KB; kb += 4) {
-          Scale4 x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i].load(row0 + 32 * i < p.M ? p.xs + (row0 + 32 * i) * p.KB : nullptr, kb, p.KB, p.xs_vec);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (kb + j >= p.KB) break;
-            const uint32_t slot = g % kScaleSlots;
-            if (!mbar_wait(sc_empty0 + 8 * slot, ((g / kScaleSlots) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+      uint32_t g = SECOND ? done : 0u;
+      if (warp == 0 && lane == 0) {
+        // ---------------- TMA producer (both CTAs) ----------------
+        for (int t = pair; ok && t < p.num_tiles; t += pairs) {
+          const PairTile w = pair_tile(p, t);
+          const int x_row = (int)w.row0 + (int)rank * 128, w_row = (int)w.col0 + (int)rank * (w.cols / 2);
+          for (int kb = 0; kb < p.KB; ++kb, ++g) {
+            const uint32_t s = g % S::stages;
+            if (!mbar_wait(empty0 + 8 * s, ((g / S::stages) & 1u) ^ 1u, p.timeout_ns, p.status)) {
               ok = false;
               break;
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) scales[slot * kSlotFloats + lane + 32 * i] = x[i].v[j];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sc_full0 + 8 * slot);
-            ++g;
+            if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * (kPairABytes + kPairBBytes));
+            const uint32_t full_even = map_to_cta(full0 + 8 * s, 0);
+            tma_load_2d_pair(a_base + s * kPairABytes, &map_x, kb * kBlock, x_row, full_even);
+            tma_load_2d_pair(b_base + s * kPairBBytes, &map_w, kb * kBlock, w_row, full_even);
           }
         }
-      }
-    } else if (COLS && warp == 2) {
-      // ---------------- column factors: a lane's 4 neighbouring columns of either half ----------------
-      uint32_t g = 0;
-      bool ok = true;
-      for (int t = pair; ok && t < p.num_tiles; t += pairs) {
-        const int64_t col0 = pair_tile(p, t).col0 + 4 * lane;
-        for (int kb = 0; ok && kb < p.KB; kb += 4) {
-          Scale4 x[2][4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int64_t c = col0 + 128 * h + i;
-              x[h][i].load(c < p.N ? p.ws + c * p.KB : nullptr, kb, p.KB, p.ws_vec);
-            }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (kb + j >= p.KB) break;
-            const uint32_t slot = g % kScaleSlots;
-            if (!mbar_wait(sc_empty0 + 8 * slot, ((g / kScaleSlots) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+        // Before exit the pair's copies of the last blocks must have landed, and the commits that free their
+        // slots, which the MMA issuer multicasts last, must have arrived in both CTAs.
+        const uint32_t last = g > (uint32_t)S::stages ? g - S::stages : 0u;
+        if (rank == 0)
+          for (uint32_t j = last; j < g; ++j)
+            mbar_wait(full0 + 8 * (j % S::stages), (j / S::stages) & 1u, p.timeout_ns, p.status);
+        for (uint32_t j = last; ok && j < g; ++j)
+          ok = mbar_wait(empty0 + 8 * (j % S::stages), (j / S::stages) & 1u, p.timeout_ns, p.status);
+      } else if (warp == 1 && rank == 0) {
+        // ---------------- MMA issuer (even CTA) ----------------
+        // One warp issues everything, so what it does for a block of k is kept short: ring
+        // positions by counters, descriptors by adding to those of the first slot (16-byte units)
+        const bool leader = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t a0 = sw128_kmajor_desc(a_base), b0 = sw128_kmajor_desc(b_base);
+        uint32_t s = g % S::stages, s_phase = g / S::stages & 1u, acc = g & 1u, acc_phase = (g >> 1 & 1u) ^ 1u;
+        for (int t = pair; ok && t < p.num_tiles; t += pairs) {
+          const uint32_t idesc = umma_idesc_e4m3_f32(256, pair_tile(p, t).cols);
+          for (int kb = 0; kb < p.KB; ++kb) {
+            if (!mbar_wait(acc_empty0 + 8 * acc, acc_phase, p.timeout_ns, p.status) ||
+                !mbar_wait(full0 + 8 * s, s_phase, p.timeout_ns, p.status)) {
               ok = false;
               break;
             }
-            // column 4 lane + i of a half: pair (4 lane + i) % 8 / 2 of 8 columns
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float* dst = scales + slot * kSlotFloats + kRowFactors + (2 * h + (lane >> 4)) * 4 * kColGroup + 2 * ((lane & 15) >> 1);
-#pragma unroll
-              for (int i = 0; i < 4; i += 2)
-                *reinterpret_cast<float2*>(dst + ((lane & 1) * 2 + i / 2) * kColGroup) = make_float2(x[h][i].v[j], x[h][i + 1].v[j]);
+            tc_fence_after();
+            const uint64_t a = a0 + s * (kPairABytes >> 4), b = b0 + s * (kPairBBytes >> 4);
+            const uint32_t d = tm + acc * 256;
+            if (leader) {
+              umma_e4m3_pair<false>(d, a, b, idesc);
+              umma_e4m3_pair<true>(d, a + 2, b + 2, idesc);
+              umma_e4m3_pair<true>(d, a + 4, b + 4, idesc);
+              umma_e4m3_pair<true>(d, a + 6, b + 6, idesc);
+              umma_commit_pair(acc_full0 + 8 * acc, 0x3);  // the block's sums are there
+              umma_commit_pair(empty0 + 8 * s, 0x3);       // both CTAs' slots are free once read
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(sc_full0 + 8 * slot);
-            ++g;
+            acc ^= 1;
+            acc_phase ^= acc == 0;
+            if (++s == S::stages) {
+              s = 0;
+              s_phase ^= 1;
+            }
+          }
+        }
+      } else if (COLS && warp == 3) {
+        // ---------------- row factors ----------------
+        for (int t = pair; ok && t < p.num_tiles; t += pairs) {
+          const int64_t row0 = pair_tile(p, t).row0 + (int)rank * 128 + lane;
+          for (int kb = 0; ok && kb < p.KB; kb += 4) {
+            Scale4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i].load(row0 + 32 * i < p.M ? p.xs + (row0 + 32 * i) * p.KB : nullptr, kb, p.KB, p.xs_vec);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (kb + j >= p.KB) break;
+              const uint32_t slot = g % kScaleSlots;
+              if (!mbar_wait(sc_empty0 + 8 * slot, ((g / kScaleSlots) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+                ok = false;
+                break;
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) scales[slot * kSlotFloats + lane + 32 * i] = x[i].v[j];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(sc_full0 + 8 * slot);
+              ++g;
+            }
+          }
+        }
+      } else if (COLS && warp == 2) {
+        // ---------------- column factors: a lane's 4 neighbouring columns of either half ----------------
+        for (int t = pair; ok && t < p.num_tiles; t += pairs) {
+          const int64_t col0 = pair_tile(p, t).col0 + 4 * lane;
+          for (int kb = 0; ok && kb < p.KB; kb += 4) {
+            Scale4 x[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int64_t c = col0 + 128 * h + i;
+                x[h][i].load(c < p.N ? p.ws + c * p.KB : nullptr, kb, p.KB, p.ws_vec);
+              }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (kb + j >= p.KB) break;
+              const uint32_t slot = g % kScaleSlots;
+              if (!mbar_wait(sc_empty0 + 8 * slot, ((g / kScaleSlots) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+                ok = false;
+                break;
+              }
+              // column 4 lane + i of a half: pair (4 lane + i) % 8 / 2 of 8 columns
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float* dst = scales + slot * kSlotFloats + kRowFactors + (2 * h + (lane >> 4)) * 4 * kColGroup + 2 * ((lane & 15) >> 1);
+#pragma unroll
+                for (int i = 0; i < 4; i += 2)
+                  *reinterpret_cast<float2*>(dst + ((lane & 1) * 2 + i / 2) * kColGroup) = make_float2(x[h][i].v[j], x[h][i + 1].v[j]);
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(sc_full0 + 8 * slot);
+              ++g;
+            }
+          }
+        }
+      } else if (!SECOND && warp == 1 + !COLS) {
+        // ---------------- are there scales that the epilogue's loop does not serve? ----------------
+        // (The odd CTA's MMA warp looks at the column factors; where wt is scaled by tiles, warp 2 at the products.)
+        for (int t = pair; t < p.num_tiles; t += pairs) {
+          const PairTile w = pair_tile(p, t);
+          if constexpr (COLS) {
+            Extent all;
+            all.add(p.ws + w.col0 * p.KB, (min((int64_t)p.N, w.col0 + 256) - w.col0) * p.KB, lane);
+            if (!(all.least >= 0x1p-108f && all.most < 0x1p103f)) tell(kRare);
+          } else {
+            const int64_t row0 = w.row0 + (int)rank * 128, rows = min((int64_t)p.M, row0 + 128) - row0;
+            const int64_t tile0 = w.col0 / kBlock, tiles = min(((int64_t)p.N + kBlock - 1) / kBlock, tile0 + 2) - tile0;
+            if (rows <= 0) continue;
+            Extent x, f;
+            x.add(p.xs + row0 * p.KB, rows * p.KB, lane);
+            f.add(p.ws + tile0 * p.KB, tiles * p.KB, lane);
+            x.join();
+            f.join();
+            if (one_factor(x.least, f.least) && one_factor(x.most, f.most)) continue;  // and all between
+            for (int64_t r = row0; r < row0 + rows; ++r)
+              for (int64_t h = tile0; h < tile0 + tiles; ++h)
+                for (int kb = lane; kb < p.KB; kb += 32)
+                  if (!one_factor(p.xs[r * p.KB + kb], p.ws[h * p.KB + kb])) tell(kRare);
           }
         }
       }
+      if (!ok) tell(kGaveUp);
+    };
+    role(std::false_type{});
+    if (again()) {
+      role(std::true_type{});
+      again();
     }
   } else {
     // ---------------- epilogue ----------------
@@ -478,169 +592,234 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::th
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(part * WIDE);
     const uint32_t acc_empty_even = map_to_cta(acc_empty0, 0);
     unsigned char* box = smem + S::ring + (warp - 4) * 4096;
-    uint32_t g = 0;
-    bool ok = true;
-    if constexpr (COLS) {
-      // A thread keeps rows t, t + 8, t + 16, t + 24 of its warp's 32 (t = lane / 4) and the columns
-      // 8 i + 2 q, 8 i + 2 q + 1 (q = lane % 4) of its 64: 4 row factors and 16 column factors for its
-      // 64 outputs.  (8192^3 with both sides scaled by rows: a row of 128 columns a thread, each
-      // column factor read by every lane of every warp, 799 us: shared memory's bandwidth is what
-      // the MMA's operands already take; fragments of 128 columns on 8 warps 730.)
-      const int t4 = lane >> 2, q = lane & 3;
-      const float* row_factors = scales + quarter * 32 + t4;
-      const float* col_factors = scales + kRowFactors + (part * 4 + q) * kColGroup;
-      for (int t = pair; ok && t < p.num_tiles; t += pairs) {
-        const PairTile w = pair_tile(p, t);
-        const int64_t row = w.row0 + (int)rank * 128 + quarter * 32;  // the warp's first
-        const int64_t col = w.col0 + part * WIDE;
-        const int mine = w.cols - part * WIDE;  // columns of this warp (may be none)
-        float acc[64];
+    auto role = [&](auto second) {
+      constexpr bool SECOND = decltype(second)::value;
+      uint32_t g = SECOND ? done : 0u;
+      bool ok = true;
+      if constexpr (COLS) {
+        // A thread keeps rows t, t + 8, t + 16, t + 24 of its warp's 32 (t = lane / 4) and the columns
+        // 8 i + 2 q, 8 i + 2 q + 1 (q = lane % 4) of its 64: 4 row factors and 16 column factors for its
+        // 64 outputs.  (8192^3 with both sides scaled by rows: a row of 128 columns a thread, each
+        // column factor read by every lane of every warp, 799 us: shared memory's bandwidth is what
+        // the MMA's operands already take; fragments of 128 columns on 8 warps 730.)
+        const int t4 = lane >> 2, q = lane & 3;
+        const float* row_factors = scales + quarter * 32 + t4;
+        const float* col_factors = scales + kRowFactors + (part * 4 + q) * kColGroup;
+        for (int t = pair; ok && t < p.num_tiles; t += pairs) {
+          const PairTile w = pair_tile(p, t);
+          const int64_t row = w.row0 + (int)rank * 128 + quarter * 32;  // the warp's first
+          const int64_t col = w.col0 + part * WIDE;
+          const int mine = w.cols - part * WIDE;  // columns of this warp (may be none)
+          float acc[64];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+          for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+          if constexpr (SECOND) {
 #pragma unroll 1
-        for (int kb = 0; kb < p.KB; ++kb, ++g) {
-          const uint32_t buf = g & 1u, slot = g % kScaleSlots;
-          if (!mbar_wait(sc_full0 + 8 * slot, (g / kScaleSlots) & 1u, p.timeout_ns, p.status)) {
-            ok = false;
-            break;
-          }
-          // Every trip to shared memory takes ~300 cycles here, behind the MMA's operands: the factors
-          // are read before the sums are waited for, the column factors two chunks ahead.
-          const float* rf = row_factors + slot * kSlotFloats;
-          const float4* cf = reinterpret_cast<const float4*>(col_factors + slot * kSlotFloats);
-          float sr[4];
+            for (int kb = 0; kb < p.KB; ++kb, ++g) {
+              const uint32_t buf = g & 1u, slot = g % kScaleSlots;
+              if (!mbar_wait(sc_full0 + 8 * slot, (g / kScaleSlots) & 1u, p.timeout_ns, p.status) ||
+                  !mbar_wait(acc_full0 + 8 * buf, (g >> 1) & 1u, p.timeout_ns, p.status)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
 #pragma unroll
-          for (int u = 0; u < 4; ++u) sr[u] = rf[8 * u];
-          float4 f = cf[0], f1 = cf[1];
-          if (!mbar_wait(acc_full0 + 8 * buf, (g >> 1) & 1u, p.timeout_ns, p.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          // All 64 columns always: those past a narrow tile's hold what nobody stores.  (The other
-          // warps of this SM quarter add while this one loads.)
+              for (int c = 0; c < 4; ++c) {
+                uint32_t r[16];
+                tmem_ld_frag_sync(lanes + buf * 256 + 16 * c, r);
+                const float4 f = reinterpret_cast<const float4*>(col_factors + slot * kSlotFloats)[c];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t r[16];
-            tmem_ld_frag_sync(lanes + buf * 256 + 16 * c, r);
-            if (c == 3) {  // all read: this warp's share of the buffer is free
+                for (int u = 0; u < 4; ++u) {
+                  const float sr = row_factors[slot * kSlotFloats + 8 * u];
+                  const int o = 8 * (u >> 1) + 2 * (u & 1);
+                  float* a = &acc[16 * c + o];
+                  a[0] = __fadd_rn(a[0], scaled(__uint_as_float(r[o]), f.x, sr));
+                  a[1] = __fadd_rn(a[1], scaled(__uint_as_float(r[o + 1]), f.y, sr));
+                  a[4] = __fadd_rn(a[4], scaled(__uint_as_float(r[o + 4]), f.z, sr));
+                  a[5] = __fadd_rn(a[5], scaled(__uint_as_float(r[o + 5]), f.w, sr));
+                }
+              }
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive_remote(acc_empty_even + 8 * buf);
+                mbar_arrive(sc_empty0 + 8 * slot);
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int kb = 0; kb < p.KB; ++kb, ++g) {
+              const uint32_t buf = g & 1u, slot = g % kScaleSlots;
+              if (!mbar_wait(sc_full0 + 8 * slot, (g / kScaleSlots) & 1u, p.timeout_ns, p.status)) {
+                ok = false;
+                break;
+              }
+              // Every trip to shared memory takes ~300 cycles here, behind the MMA's operands: the factors
+              // are read before the sums are waited for, the column factors two chunks ahead.
+              const float* rf = row_factors + slot * kSlotFloats;
+              const float4* cf = reinterpret_cast<const float4*>(col_factors + slot * kSlotFloats);
+              float sr[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) sr[u] = rf[8 * u];
+              float4 f = cf[0], f1 = cf[1];
+              if (!mbar_wait(acc_full0 + 8 * buf, (g >> 1) & 1u, p.timeout_ns, p.status)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              // All 64 columns always: those past a narrow tile's hold what nobody stores.  (The other
+              // warps of this SM quarter add while this one loads.)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t r[16];
+                tmem_ld_frag_sync(lanes + buf * 256 + 16 * c, r);
+                if (c == 3) {  // all read: this warp's share of the buffer is free
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
+                }
+                const float4 f2 = c < 2 ? cf[c + 2] : f1;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {  // row t + 8 u
+                  const int o = 8 * (u >> 1) + 2 * (u & 1);
+                  float* a = &acc[16 * c + o];
+                  a[0] = __fmaf_rn(__fmul_rn(__uint_as_float(r[o]), f.x), sr[u], a[0]);
+                  a[1] = __fmaf_rn(__fmul_rn(__uint_as_float(r[o + 1]), f.y), sr[u], a[1]);
+                  a[4] = __fmaf_rn(__fmul_rn(__uint_as_float(r[o + 4]), f.z), sr[u], a[4]);
+                  a[5] = __fmaf_rn(__fmul_rn(__uint_as_float(r[o + 5]), f.w), sr[u], a[5]);
+                }
+                f = f1;
+                f1 = f2;
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(sc_empty0 + 8 * slot);
+            }
+          }
+          if (!ok) break;
+          const bool f32 = p.out_dtype == FAR_F32;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {  // 16 columns
+            if (mine <= 16 * c) break;
+            if (c == 0 || (f32 && c == 2)) begin_box(p, lane);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float* a = &acc[16 * c + 8 * (u >> 1) + 2 * (u & 1) + 4 * i];
+                unsigned char* line = box + (t4 + 8 * u) * 128;  // row t4 + 8 u: its units are permuted by t4
+                if (f32) {
+                  *reinterpret_cast<float2*>(line + (((4 * (c & 1) + 2 * i + (q >> 1)) ^ t4) * 16) + (q & 1) * 8) = make_float2(a[0], a[1]);
+                } else {
+                  const uint32_t v = p.out_dtype == FAR_F16 ? narrow2<FAR_F16>(a[0], a[1]) : narrow2<FAR_BF16>(a[0], a[1]);
+                  *reinterpret_cast<uint32_t*>(line + (((2 * c + i) ^ t4) * 16) + q * 4) = v;
+                }
+              }
+            if (c == 3 || (f32 && c == 1) || mine <= 16 * (c + 1))
+              store_box(p, &map_out, box, lane, row, col + (f32 ? 32 * (c / 2) : 0));
+          }
+        }
+      } else {
+        // Scaled by tiles: a thread keeps one row's 128 columns, its factors (xs times ws) in registers.
+        for (int t = pair; ok && t < p.num_tiles; t += pairs) {
+          const PairTile w = pair_tile(p, t);
+          const int64_t row = w.row0 + (int)rank * 128 + quarter * 32 + lane;
+          const int64_t col = w.col0 + part * WIDE;
+          const int mine = w.cols - part * WIDE;  // columns of this warp (may be none)
+          const float* xrow = row < p.M ? p.xs + row * p.KB : nullptr;
+          const float* wrow = col < p.N ? p.ws + col / kBlock * p.KB : nullptr;
+          float acc[128];
+#pragma unroll
+          for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+          if constexpr (SECOND) {
+#pragma unroll 1
+            for (int kb = 0; kb < p.KB; ++kb, ++g) {
+              const uint32_t buf = g & 1u;
+              const float2 two = factors(xrow ? xrow[kb] : 0.f, wrow ? wrow[kb] : 0.f);
+              if (!mbar_wait(acc_full0 + 8 * buf, (g >> 1) & 1u, p.timeout_ns, p.status)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                uint32_t r[16];
+                tmem_ld16(lanes + buf * 256 + 16 * c, r);
+                tmem_ld_wait(r);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  acc[16 * c + i] = __fmaf_rn(__fmul_rn(__uint_as_float(r[i]), two.x), two.y, acc[16 * c + i]);
+              }
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
             }
-            const float4 f2 = c < 2 ? cf[c + 2] : f1;
+          } else {
+            Scale4 xn, wn;
+            xn.load(xrow, 0, p.KB, p.xs_vec);
+            wn.load(wrow, 0, p.KB, p.ws_vec);
+            for (int kb4 = 0; ok && kb4 < p.KB; kb4 += 4) {
+              Scale4 sc;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {  // row t + 8 u
-              const int o = 8 * (u >> 1) + 2 * (u & 1);
-              float* a = &acc[16 * c + o];
-              a[0] = __fmaf_rn(__fmul_rn(__uint_as_float(r[o]), f.x), sr[u], a[0]);
-              a[1] = __fmaf_rn(__fmul_rn(__uint_as_float(r[o + 1]), f.y), sr[u], a[1]);
-              a[4] = __fmaf_rn(__fmul_rn(__uint_as_float(r[o + 4]), f.z), sr[u], a[4]);
-              a[5] = __fmaf_rn(__fmul_rn(__uint_as_float(r[o + 5]), f.w), sr[u], a[5]);
-            }
-            f = f1;
-            f1 = f2;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sc_empty0 + 8 * slot);
-        }
-        if (!ok) break;
-        const bool f32 = p.out_dtype == FAR_F32;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {  // 16 columns
-          if (mine <= 16 * c) break;
-          if (c == 0 || (f32 && c == 2)) begin_box(p, lane);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float* a = &acc[16 * c + 8 * (u >> 1) + 2 * (u & 1) + 4 * i];
-              unsigned char* line = box + (t4 + 8 * u) * 128;  // row t4 + 8 u: its units are permuted by t4
-              if (f32) {
-                *reinterpret_cast<float2*>(line + (((4 * (c & 1) + 2 * i + (q >> 1)) ^ t4) * 16) + (q & 1) * 8) = make_float2(a[0], a[1]);
-              } else {
-                const uint32_t v = p.out_dtype == FAR_F16 ? narrow2<FAR_F16>(a[0], a[1]) : narrow2<FAR_BF16>(a[0], a[1]);
-                *reinterpret_cast<uint32_t*>(line + (((2 * c + i) ^ t4) * 16) + q * 4) = v;
-              }
-            }
-          if (c == 3 || (f32 && c == 1) || mine <= 16 * (c + 1))
-            store_box(p, &map_out, box, lane, row, col + (f32 ? 32 * (c / 2) : 0));
-        }
-      }
-    } else {
-      // Scaled by tiles: a thread keeps one row's 128 columns, its factors (xs times ws) in registers.
-      for (int t = pair; ok && t < p.num_tiles; t += pairs) {
-        const PairTile w = pair_tile(p, t);
-        const int64_t row = w.row0 + (int)rank * 128 + quarter * 32 + lane;
-        const int64_t col = w.col0 + part * WIDE;
-        const int mine = w.cols - part * WIDE;  // columns of this warp (may be none)
-        const float* xrow = row < p.M ? p.xs + row * p.KB : nullptr;
-        const float* wrow = col < p.N ? p.ws + col / kBlock * p.KB : nullptr;
-        Scale4 xn, wn;
-        xn.load(xrow, 0, p.KB, p.xs_vec);
-        wn.load(wrow, 0, p.KB, p.ws_vec);
-        float acc[128];
-#pragma unroll
-        for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-        for (int kb4 = 0; ok && kb4 < p.KB; kb4 += 4) {
-          Scale4 sc;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sc.v[j] = __fmul_rn(xn.v[j], wn.v[j]);
-          xn.load(xrow, kb4 + 4, p.KB, p.xs_vec);  // the next four blocks', while these are worked on
-          wn.load(wrow, kb4 + 4, p.KB, p.ws_vec);
+              for (int j = 0; j < 4; ++j) sc.v[j] = __fmul_rn(xn.v[j], wn.v[j]);
+              xn.load(xrow, kb4 + 4, p.KB, p.xs_vec);  // the next four blocks', while these are worked on
+              wn.load(wrow, kb4 + 4, p.KB, p.ws_vec);
 #pragma unroll 1
-          for (int j = 0; j < 4 && kb4 + j < p.KB; ++j, ++g) {
-            const uint32_t buf = g & 1u;
-            const float sr = sc.at(j);
-            if (!mbar_wait(acc_full0 + 8 * buf, (g >> 1) & 1u, p.timeout_ns, p.status)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            // All 128 columns always: those past a narrow tile's hold what nobody stores.  (The
-            // other warp of this SM quarter adds while this one loads.)
+              for (int j = 0; j < 4 && kb4 + j < p.KB; ++j, ++g) {
+                const uint32_t buf = g & 1u;
+                const float sr = sc.at(j);
+                if (!mbar_wait(acc_full0 + 8 * buf, (g >> 1) & 1u, p.timeout_ns, p.status)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                // All 128 columns always: those past a narrow tile's hold what nobody stores.  (The
+                // other warp of this SM quarter adds while this one loads.)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t r[32];
-              tmem_ld32_sync(lanes + buf * 256 + 32 * c, r);
-              if (c == 3) {  // all read: this warp's share of the buffer is free
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
+                for (int c = 0; c < 4; ++c) {
+                  uint32_t r[32];
+                  tmem_ld32_sync(lanes + buf * 256 + 32 * c, r);
+                  if (c == 3) {  // all read: this warp's share of the buffer is free
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
+                  }
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) acc[32 * c + i] = __fmaf_rn(__uint_as_float(r[i]), sr, acc[32 * c + i]);
+                }
               }
-#pragma unroll
-              for (int i = 0; i < 32; ++i) acc[32 * c + i] = __fmaf_rn(__uint_as_float(r[i]), sr, acc[32 * c + i]);
             }
           }
-        }
-        if (!ok) break;
-        const bool f32 = p.out_dtype == FAR_F32;
+          if (!ok) break;
+          const bool f32 = p.out_dtype == FAR_F32;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (mine <= 32 * c) break;
-          if (f32 || (c & 1) == 0) begin_box(p, lane);
-          uint32_t v[32];
-          if (f32) narrow<FAR_F32, 32>(acc + 32 * c, v);
-          else if (p.out_dtype == FAR_F16) narrow<FAR_F16, 32>(acc + 32 * c, v);
-          else narrow<FAR_BF16, 32>(acc + 32 * c, v);
+          for (int c = 0; c < 4; ++c) {
+            if (mine <= 32 * c) break;
+            if (f32 || (c & 1) == 0) begin_box(p, lane);
+            uint32_t v[32];
+            if (f32) narrow<FAR_F32, 32>(acc + 32 * c, v);
+            else if (p.out_dtype == FAR_F16) narrow<FAR_F16, 32>(acc + 32 * c, v);
+            else narrow<FAR_BF16, 32>(acc + 32 * c, v);
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            if (u < 4 || f32) {
-              const int unit = (f32 || (c & 1) == 0 ? u : u + 4) ^ (lane & 7);
-              *reinterpret_cast<uint4*>(box + lane * 128 + unit * 16) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+            for (int u = 0; u < 8; ++u) {
+              if (u < 4 || f32) {
+                const int unit = (f32 || (c & 1) == 0 ? u : u + 4) ^ (lane & 7);
+                *reinterpret_cast<uint4*>(box + lane * 128 + unit * 16) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+              }
             }
+            if (f32 || (c & 1) == 1 || mine <= 32 * (c + 1))
+              store_box(p, &map_out, box, lane, row - lane, col + (f32 ? 32 * c : 64 * (c / 2)));
           }
-          if (f32 || (c & 1) == 1 || mine <= 32 * (c + 1))
-            store_box(p, &map_out, box, lane, row - lane, col + (f32 ? 32 * c : 64 * (c / 2)));
         }
       }
+      if (lane == 0) bulk_wait_all();
+      if (!ok) tell(kGaveUp);
+    };
+    role(std::false_type{});
+    if (again()) {
+      role(std::true_type{});
+      again();
     }
-    if (lane == 0) bulk_wait_all();
   }
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();  // no CTA leaves while its peer may still signal its barriers
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
@@ -673,9 +852,51 @@ struct SmallShape {
   static_assert(NT * 128 * 4 <= ring, "the sums that the cluster adds up lie in the ring");
 };
 
+// small_kernel's tile over the CTA's blocks of k once more, on the FMA pipe and with scaled(): into the ring, or out
+// where the CTA has all of k.  (Its place comes from the special registers again: what the kernel's loop
+// keeps for it costs the loop registers, 3 to 5 % with 64 rows of x.)
+template <int NT>
+__device__ __forceinline__ void small_again(const Gemm8Params& p, float* sums) {
+  int split, rank, y, z;
+  asm volatile("mov.u32 %0, %%nctaid.x;\n\tmov.u32 %1, %%ctaid.x;\n\tmov.u32 %2, %%ctaid.y;\n\tmov.u32 %3, %%ctaid.z;"
+               : "=r"(split), "=r"(rank), "=r"(y), "=r"(z));
+  const int64_t n0 = (int64_t)y * 128, m0 = (int64_t)z * NT;
+  const int kb0 = (int)((int64_t)p.KB * rank / split), kb1 = (int)((int64_t)p.KB * (rank + 1) / split);
+  const int r = threadIdx.x & 127;
+  const int64_t n = n0 + r;
+  if (n >= p.N) return;
+  for (int c0 = 4 * (int)(threadIdx.x >> 7); c0 < NT && m0 + c0 < p.M; c0 += 8) {
+    const int cols = (int)min((int64_t)4, p.M - m0 - c0);
+    float acc[4] = {};
+#pragma unroll 1
+    for (int kb = kb0; kb < kb1; ++kb) {
+      float part[4] = {};
+      const int64_t end = min((int64_t)p.K, ((int64_t)kb + 1) * kBlock);
+#pragma unroll 1
+      for (int64_t k = (int64_t)kb * kBlock; k < end; ++k) {
+        const float w = e4m3_value(p.wt[n * p.ldw + k]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < cols) part[c] = __fmaf_rn(w, e4m3_value(p.x[(m0 + c0 + c) * p.ldx + k]), part[c]);
+      }
+      const float ws = p.ws[(p.tile_scales ? n / kBlock : n) * p.KB + kb];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < cols) acc[c] = __fadd_rn(acc[c], scaled(part[c], p.xs[(m0 + c0 + c) * p.KB + kb], ws));
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c >= cols) continue;
+      if (split > 1) sums[(c0 + c) * 128 + r] = acc[c];
+      else store_out(p, m0 + c0 + c, n, acc[c]);
+    }
+  }
+}
+
 template <int NT>
 __global__ void __launch_bounds__(kSmallThreads, SmallShape<NT>::ctas)
-    small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const Gemm8Params p) {
+    small_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                 const __grid_constant__ Gemm8Params p) {
   using S = SmallShape<NT>;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -684,6 +905,7 @@ __global__ void __launch_bounds__(kSmallThreads, SmallShape<NT>::ctas)
   float* scales = reinterpret_cast<float*>(smem + S::ring);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::ring + kScaleSlots * NT * 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + S::bars);
+  volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t full0 = smem_addr(&bars[0]), empty0 = full0 + 8 * S::stages;
   const uint32_t acc_full0 = empty0 + 8 * S::stages, acc_empty0 = acc_full0 + 8 * S::bufs;
   const uint32_t sc_full0 = acc_empty0 + 8 * S::bufs, sc_empty0 = sc_full0 + 8 * kScaleSlots;
@@ -698,6 +920,7 @@ __global__ void __launch_bounds__(kSmallThreads, SmallShape<NT>::ctas)
   if (warp == 3 && lane == 0)
     for (int kb = kb0; kb < kb1 && kb < kb0 + S::stages; ++kb) tma_prefetch_2d(&map_w, kb * kBlock, (int)n0);
   if (threadIdx.x == 0) {
+    for (int i = 0; i < kFlags; ++i) flags[i] = 0;
     for (int s = 0; s < S::stages; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
@@ -782,6 +1005,15 @@ __global__ void __launch_bounds__(kSmallThreads, SmallShape<NT>::ctas)
     }
   } else if (warp == 2) {
     fill_scales<NT>(scales, sc_full0, sc_empty0, p.xs, m0, p.M, kb0, kb1, p.KB, 0u, lane, p);
+  } else if (warp == 3) {
+    // are there scales of x that are no first_factor?
+    Extent all;
+    const int rows = (int)min((int64_t)NT, p.M - m0);
+    const unsigned per = (unsigned)(kb1 - kb0);
+    const float* first = p.xs + m0 * p.KB + kb0;
+#pragma unroll 8
+    for (unsigned i = lane; i < rows * per; i += 32) all.add(first[(int64_t)(i / per) * p.KB + i % per]);  // (64 x 2^24 at most)
+    if (!(all.least >= 0x1p-108f && all.most < 0x1p103f)) flags[kRare] = 1;
   } else if (warp >= 4) {
     const int quarter = warp & 3;
     const int64_t n = n0 + quarter * 32 + lane;
@@ -849,18 +1081,22 @@ __global__ void __launch_bounds__(kSmallThreads, SmallShape<NT>::ctas)
     tc_fence_after();
     tmem_dealloc(tmem, S::tmem_cols);
   }
-  if (split > 1) {
-    // every copy has landed and every MMA has read: the ring now holds this CTA's sums [NT][128]
-    float* sums = reinterpret_cast<float*>(smem);
+  // every copy has landed and every MMA has read: the ring now holds this CTA's sums [NT][128]
+  float* sums = reinterpret_cast<float*>(smem);
+  if (split > 1 && warp >= 4) {
     const int r = (int)threadIdx.x - 128;
-    if (warp >= 4) {
 #pragma unroll
-      for (int i = 0; i < NT / 2; ++i) {
-        const float2 f = unpk(acc[i]);
-        sums[(2 * i) * 128 + r] = f.x;
-        sums[(2 * i + 1) * 128 + r] = f.y;
-      }
+    for (int i = 0; i < NT / 2; ++i) {
+      const float2 f = unpk(acc[i]);
+      sums[(2 * i) * 128 + r] = f.x;
+      sums[(2 * i + 1) * 128 + r] = f.y;
     }
+  }
+  if (flags[kRare]) {
+    __syncthreads();
+    small_again<NT>(p, sums);
+  }
+  if (split > 1) {
     cluster_sync();
     const int64_t n = n0 + (threadIdx.x & 127);
     const uint32_t mine = smem_addr(sums) + (threadIdx.x & 127) * 4;

@@ -239,9 +239,10 @@ PyObject* qk_norm_rope_backward_(PyObject* const* a) {
   const Tensor* ws = maybe(a[12]);
   const Place place{&q, k, qw, kw, &table, &pos, gq, gk, maybe(a[10]), maybe(a[11]), ws};
   const Out yq = output(place, &q, a[10]), yk = output(place, k, a[11]);
-  const Tensor dqw = place.empty({s.dim}, at::ScalarType::Float);
-  Tensor dkw, own;
+  Tensor dqw = place.empty({s.dim}, at::ScalarType::Float), dkw, own;
   if (k) dkw = place.empty({s.dim}, at::ScalarType::Float);
+  if (s.q == 0) dqw.zero_();  // (the C entry point leaves the arguments of a half without heads alone)
+  if (k && s.k == 0) dkw.zero_();
   if (!ws) {
     const int64_t bytes = far_qk_backward_workspace_bytes(s.dim);
     if (bytes < 0) throw Status{(int)-bytes};

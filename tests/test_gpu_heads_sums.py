@@ -1,5 +1,5 @@
 """The gradients of qk_norm_rope where every sum is exact, so that one (token, head) left out or taken twice shows at any
-size."""
+size; and heads that are not there."""
 import pytest
 import torch
 
@@ -78,3 +78,26 @@ def test_every_head_counts_once(far, size, act, pairs):
         else:  # all terms carry r; a lane's chain, the warps', blocks' and rows' trees: at most 200 additions of 2^-24
             size = r * (live * turned.abs()).sum((0, 1))
             assert bool(((dw.double() - r * want).abs() <= 200 * 2.0 ** -24 * size).all())
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_no_query_or_no_key_heads(far, act):
+    """A tensor without heads: nothing to normalise, and zeros for its weight's gradient (not what lay in memory)."""
+    t, n, d = TYPES[act], 33, 128
+    table, pos = far.rope_table(64, d), torch.arange(n, device="cuda")
+    w = torch.ones(d, device="cuda", dtype=t)
+    some, none = torch.randn(n, 3, d, device="cuda").to(t), torch.empty(n, 0, d, device="cuda", dtype=t)
+    alone = far.qk_norm_rope_backward(some, None, some, None, w, None, 1e-6, table, pos)
+    for q, k, filled in ((some, none, 0), (none, some, 1), (none, none, None)):
+        y = far.qk_norm_rope(q, k, w, w, 1e-6, table, pos)
+        assert y[0].shape == q.shape and y[1].shape == k.shape
+        used = [torch.full((d,), float("nan"), device="cuda") for _ in range(64)]
+        torch.cuda.synchronize()
+        del used  # what the allocator hands out next holds NaN
+        got = far.qk_norm_rope_backward(q, k, q, k, w, w, 1e-6, table, pos)
+        assert far.device_status() == 0
+        for i in (0, 1):
+            if i == filled:
+                assert torch.equal(got[2 + i], alone[2]) and torch.equal(got[i], alone[0])
+            else:
+                assert bool((got[2 + i] == 0).all()) and got[i].numel() == 0

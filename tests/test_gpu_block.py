@@ -433,3 +433,26 @@ def test_attention_inputs_of_a_layer(far, tokens):
     assert bool(((dw.double() - full).abs() <= 0.13 * size + 1e-2 * size.mean()).all())
     assert dw.shape == weight.shape
     assert np.isfinite(float(dw.sum()))
+
+
+def test_quant_more_tile_rows_than_one_grid_axis(far):
+    """More than 32768 rows of tiles (blockIdx.z takes part): each tile's values depend on its own rows alone, so those
+    behind the first 32768 equal quantising them apart, which the definition checks."""
+    behind = 32768 * BLOCK
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(behind + 32768 + 200, 8, generator=g, device="cuda").half()
+    for block in ("row", "tile"):
+        for transpose in (False, True):
+            q, s = far.quant_block_fp8(x, block, transpose)
+            assert far.device_status() == 0
+            for cut in (slice(0, 384), slice(behind - 256, behind + 384), slice(behind + 32768 - 128, None)):
+                part = x[cut]
+                v, rs = quantise(part.cpu().T if transpose else part.cpu(), block)
+                lo = cut.start // BLOCK
+                if transpose:
+                    got, sc = q[:, cut], s[:, lo:lo + nblocks(part.shape[0])]
+                elif block == "tile":
+                    got, sc = q[cut], s[lo:lo + nblocks(part.shape[0])]
+                else:
+                    got, sc = q[cut], s[cut]
+                assert same_scales(sc, rs) and same_values(got.contiguous(), v), f"{block} {transpose} {cut}"

@@ -36,6 +36,17 @@ void check(int status) {
   if (status != FAR_OK) throw Status{status};
 }
 
+// f() without Python's lock: an allocation may wait for the device, and a launch for room in its queue, either of which
+// may itself wait for a host function that needs the lock.  One region a call, at its end: 0.2 us.
+template <class F>
+auto unlocked(const F& f) {
+  struct Lock {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Lock() { PyEval_RestoreThread(state); }
+  } lock;
+  return f();
+}
+
 using at::Tensor;
 constexpr auto kE4M3 = at::ScalarType::Float8_e4m3fn;
 
@@ -156,10 +167,18 @@ void table_and_positions(const Tensor& table, const Tensor& pos, int64_t tokens)
   if (pos.numel() != tokens) refuse("one position for each token");
 }
 
-// an output given (checked against its input) or a new one; None where there is no input
+using Shape = c10::SmallVector<int64_t, 6>;
+
+// an output given (checked) or one to make, without Python's lock, before the call; None where there is no input
 struct Out {
   Tensor t;
   PyObject* given = nullptr;
+  Shape shape;
+  at::ScalarType type = at::ScalarType::Float;
+  bool wanted = false;
+  void make(const Place& place) {
+    if (wanted) t = place.empty(shape, type);
+  }
   const Tensor* get() const { return t.defined() ? &t : nullptr; }
   PyObject* object() const {
     if (given) return Py_NewRef(given);
@@ -167,18 +186,24 @@ struct Out {
     return THPVariable_Wrap(t);
   }
 };
-Out output(const Place& place, const Tensor* in, PyObject* o) {
+Out fresh(at::IntArrayRef shape, at::ScalarType type) {
+  Out r;
+  r.shape.assign(shape.begin(), shape.end());
+  r.type = type;
+  r.wanted = true;
+  return r;
+}
+Out output(const Tensor* in, PyObject* o) {
   Out r;
   if (!in) {
     if (o != Py_None) refuse("an output without its input");
-  } else if (o == Py_None) {
-    r.t = place.empty(in->sizes(), in->scalar_type());
-  } else {
-    r.t = tensor(o);
-    if (r.t.sizes() != in->sizes() || r.t.scalar_type() != in->scalar_type())
-      refuse("an output has its input's shape and dtype");
-    r.given = o;
+    return r;
   }
+  if (o == Py_None) return fresh(in->sizes(), in->scalar_type());
+  r.t = tensor(o);
+  if (r.t.sizes() != in->sizes() || r.t.scalar_type() != in->scalar_type())
+    refuse("an output has its input's shape and dtype");
+  r.given = o;
   return r;
 }
 
@@ -198,12 +223,19 @@ PyObject* qk_norm_rope_(PyObject* const* a) {
   const int code = weights(q, k, qw, kw, s.dim);
   table_and_positions(table, pos, s.tokens);
   const Place place{&q, k, qw, kw, &table, &pos, maybe(a[8]), maybe(a[9])};
-  const Out yq = output(place, &q, a[8]), yk = output(place, k, a[9]);
-  const Heads x = heads(&q), xk = heads(k), y = heads(yq.get()), z = heads(yk.get());
-  check(qk_norm_rope(x.p, x.ts, x.hs, xk.p, xk.ts, xk.hs, ptr(qw), k ? ptr(kw) : nullptr, (float)real(a[4]),
-                     static_cast<const float*>(table.data_ptr()), table.size(0), pos.data_ptr(), (int)pos.element_size(),
-                     y.p, y.ts, y.hs, z.p, z.ts, z.hs, s.tokens, s.q, s.k, s.dim, table.size(1), (int)integer(a[7]), code,
-                     place.stream));
+  Out yq = output(&q, a[8]), yk = output(k, a[9]);
+  const Heads x = heads(&q), xk = heads(k);
+  const float eps = (float)real(a[4]);
+  const int pairs = (int)integer(a[7]);
+  check(unlocked([&] {
+    yq.make(place);
+    yk.make(place);
+    const Heads y = heads(yq.get()), z = heads(yk.get());
+    return qk_norm_rope(x.p, x.ts, x.hs, xk.p, xk.ts, xk.hs, ptr(qw), k ? ptr(kw) : nullptr, eps,
+                        static_cast<const float*>(table.data_ptr()), table.size(0), pos.data_ptr(),
+                        (int)pos.element_size(), y.p, y.ts, y.hs, z.p, z.ts, z.hs, s.tokens, s.q, s.k, s.dim,
+                        table.size(1), pairs, code, place.stream);
+  }));
   return tuple({yq.object(), yk.object()});
 }
 
@@ -216,11 +248,17 @@ PyObject* rope_(PyObject* const* a) {
   const int act = code_of(q.scalar_type());
   table_and_positions(table, pos, s.tokens);
   const Place place{&q, k, &table, &pos, maybe(a[6]), maybe(a[7])};
-  const Out yq = output(place, &q, a[6]), yk = output(place, k, a[7]);
-  const Heads x = heads(&q), xk = heads(k), y = heads(yq.get()), z = heads(yk.get());
-  check(rope(x.p, x.ts, x.hs, xk.p, xk.ts, xk.hs, static_cast<const float*>(table.data_ptr()), table.size(0),
-             pos.data_ptr(), (int)pos.element_size(), y.p, y.ts, y.hs, z.p, z.ts, z.hs, s.tokens, s.q, s.k, s.dim,
-             table.size(1), (int)integer(a[4]), (int)integer(a[5]), act, place.stream));
+  Out yq = output(&q, a[6]), yk = output(k, a[7]);
+  const Heads x = heads(&q), xk = heads(k);
+  const int pairs = (int)integer(a[4]), transpose = (int)integer(a[5]);
+  check(unlocked([&] {
+    yq.make(place);
+    yk.make(place);
+    const Heads y = heads(yq.get()), z = heads(yk.get());
+    return rope(x.p, x.ts, x.hs, xk.p, xk.ts, xk.hs, static_cast<const float*>(table.data_ptr()), table.size(0),
+                pos.data_ptr(), (int)pos.element_size(), y.p, y.ts, y.hs, z.p, z.ts, z.hs, s.tokens, s.q, s.k, s.dim,
+                table.size(1), pairs, transpose, act, place.stream);
+  }));
   return tuple({yq.object(), yk.object()});
 }
 
@@ -238,26 +276,30 @@ PyObject* qk_norm_rope_backward_(PyObject* const* a) {
   if (!like(gq, &q) || !like(gk, k)) refuse("an output's gradient has its input's shape and dtype");
   const Tensor* ws = maybe(a[12]);
   const Place place{&q, k, qw, kw, &table, &pos, gq, gk, maybe(a[10]), maybe(a[11]), ws};
-  const Out yq = output(place, &q, a[10]), yk = output(place, k, a[11]);
-  Tensor dqw = place.empty({s.dim}, at::ScalarType::Float), dkw, own;
-  if (k) dkw = place.empty({s.dim}, at::ScalarType::Float);
-  if (s.q == 0) dqw.zero_();  // (the C entry point leaves the arguments of a half without heads alone)
-  if (k && s.k == 0) dkw.zero_();
-  if (!ws) {
-    const int64_t bytes = far_qk_backward_workspace_bytes(s.dim);
-    if (bytes < 0) throw Status{(int)-bytes};
-    own = place.empty({bytes}, at::ScalarType::Byte);
-    ws = &own;
-  } else if (!ws->is_contiguous()) {
-    refuse("workspace must be contiguous");
-  }
-  const Heads g = heads(gq), h = heads(gk), x = heads(&q), xk = heads(k), y = heads(yq.get()), z = heads(yk.get());
-  check(qk_norm_rope_backward(g.p, g.ts, g.hs, h.p, h.ts, h.hs, x.p, x.ts, x.hs, xk.p, xk.ts, xk.hs, ptr(qw),
-                              k ? ptr(kw) : nullptr, (float)real(a[6]), static_cast<const float*>(table.data_ptr()),
-                              table.size(0), pos.data_ptr(), (int)pos.element_size(), y.p, y.ts, y.hs, z.p, z.ts, z.hs,
-                              static_cast<float*>(dqw.data_ptr()), k ? static_cast<float*>(dkw.data_ptr()) : nullptr,
-                              ws->data_ptr(), ws->numel() * (int64_t)ws->element_size(), s.tokens, s.q, s.k, s.dim,
-                              table.size(1), (int)integer(a[9]), code, place.stream));
+  Out yq = output(&q, a[10]), yk = output(k, a[11]);
+  if (ws && !ws->is_contiguous()) refuse("workspace must be contiguous");
+  const int64_t bytes = ws ? ws->numel() * (int64_t)ws->element_size() : far_qk_backward_workspace_bytes(s.dim);
+  if (bytes < 0) throw Status{(int)-bytes};
+  const Heads g = heads(gq), h = heads(gk), x = heads(&q), xk = heads(k);
+  const float eps = (float)real(a[6]);
+  const int pairs = (int)integer(a[9]);
+  Tensor dqw, dkw, own;
+  check(unlocked([&] {
+    yq.make(place);
+    yk.make(place);
+    dqw = place.empty({s.dim}, at::ScalarType::Float);
+    if (k) dkw = place.empty({s.dim}, at::ScalarType::Float);
+    if (s.q == 0) dqw.zero_();  // (the C entry point leaves the arguments of a half without heads alone)
+    if (k && s.k == 0) dkw.zero_();
+    if (!ws) own = place.empty({bytes}, at::ScalarType::Byte);
+    const Heads y = heads(yq.get()), z = heads(yk.get());
+    return qk_norm_rope_backward(g.p, g.ts, g.hs, h.p, h.ts, h.hs, x.p, x.ts, x.hs, xk.p, xk.ts, xk.hs, ptr(qw),
+                                 k ? ptr(kw) : nullptr, eps, static_cast<const float*>(table.data_ptr()), table.size(0),
+                                 pos.data_ptr(), (int)pos.element_size(), y.p, y.ts, y.hs, z.p, z.ts, z.hs,
+                                 static_cast<float*>(dqw.data_ptr()), k ? static_cast<float*>(dkw.data_ptr()) : nullptr,
+                                 (ws ? *ws : own).data_ptr(), bytes, s.tokens, s.q, s.k, s.dim, table.size(1), pairs,
+                                 code, place.stream);
+  }));
   return tuple({yq.object(), yk.object(), THPVariable_Wrap(dqw), k ? THPVariable_Wrap(dkw) : Py_NewRef(Py_None)});
 }
 
@@ -281,36 +323,29 @@ Rows rows_of(const Tensor& t, const char* refusal = "non-contiguous tensors must
   return {t.size(0), c, t.size(0) > 1 ? t.stride(0) : c};
 }
 
-using Shape = c10::SmallVector<int64_t, 6>;
 Shape with_last(const Tensor& t, int64_t last) {
   Shape s(t.sizes().begin(), t.sizes().end());
   s.back() = last;
   return s;
 }
 
-Out codes(const Place& place, PyObject* o, at::IntArrayRef shape) {
+Out codes(PyObject* o, at::IntArrayRef shape) {
+  if (o == Py_None) return fresh(shape, kE4M3);
   Out r;
-  if (o == Py_None) {
-    r.t = place.empty(shape, kE4M3);
-  } else {
-    r.t = tensor(o);
-    r.given = o;
-    if (r.t.sizes() != shape || (r.t.scalar_type() != kE4M3 && r.t.scalar_type() != at::ScalarType::Byte) ||
-        !r.t.is_contiguous())
-      refuse("q must be a contiguous float8_e4m3fn (or uint8) tensor of the output's shape");
-  }
+  r.t = tensor(o);
+  r.given = o;
+  if (r.t.sizes() != shape || (r.t.scalar_type() != kE4M3 && r.t.scalar_type() != at::ScalarType::Byte) ||
+      !r.t.is_contiguous())
+    refuse("q must be a contiguous float8_e4m3fn (or uint8) tensor of the output's shape");
   return r;
 }
-Out scales(const Place& place, PyObject* o, at::IntArrayRef shape) {
+Out scales(PyObject* o, at::IntArrayRef shape) {
+  if (o == Py_None) return fresh(shape, at::ScalarType::Float);
   Out r;
-  if (o == Py_None) {
-    r.t = place.empty(shape, at::ScalarType::Float);
-  } else {
-    r.t = tensor(o);
-    r.given = o;
-    if (r.t.sizes() != shape || r.t.scalar_type() != at::ScalarType::Float || !r.t.is_contiguous())
-      refuse("scale must be a contiguous float32 tensor, one value a block");
-  }
+  r.t = tensor(o);
+  r.given = o;
+  if (r.t.sizes() != shape || r.t.scalar_type() != at::ScalarType::Float || !r.t.is_contiguous())
+    refuse("scale must be a contiguous float32 tensor, one value a block");
   return r;
 }
 
@@ -324,20 +359,25 @@ PyObject* norm_quant_block_(PyObject* const* a) {
   if (r && (r->sizes() != x.sizes() || r->scalar_type() != x.scalar_type()))
     refuse("x and residual must share a shape and a dtype");
   const Place place{&x, r, &w, maybe(a[4]), maybe(a[5]), maybe(a[6])};
-  const Out res = output(place, r, a[6]);
-  const Out q = codes(place, a[4], x.sizes()), s = scales(place, a[5], with_last(x, blocks(x.size(-1))));
+  Out res = output(r, a[6]);
+  Out q = codes(a[4], x.sizes()), sc = scales(a[5], with_last(x, blocks(x.size(-1))));
   const Rows X = rows_of(x);
+  const int64_t r_stride = r ? rows_of(*r).stride : 0;
   const float eps = (float)real(a[3]);
-  float* sp = static_cast<float*>(s.t.data_ptr());
-  if (r) {
-    check(fused_add_rmsnorm_quant_block(x.data_ptr(), X.stride, r->data_ptr(), rows_of(*r).stride, w.data_ptr(), eps,
-                                        q.t.data_ptr(), sp, res.t.data_ptr(), rows_of(res.t).stride, X.rows, X.cols, code,
-                                        place.stream));
-    return tuple({q.object(), s.object(), res.object()});
-  }
-  check(rmsnorm_quant_block(x.data_ptr(), X.stride, w.data_ptr(), eps, q.t.data_ptr(), sp, X.rows, X.cols, code,
-                            place.stream));
-  return tuple({q.object(), s.object()});
+  check(unlocked([&] {
+    res.make(place);
+    q.make(place);
+    sc.make(place);
+    float* sp = static_cast<float*>(sc.t.data_ptr());
+    if (!r)
+      return rmsnorm_quant_block(x.data_ptr(), X.stride, w.data_ptr(), eps, q.t.data_ptr(), sp, X.rows, X.cols, code,
+                                 place.stream);
+    return fused_add_rmsnorm_quant_block(x.data_ptr(), X.stride, r->data_ptr(), r_stride, w.data_ptr(), eps,
+                                         q.t.data_ptr(), sp, res.t.data_ptr(), rows_of(res.t).stride, X.rows, X.cols,
+                                         code, place.stream);
+  }));
+  if (!r) return tuple({q.object(), sc.object()});
+  return tuple({q.object(), sc.object(), res.object()});
 }
 
 // x, block (0 rows, 1 tiles), transpose, q, scale
@@ -349,9 +389,13 @@ PyObject* quant_block_fp8_(PyObject* const* a) {
   const Place place{&x, maybe(a[3]), maybe(a[4])};
   const Rows X = rows_of(x, "x must have contiguous rows");
   const int64_t r = transpose ? X.cols : X.rows, c = transpose ? X.rows : X.cols;
-  const Out q = codes(place, a[3], {r, c}), s = scales(place, a[4], {block == FAR_BLOCK_ROW ? r : blocks(r), blocks(c)});
-  check(quant_block_fp8(x.data_ptr(), X.stride, q.t.data_ptr(), static_cast<float*>(s.t.data_ptr()), X.rows, X.cols, block,
-                        transpose, act, place.stream));
+  Out q = codes(a[3], {r, c}), s = scales(a[4], {block == FAR_BLOCK_ROW ? r : blocks(r), blocks(c)});
+  check(unlocked([&] {
+    q.make(place);
+    s.make(place);
+    return quant_block_fp8(x.data_ptr(), X.stride, q.t.data_ptr(), static_cast<float*>(s.t.data_ptr()), X.rows, X.cols,
+                           block, transpose, act, place.stream);
+  }));
   return tuple({q.object(), s.object()});
 }
 
@@ -374,20 +418,22 @@ PyObject* gemm_fp8_block_(PyObject* const* a) {
   // (n = 1 has one of either: the same numbers)
   const int block = ws.size(0) == blocks(n) ? FAR_BLOCK_TILE : FAR_BLOCK_ROW;
   const Place place{&x, &xs, &w, &ws, maybe(a[5])};
-  Out out;
-  const Shape shape = with_last(x, n);
-  if (a[5] == Py_None) {
-    out.t = place.empty(shape, ot);
-  } else {
+  Out out = fresh(with_last(x, n), ot);
+  if (a[5] != Py_None) {
     out.t = tensor(a[5]);
     out.given = a[5];
-    if (out.t.sizes() != at::IntArrayRef(shape) || out.t.scalar_type() != ot) refuse("out has shape [..., n] and out_dtype");
+    out.wanted = false;
+    if (out.t.sizes() != at::IntArrayRef(out.shape) || out.t.scalar_type() != ot) refuse("out has shape [..., n] and out_dtype");
   }
   int64_t m = 1;
   for (int64_t i = 0; i + 1 < x.dim(); ++i) m *= x.size(i);
-  check(gemm_fp8_block(x.data_ptr(), k ? rows_of(x).stride : 0, static_cast<const float*>(xs.data_ptr()), w.data_ptr(),
-                       k ? rows_of(w).stride : 0, static_cast<const float*>(ws.data_ptr()), block, out.t.data_ptr(),
-                       rows_of(out.t).stride, m, n, k, od, place.stream));
+  const int64_t ldx = k ? rows_of(x).stride : 0, ldw = k ? rows_of(w).stride : 0;
+  check(unlocked([&] {
+    out.make(place);
+    return gemm_fp8_block(x.data_ptr(), ldx, static_cast<const float*>(xs.data_ptr()), w.data_ptr(), ldw,
+                          static_cast<const float*>(ws.data_ptr()), block, out.t.data_ptr(), rows_of(out.t).stride, m, n,
+                          k, od, place.stream);
+  }));
   return out.object();
 }
 

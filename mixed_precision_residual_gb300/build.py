@@ -23,6 +23,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libfar.so")
 BINDING = os.path.join(BUILD, "_far_torch.so")
 BINDING_SOURCE = "far_torch.cpp"
+BINDING_STAMP = os.path.join(BUILD, "_far_torch.built_for")  # the Python and PyTorch that the binding was built for
 SOURCES = ["far_api.cu", "far_inst_f16.cu", "far_inst_bf16.cu", "far_inst_f32.cu", "far_inst_q_f16.cu",
            "far_inst_q_bf16.cu", "far_inst_q_f32.cu", "far_inst_ln_f16.cu", "far_inst_ln_bf16.cu",
            "far_inst_ln_f32.cu", "far_inst_qb_f16.cu", "far_inst_qb_bf16.cu", "far_inst_qb_f32.cu", "far_noalloc.cu",
@@ -59,49 +60,70 @@ def _torch_flags() -> tuple[list, list]:
     return cc, ld
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _built_for() -> str:
+    import torch
+
+    return f"python {sys.version.split()[0]}, torch {torch.__version__} at {os.path.dirname(torch.__file__)}\n"
+
+
+def _older(target: str, sources: list) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(f) > os.path.getmtime(target) for f in sources)
+
+
+def _library_stale() -> bool:
+    return _older(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "far.h")])
+
+
+def _binding_stale() -> bool:
+    """Older than its sources, or built for another Python or PyTorch (whose symbols it would miss)."""
+    if _older(BINDING, [os.path.join(CSRC, BINDING_SOURCE), os.path.join(ROOT, "include", "far.h")]):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [BINDING_SOURCE]] + [os.path.join(ROOT, "include", "far.h")]
-    return any(os.path.getmtime(d) > t for d in deps)
+    if not os.path.exists(BINDING_STAMP):
+        return True
+    with open(BINDING_STAMP) as f:
+        return f.read() != _built_for()
+
+
+def _stale() -> bool:
+    return _library_stale() or _binding_stale()
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
+    library, binding = force or _library_stale(), force or _binding_stale()
+    if not (library or binding):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
+    cc, ld = _torch_flags() if binding else ([], [])
 
-    cc, ld = _torch_flags()
+    def run(cmd, what):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+        return r.stderr
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-        if src == BINDING_SOURCE:
-            cmd = ["g++", *cc, "-c", os.path.join(CSRC, src), "-o", obj]
-        else:
-            cmd = [nvcc, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
-        return obj, r.stderr
+        compiler = ["g++", *cc] if src == BINDING_SOURCE else [nvcc, *NVCC_FLAGS]
+        return obj, run([*compiler, "-c", os.path.join(CSRC, src), "-o", obj], f"{compiler[0]} failed for {src}")
+
+    def link(cmd, target):
+        tmp = target + f".tmp{os.getpid()}"
+        run([*cmd, "-o", tmp], "link failed")
+        os.replace(tmp, target)
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        *results, (binding, _) = ex.map(compile_one, SOURCES + [BINDING_SOURCE])
-    with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
-        for (_, log), src in zip(results, SOURCES):
-            f.write(f"==== {src}\n{log}\n")
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results]]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    tmp = BINDING + f".tmp{os.getpid()}"
-    r = subprocess.run(["g++", binding, "-o", tmp, *ld], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
+        module = ex.submit(compile_one, BINDING_SOURCE) if binding else None
+        results = list(ex.map(compile_one, SOURCES)) if library else []
+    if library:  # first: it does not need the binding
+        with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
+            for (_, log), src in zip(results, SOURCES):
+                f.write(f"==== {src}\n{log}\n")
+        link([nvcc, *ARCH, "-shared", *[o for o, _ in results]], LIB)
+    if module:
+        link(["g++", module.result()[0], *ld], BINDING)
+        with open(BINDING_STAMP, "w") as f:
+            f.write(_built_for())
     if verbose:
         print(f"built {LIB}", file=sys.stderr)
     return LIB

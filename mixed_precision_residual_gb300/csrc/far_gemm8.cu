@@ -569,10 +569,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::th
             x.join();
             f.join();
             if (one_factor(x.least, f.least) && one_factor(x.most, f.most)) continue;  // and all between
-            for (int64_t r = row0; r < row0 + rows; ++r)
-              for (int64_t h = tile0; h < tile0 + tiles; ++h)
-                for (int kb = lane; kb < p.KB; kb += 32)
-                  if (!one_factor(p.xs[r * p.KB + kb], p.ws[h * p.KB + kb])) tell(kRare);
+            bool odd = false;
+            for (int64_t h = tile0; h < tile0 + tiles; ++h)
+              for (int kb = lane; kb < p.KB; kb += 32) {
+                const float b = p.ws[h * p.KB + kb];
+#pragma unroll 8
+                for (int64_t r = row0; r < row0 + rows; ++r) odd |= !one_factor(p.xs[r * p.KB + kb], b);
+              }
+            if (odd) tell(kRare);
           }
         }
       }

@@ -159,3 +159,19 @@ def test_infinite_and_nan_scales_and_codes(far, m, k, rows, kernel):
     nans = torch.zeros(m, N, dtype=torch.bool, device="cuda")
     nans[1], nans[:, 300] = True, True
     assert torch.equal(far.gemm_fp8_block(xq[:, :], xs / xs, wq, ws / ws, out_dtype=torch.float32).isnan(), nans)
+
+
+@pytest.mark.parametrize("m,k,rows,kernel", KERNELS, ids=str)
+def test_far_scales_that_do_not_meet(far, m, k, rows, kernel):
+    """Tiny scales of x in some blocks and of wt in others, no product of two out of range: the results of ordinary
+    scales times the powers of two, bit for bit where every block's scales are the same power of two apart."""
+    g = torch.Generator(device="cuda").manual_seed(m + k + 4)
+    xq, wq = codes(g, m, k), codes(g, N, k)
+    kb, wn = nblocks(k), N if rows == "row" else nblocks(N)
+    xs, ws = torch.rand(m, kb, generator=g, device="cuda") + 0.5, torch.rand(wn, kb, generator=g, device="cuda") + 0.5
+    want = far.gemm_fp8_block(xq, xs, wq, ws, out_dtype=torch.float32)
+    a = torch.tensor([-90.0 if b % 2 else -10.0 for b in range(kb)], device="cuda")
+    far_x, far_w = xs * torch.exp2(a), ws * torch.exp2(-100.0 - a)  # block by block a product 2^-100 of the one before
+    check(far, kernel, xq, far_x, wq, far_w)
+    got = far.gemm_fp8_block(xq, far_x, wq, far_w, out_dtype=torch.float32)
+    assert torch.equal(got, want * 2.0 ** -100)

@@ -230,7 +230,8 @@ int rmsnorm_quant_strided(const void* x, int64_t x_row_stride, const void* weigh
 /*
  * Per-head RMSNorm of queries and keys and the rotation by position, in one pass.  For
  * each token t and head, with x the head's head_dim values (widened to binary32):
- *   r   = 1 / sqrt(S / head_dim + eps) in binary32 (within 4 * 2^-24), S the binary32 sum of x_i^2
+ *   r   = 1 / sqrt(S / head_dim + eps) in binary32, S the binary32 sum of x_i^2 (r within
+ *         5.5 * 2^-24 of that of S, and half of S's own error)
  *   n_i = x_i * r * w_i                                          (w: q_weight or k_weight)
  *   for the first rot_dim values, with c_j and s_j the table's row positions[t]:
  *     pairs FAR_PAIRS_HALF:        j = 0 .. rot_dim/2 - 1, (a, b) = (n_j, n_{j + rot_dim/2})
@@ -288,7 +289,10 @@ int rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, const voi
  *   dw_i = sum over tokens and heads of g_i u_i
  *   dx_i = r * (h_i - u_i * mean_j(h_j u_j)),  h_i = g_i w_i
  * in binary32, dx rounded once to act.  The weights' gradients are binary32 whatever the
- * weights' dtype; their sums are taken in a fixed order (the same bits every run).
+ * weights' dtype; their sums are taken in binary32 in a fixed order (the same bits every run): a
+ * lane adds its share of the heads one after another (of 128 16-bit values: queries' and keys'
+ * heads * tokens / 10^4), the rest are trees, so that a sum's error is at most that number and
+ * some 60 more times 2^-24 of the sum of its terms' magnitudes.
  *   dq_out, dk_out        act, device, read: shapes of q and k, strides of their own
  *   dq, dk                act, device, written: shapes of q and k; each may be exactly its
  *                         q / k or its dq_out / dk_out (pointer and strides)

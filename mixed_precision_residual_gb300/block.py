@@ -1,5 +1,5 @@
 """FP8 E4M3 in blocks of 128: RMSNorm with a block-quantised output, quantising a matrix, and
-the product of two block-scaled matrices (ctypes binding; the contracts stand in
+the product of two block-scaled matrices (through the native binding; the contracts stand in
 ``include/far.h`` at fused_add_rmsnorm_quant_block, quant_block_fp8 and gemm_fp8_block).
 
     wq, ws = quant_block_fp8(weight, block="tile")                     # once

@@ -1,6 +1,7 @@
 """Per-head RMSNorm of queries and keys with the rotation by position, its gradients, the
-rotation alone, and the table of cosines and sines they read (ctypes binding; the contract
-stands in ``include/far.h`` at qk_norm_rope).
+rotation alone, and the table of cosines and sines they read (tensor calls through the native
+binding, frequencies and tables through ctypes; the contract stands in ``include/far.h`` at
+qk_norm_rope).
 
     table = rope_table(32768, 128, base=1e6, scaling={"type": "yarn", "factor": 4.0, "trained": 8192})
     q, k = qk_norm_rope(q, k, q_weight, k_weight, 1e-6, table, positions)

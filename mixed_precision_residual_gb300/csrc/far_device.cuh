@@ -473,8 +473,9 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 }
 
 // Wait until every kernel before this one on the stream has completed and its memory
-// operations are visible.  Every kernel here calls it before its first access to global
-// memory, so stream order holds whatever the launch attribute.
+// operations are visible.  Every kernel here calls it before it reads or writes global
+// memory (one has lines of a tensor brought into L2 before), so stream order holds whatever
+// the launch attribute.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------

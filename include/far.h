@@ -289,10 +289,10 @@ int rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, const voi
  *   dw_i = sum over tokens and heads of g_i u_i
  *   dx_i = r * (h_i - u_i * mean_j(h_j u_j)),  h_i = g_i w_i
  * in binary32, dx rounded once to act.  The weights' gradients are binary32 whatever the
- * weights' dtype; their sums are taken in binary32 in a fixed order (the same bits every run): a
- * lane adds its share of the heads one after another (of 128 16-bit values: queries' and keys'
- * heads * tokens / 10^4), the rest are trees, so that a sum's error is at most that number and
- * some 60 more times 2^-24 of the sum of its terms' magnitudes.
+ * weights' dtype; their sums are taken in a fixed order (the same bits every run): in binary32
+ * a lane adds its share of the heads one after another (of 128 16-bit values: queries' and keys'
+ * heads * tokens / 10^4) and a block its lanes' sums, so that the error is at most that number and
+ * 13 more times 2^-24 of the sum of the terms' magnitudes; the blocks' sums are added without loss.
  *   dq_out, dk_out        act, device, read: shapes of q and k, strides of their own
  *   dq, dk                act, device, written: shapes of q and k; each may be exactly its
  *                         q / k or its dq_out / dk_out (pointer and strides)

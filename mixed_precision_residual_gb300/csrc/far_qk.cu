@@ -682,31 +682,48 @@ __global__ void __launch_bounds__(kQkThreads) qk_any_kernel(const QkParams p, in
   }
 }
 
-// The partial rows summed in a fixed order (every 32nd row by a lane of rows, then the lanes by
-// halves), in binary32: at most 32 + 5 additions deep, where the lanes that made the rows have added their share
-// of the heads one after another.  Binary64 took some 2 us longer of the backward pass's 53 (8192 tokens of 32 + 8
-// heads), for little: binary32 gradients of 777, 8192 and 30000 tokens lie 1.2, 1.8 and 3.7e-7 of their norm from
-// the exact ones, with these rows added in 64 bits 0.9, 1.6 and 3.5e-7 (64-bit sums throughout: 0.7e-7): block (32 columns x 32 row lanes), blockIdx.y = 0 the queries' weight, 1 the keys'.
+// A sum in two binary32 numbers: what each addition rounds off (exact, Knuth 1969) is added up beside it.
+struct Two {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
+    hi = s;
+  }
+  __device__ __forceinline__ void add(const Two& x) {
+    add(x.hi);
+    lo = __fadd_rn(lo, x.lo);
+  }
+  __device__ __forceinline__ float value() const { return isfinite(hi) ? __fadd_rn(hi, lo) : hi; }
+};
+
+// The partial rows summed in a fixed order (every 32nd row by a lane of rows, then the lanes by halves), each sum in two
+// binary32 numbers (Two): in binary64 it took some 2 us longer of the backward pass's 53 (8192 tokens of 32 + 8 heads).
+// So what the gradients err is what the lanes that made the rows add up, one head after another: block (32 columns x 32 row lanes), blockIdx.y = 0 the queries' weight, 1 the keys'.
 __global__ void __launch_bounds__(1024)
     qk_weight_grad_kernel(const float* parts, int D, int rows_q, int rows_k, float* dq_weight, float* dk_weight) {
-  __shared__ float sm[32][33];
+  __shared__ float2 sm[32][33];
   pdl_launch_dependents();
   pdl_wait();
   const int col = blockIdx.x * 32 + threadIdx.x;
   const int rows = blockIdx.y ? rows_k : rows_q;
   const float* base = parts + (blockIdx.y ? (int64_t)rows_q * D : 0);
   float* out = blockIdx.y ? dk_weight : dq_weight;
-  float v = 0.f;
+  Two v;
   if (col < D) {
 #pragma unroll 8
-    for (int r = threadIdx.y; r < rows; r += 32) v = __fadd_rn(v, base[(int64_t)r * D + col]);
+    for (int r = threadIdx.y; r < rows; r += 32) v.add(base[(int64_t)r * D + col]);
   }
-  sm[threadIdx.y][threadIdx.x] = v;
+  sm[threadIdx.y][threadIdx.x] = make_float2(v.hi, v.lo);
   __syncthreads();
   // turned: a warp adds the 32 row lanes of one column
-  const float t = lanes_sum(sm[threadIdx.x][threadIdx.y], 32);
+  const float2 mine = sm[threadIdx.x][threadIdx.y];
+  Two t{mine.x, mine.y};
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    t.add(Two{__shfl_xor_sync(0xffffffffu, t.hi, off), __shfl_xor_sync(0xffffffffu, t.lo, off)});
   const int c = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && c < D && out) out[c] = t;
+  if (threadIdx.x == 0 && c < D && out) out[c] = t.value();
 }
 
 struct Freqs {

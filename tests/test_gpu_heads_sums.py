@@ -80,6 +80,30 @@ def test_every_head_counts_once(far, size, act, pairs):
             assert bool(((dw.double() - r * want).abs() <= 200 * 2.0 ** -24 * size).all())
 
 
+@pytest.mark.parametrize("tokens,h,hk,d,scalar", [(8000, 8, 3, 128, False), (30000, 4, 1, 64, False), (8000, 8, 3, 128, True),
+                                                  (777, 12, 12, 256, False)])
+def test_partial_sums_are_added_without_loss(far, tokens, h, hk, d, scalar):
+    """Heads of +-1 again (r = 1), not turned, with gradients of up to 2^14 and the heads' signs: what one block adds up
+    (at most 800 heads: below 2^24) is exact, the sum over the blocks is not a binary32 number
+    any more, and the weights' gradient is that sum rounded once."""
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    place = off_by_one if scalar else (lambda x: x)
+    table = torch.cat([torch.ones(1, d // 2, device="cuda"), torch.zeros(1, d // 2, device="cuda")], 1).contiguous()
+    pos = torch.zeros(tokens, dtype=torch.int64, device="cuda")
+    x = [place(1.0 - 2.0 * torch.randint(0, 2, (tokens, n, d), generator=g, device="cuda").float()) for n in (h, hk)]
+    dy = [place(v * torch.randint(1, (1 << 14) + 1, v.shape, generator=g, device="cuda").float()) for v in x]
+    w = torch.ones(d, device="cuda")
+    y, _ = far.qk_norm_rope(x[0][:1].clone(), None, w, None, 0.0, table, pos[:1])
+    if not bool((y.abs() == 1.0).all()):
+        pytest.skip("r is not 1 here: the terms are not whole numbers")
+    got = far.qk_norm_rope_backward(dy[0], dy[1], x[0], x[1], w, w, 0.0, table, pos)
+    assert far.device_status() == 0
+    for v, gr, dw in zip(x, dy, got[2:]):
+        want = (v.double() * gr.double()).sum((0, 1))  # whole numbers below 2^53
+        assert float(want.min()) > 2.0 ** 24
+        assert torch.equal(dw, want.float()), f"{int((dw != want.float()).sum())} of {d} sums not rounded once"
+
+
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 def test_no_query_or_no_key_heads(far, act):
     """A tensor without heads: nothing to normalise, and zeros for its weight's gradient (not what lay in memory)."""

@@ -56,8 +56,8 @@ def check(far, kernel, xq, xs, wq, ws, dtype=torch.float32, where=""):
     """Every output whose terms all lie in range within the bound of its binary32 steps (block_ref.product's, and one
     rounding a term and a sum to binary32's smallest step); one with one term past the range infinite, of its sign;
     infinite and NaN scales as the definition has them."""
-    m, k = xq.shape
-    plan = far.plan_gemm_fp8_for_sms(m, N, k, "row" if ws.shape[0] == N else "tile",
+    (m, k), n = xq.shape, wq.shape[0]
+    plan = far.plan_gemm_fp8_for_sms(m, n, k, "row" if ws.shape[0] == n else "tile",
                                      torch.cuda.get_device_properties(0).multi_processor_count)
     assert (plan["kind"], plan["rows"]) == kernel, "the shape no longer reaches the kernel it is meant for"
     y = far.gemm_fp8_block(xq, xs, wq, ws, out_dtype=dtype).double()
@@ -175,3 +175,33 @@ def test_far_scales_that_do_not_meet(far, m, k, rows, kernel):
     check(far, kernel, xq, far_x, wq, far_w)
     got = far.gemm_fp8_block(xq, far_x, wq, far_w, out_dtype=torch.float32)
     assert torch.equal(got, want * 2.0 ** -100)
+
+
+@pytest.mark.parametrize("dtype,columns", [(torch.float32, 2056), (torch.bfloat16, 2050)])
+@pytest.mark.parametrize("rows", ["tile", "row"])
+def test_second_pass_over_several_tiles(far, rows, dtype, columns):
+    """Far scales in a few places of a product of three tiles a CTA pair: all of it is right, with outputs that leave by TMA
+    and with ones that are stored row by row (rows off a 16-byte boundary)."""
+    m, k = 5200, 656
+    g = torch.Generator(device="cuda").manual_seed(columns)
+    xq, wq = codes(g, m, k), codes(g, columns, k)
+    kb, wn = nblocks(k), columns if rows == "row" else nblocks(columns)
+    xs, ws = torch.rand(m, kb, generator=g, device="cuda") + 0.5, torch.rand(wn, kb, generator=g, device="cuda") + 0.5
+    usual = far.gemm_fp8_block(xq, xs, wq, ws, out_dtype=dtype)
+    xs[[3, 2600, m - 1], [0, 3, kb - 1]] = torch.tensor([2.0 ** -120, 2.0 ** 100, 0.0], device="cuda")
+    ws[[0, wn // 2, wn - 1], [0, 3, kb - 1]] = torch.tensor([2.0 ** -20, 2.0 ** -110, 2.0 ** 105], device="cuda")
+    check(far, (1, 0), xq, xs, wq, ws, dtype=dtype, where=rows)
+    again = far.gemm_fp8_block(xq, xs, wq, ws, out_dtype=dtype)
+    assert torch.equal(far.gemm_fp8_block(xq, xs, wq, ws, out_dtype=dtype), again)
+    same = torch.ones(m, columns, dtype=torch.bool, device="cuda")
+    same[[3, 2600, m - 1]] = False
+    cols = torch.arange(columns, device="cuda") // (1 if rows == "row" else BLOCK)
+    for j in (0, wn // 2, wn - 1):
+        same[:, cols == j] = False
+    # Elsewhere the scales are the usual ones, and the tensor cores' sums the same bits in either pass: a term is rounded
+    # twice and added once, each of it by at most 2^-24 of the terms' magnitudes T that have been added, so each
+    # result is within 3 * blocks * 2^-24 T of the exact sum of those terms, and rounded once to dtype.
+    _, size = terms(xq, xs, wq, ws)
+    bound = 2 * 3 * kb * 2.0 ** -24 * size.sum(0)[same]
+    off = (again[same].double() - usual[same].double()).abs()
+    assert bool((off <= bound + torch.finfo(dtype).eps * (usual[same].double().abs() + bound)).all())

@@ -311,9 +311,11 @@ __device__ __forceinline__ void store_box(const Gemm8Params& p, const CUtensorMa
 // the 8 epilogue warps take 216 (128 x 72 + 256 x 216 = 384 x 168).  With 16 epilogue warps
 // 640 at 96, then 56 and 104 (128 x 56 + 512 x 104 = 60416 of 61440).
 // The last column of tiles runs at the width that is left (a multiple of 32).
-// Measured: 16384 x 8192 x 8192, tile-scaled wt, bf16 out 760 to 870 us with the codes' power draw
-// (2.5 to 2.9 PFLOP/s; the same pipeline without promotion 3.7 on 8192^3), 5120 x 2056 x 4112
-// row-scaled 84 us.  Bound by the MMA (750 cycles a block beside the epilogue's TMEM loads,
+// Measured: 16384 x 8192 x 8192, tile-scaled wt, bf16 out 775 to 865 us with the codes' power draw
+// (2.5 to 2.8 PFLOP/s; the same pipeline without promotion 3.7 on 8192^3), 5120 x 2056 x 4112
+// row-scaled 84 us, 8192^3 656 us.  With a scale that sends the pairs through their second pass: 4096^3 152 us
+// from 66 (tiles), 443 from 100 (rows).  ptxas spills 140 bytes of the row-scaled kernel (220 read back),
+// in which role it does not say.  Bound by the MMA (750 cycles a block beside the epilogue's TMEM loads,
 // 512 alone) and by the two hand-overs of a TMEM half, of which a block hides only the other half's
 // MMA: two halves of 256 columns are all of TMEM.  Row-scaled also by two FMA-pipe operations
 // an output and block, and TMEM loads in fragments, which run at half rate (32 cycles for 32
@@ -837,7 +839,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairShape8<COLS>::th
 //   sums of one row of wt.
 // Then each CTA leaves its sums in its shared memory and adds up every S-th row of x over the
 // cluster's CTAs, in the order of k.
-// Bound by reading wt: m = 4, 8192 x 8192 13.0 us (5.2 TB/s), 28672 x 4096 20.7 us (5.7 TB/s); the
+// Scales of x that the loop does not serve send the CTA through small_again (64 x 4096 x 4096 2.2 ms from 8.8 us).
+// Bound by reading wt: m = 4, 8192 x 8192 13.4 us (5.0 TB/s), 28672 x 4096 20.7 us (5.7 TB/s); the
 // rest is the launch, the set-up and the sum over the cluster (about 3 us).  Two CTAs an SM with
 // five blocks in flight each and as many CTAs as fit: 1 CTA an SM with 6 or 11 blocks 15.5 and
 // 14.9 us, 8192 x 8192 shared out over 2 or 8 CTAs instead of 4 15.6 and 17.4.

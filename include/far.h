@@ -422,6 +422,100 @@ int gemm_fp8_block(const void* x, int64_t x_row_stride, const float* x_scale, co
    CTA), rows of x a CTA (kind 2), CTAs that share a tile's k (kind 2), grid} */
 int far_plan_gemm_fp8_for_sms(int64_t m, int64_t n, int64_t k, int wt_block, int sms, int* out4);
 
+/*
+ * A matrix quantised to int8 with a scale for each row: a weight's output channels, or activations'
+ * tokens.  For a row with largest magnitude amax:
+ *   scale = fl32(amax / 127), q_i = the integer nearest to fl32(x_i * fl32(127 / amax)) (ties to even);
+ *   a row with amax below 2^-100 counts as zero (scale 0, codes 0); a NaN or an infinity in a row
+ *   gives that scale and codes 0
+ *   x      [rows, cols] act (FAR_F32, FAR_F16 or FAR_BF16), row stride in elements (>= cols), device
+ *   q      [rows, cols] int8, contiguous, device;  scale  [rows] binary32, device
+ * (what the int8 output of fused_add_rmsnorm_quant is, of x as it stands.)  rows, cols >= 0, at most
+ * 2^31 - 1 each; rows == 0 is a no-op, cols == 0 gives scales 0.  q and scale share no byte with
+ * another buffer.
+ */
+int quant_rows_int8(const void* x, int64_t x_row_stride, void* q, float* scale, int64_t rows, int64_t cols, int act,
+                    void* stream);
+
+/*
+ * The product of two int8 matrices with a scale for each token and each channel:
+ *   out[i, j] = RNE_od( fl32(acc) * (xs[i] * ws[j]) + bias[j] ),  acc = sum_k x[i, k] * wt[j, k]
+ *   x        [m, k] int8, row stride in elements (>= k), device: the codes of
+ *            fused_add_rmsnorm_quant / rmsnorm_quant (FAR_Q_INT8) or quant_rows_int8
+ *   x_scale  [m] binary32, device
+ *   wt       [n, k] int8 (the transposed weight: y = x @ wt^T), row stride >= k, device
+ *   wt_scale [n] binary32, device
+ *   bias     [n] out_dtype, device, or NULL
+ *   out      [m, n] out_dtype (FAR_F32, FAR_F16, FAR_BF16), row stride >= n, device
+ *   workspace  far_gemm_int8_workspace_bytes(m, n, k) bytes of device memory on a 16-byte boundary
+ *            (NULL where that is 0), written and read by this call alone: calls that may overlap
+ *            (other streams, other graphs) need one each.  Nothing in it is kept.
+ * acc is the exact integer (every code from -128 to 127; k <= 131071, so that it fits 32 bits),
+ * rounded once to binary32; the scales' product is rounded first where it is a normal number, else acc
+ * is multiplied by one scale after the other, so that the result is right to a few units of
+ * 2^-24 wherever it lies in binary32's range.  A zero scale gives 0 + bias, unless the other scale is
+ * infinite or NaN.  out shares no byte with another buffer.  m == 0 or n == 0 is a no-op; k == 0 gives
+ * 0 + bias.  Statuses: FAR_ERR_DTYPE (out_dtype), FAR_ERR_SHAPE (sizes negative or above 2^31 - 1,
+ * k above 131071, a row stride too small, a pointer off its elements' alignment), FAR_ERR_NULL,
+ * FAR_ERR_ALIAS, FAR_ERR_WORKSPACE (too small or misaligned), FAR_ERR_CUDA.
+ */
+int64_t far_gemm_int8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+int gemm_int8(const void* x, int64_t x_row_stride, const float* x_scale, const void* wt, int64_t wt_row_stride,
+              const float* wt_scale, const void* bias, void* out, int64_t out_row_stride, void* workspace,
+              int64_t workspace_bytes, int64_t m, int64_t n, int64_t k, int out_dtype, void* stream);
+
+/*
+ * The gated feed-forward block's way in, both projections, the activation and the product in one
+ * kernel: with gate = x @ w_gate^T and up = x @ w_up^T (binary32 sums of exact products),
+ *   out      = RNE( act(gate) * up )           (neither projection is rounded before)
+ *   gate_out = RNE(gate), up_out = RNE(up)     both or neither (NULL): what the way back takes
+ *   x [tokens, hidden], w_gate and w_up [ffn, hidden], out, gate_out and up_out [tokens, ffn]: all of
+ *   dtype (FAR_F16 or FAR_BF16), row strides in elements, device
+ *   activation  FAR_ACT_SILU       g / (1 + exp(-g))
+ *               FAR_ACT_GELU       g * Phi(g), Phi the normal distribution
+ *               FAR_ACT_GELU_TANH  g / 2 * (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))
+ * in binary32, right to 2^-15 of each value (an infinite g follows the formula's limit at +inf and
+ * gives NaN at -inf; NaN gives NaN).  Few tokens read both weights once; the order of the binary32
+ * additions is not specified but the same every run.  Tensor cores (tcgen05) are used when x's and the
+ * weights' row strides are multiples of 8 and their pointers on 16-byte boundaries; any other call
+ * takes a plain kernel with the same contract.  No output shares a byte with another buffer.  Sizes
+ * 0 .. 2^31 - 1; tokens == 0 or ffn == 0 is a no-op, hidden == 0 gives zeros.  Statuses: FAR_ERR_DTYPE
+ * (dtype, activation), FAR_ERR_SHAPE (sizes, strides, a pointer off its elements' alignment),
+ * FAR_ERR_NULL, FAR_ERR_ALIAS, FAR_ERR_CUDA.
+ */
+#define FAR_ACT_SILU 0
+#define FAR_ACT_GELU 1
+#define FAR_ACT_GELU_TANH 2
+
+int gated_ffn(const void* x, int64_t x_row_stride, const void* w_gate, int64_t w_gate_row_stride, const void* w_up,
+              int64_t w_up_row_stride, void* out, int64_t out_row_stride, void* gate_out, int64_t gate_out_row_stride,
+              void* up_out, int64_t up_out_row_stride, int64_t tokens, int64_t hidden, int64_t ffn, int activation,
+              int dtype, void* stream);
+
+/*
+ * Its gradients, given that of out and the projections that gated_ffn kept:
+ *   dgate = RNE(dout * up * act'(gate)), dup = RNE(dout * act(gate))      (binary32, rounded to dtype as
+ *                                                     the operands of the products below)
+ *   dx = RNE(dgate @ w_gate + dup @ w_up), dw_gate = RNE(dgate^T @ x), dw_up = RNE(dup^T @ x)
+ *   dout, gate, up [tokens, ffn]; x, dx [tokens, hidden]; w_gate, w_up, dw_gate, dw_up [ffn, hidden];
+ *   all of dtype, row strides in elements, device
+ *   workspace  far_gated_ffn_backward_workspace_bytes(tokens, ffn) bytes of device memory on a 16-byte
+ *              boundary, written and read by this call alone: calls that may overlap (other streams,
+ *              other graphs) need one each.  Nothing in it is kept.
+ * Sums are binary32, in an order that is not specified but the same every run (no atomics).  tokens
+ * == 0 gives zero gradients of the weights, ffn == 0 a zero dx.  Everything else is as for gated_ffn;
+ * FAR_ERR_WORKSPACE: too small or misaligned.
+ */
+int64_t far_gated_ffn_backward_workspace_bytes(int64_t tokens, int64_t ffn);
+
+int gated_ffn_backward(const void* dout, int64_t dout_row_stride, const void* gate, int64_t gate_row_stride,
+                       const void* up, int64_t up_row_stride, const void* x, int64_t x_row_stride, const void* w_gate,
+                       int64_t w_gate_row_stride, const void* w_up, int64_t w_up_row_stride, void* dx,
+                       int64_t dx_row_stride, void* dw_gate, int64_t dw_gate_row_stride, void* dw_up,
+                       int64_t dw_up_row_stride, void* workspace, int64_t workspace_bytes, int64_t tokens,
+                       int64_t hidden, int64_t ffn, int activation, int dtype, void* stream);
+
 /* the output dtype od of FAR_DTYPES(act, wd), or -status when the pair is rejected */
 int far_output_dtype(int dtype);
 

@@ -439,6 +439,168 @@ PyObject* gemm_fp8_block_(PyObject* const* a) {
 }
 
 // ---------------------------------------------------------------------------
+// int8 by rows
+// ---------------------------------------------------------------------------
+
+// an output given: checked against the shape and type that it would be made with, rows contiguous
+Out given_or(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const char* refusal) {
+  Out r = fresh(shape, type);
+  if (o == Py_None) return r;
+  r.t = tensor(o);
+  r.given = o;
+  r.wanted = false;
+  if (r.t.sizes() != shape || r.t.scalar_type() != type) refuse(refusal);
+  return r;
+}
+Shape without_last(const Tensor& t) { return Shape(t.sizes().begin(), t.sizes().end() - 1); }
+int64_t rows_in(const Tensor& t) {
+  int64_t m = 1;
+  for (int64_t i = 0; i + 1 < t.dim(); ++i) m *= t.size(i);
+  return m;
+}
+// a workspace given or made
+struct Workspace {
+  const Tensor* given;
+  Tensor own;
+  int64_t bytes;
+  Workspace(const Tensor* w, int64_t needed) : given(w), bytes(needed) {
+    if (needed < 0) throw Status{(int)-needed};
+    if (w && !w->is_contiguous()) refuse("workspace must be contiguous");
+    if (w) bytes = w->numel() * (int64_t)w->element_size();
+  }
+  void* make(const Place& place) {
+    if (given) return given->data_ptr();
+    if (bytes == 0) return nullptr;
+    own = place.empty({bytes}, at::ScalarType::Byte);
+    return own.data_ptr();
+  }
+};
+
+// x, q, scale
+PyObject* quant_rows_int8_(PyObject* const* a) {
+  const Tensor& x = tensor(a[0]);
+  if (x.dim() < 1) refuse("x is [..., cols]");
+  const int act = code_of(x.scalar_type());
+  const Place place{&x, maybe(a[1]), maybe(a[2])};
+  Out q = given_or(a[1], x.sizes(), at::ScalarType::Char, "q must be a contiguous int8 tensor of x's shape");
+  Out s = given_or(a[2], without_last(x), at::ScalarType::Float, "scale must be a contiguous float32 tensor, one value a row");
+  if (q.given && !q.t.is_contiguous()) refuse("q must be a contiguous int8 tensor of x's shape");
+  if (s.given && !s.t.is_contiguous()) refuse("scale must be a contiguous float32 tensor, one value a row");
+  const Rows X = rows_of(x);
+  check(unlocked([&] {
+    q.make(place);
+    s.make(place);
+    return quant_rows_int8(x.data_ptr(), X.stride, q.t.data_ptr(), static_cast<float*>(s.t.data_ptr()), X.rows, X.cols, act,
+                           place.stream);
+  }));
+  return tuple({q.object(), s.object()});
+}
+
+// x, x_scale, wt, wt_scale, bias, out_dtype, out, workspace
+PyObject* gemm_int8_(PyObject* const* a) {
+  const Tensor &x = tensor(a[0]), &xs = tensor(a[1]), &w = tensor(a[2]), &ws = tensor(a[3]);
+  const Tensor *bias = maybe(a[4]), *space = maybe(a[7]);
+  if (x.scalar_type() != at::ScalarType::Char || w.scalar_type() != at::ScalarType::Char) refuse("x and wt hold int8 codes");
+  if (x.dim() < 2 || w.dim() != 2 || x.size(-1) != w.size(1)) refuse("x is [..., k] and wt [n, k]");
+  if (!THPDtype_Check(a[5])) throw Refused{PyExc_TypeError, "out_dtype is a torch.dtype"};
+  const at::ScalarType ot = reinterpret_cast<THPDtype*>(a[5])->scalar_type;
+  const int od = code_of(ot);
+  const int64_t n = w.size(0), k = w.size(1), m = rows_in(x);
+  if (xs.sizes() != at::IntArrayRef(without_last(x)) || xs.scalar_type() != at::ScalarType::Float || !xs.is_contiguous())
+    refuse("x_scale must be a contiguous float32 tensor, one value a row of x");
+  if (ws.dim() != 1 || ws.size(0) != n || ws.scalar_type() != at::ScalarType::Float || !ws.is_contiguous())
+    refuse("wt_scale must be a contiguous float32 [n] tensor");
+  if (bias && (bias->dim() != 1 || bias->size(0) != n || bias->scalar_type() != ot || !bias->is_contiguous()))
+    refuse("bias must be a contiguous [n] tensor of out_dtype");
+  const Place place{&x, &xs, &w, &ws, bias, maybe(a[6]), space};
+  Out out = given_or(a[6], with_last(x, n), ot, "out has shape [..., n] and out_dtype");
+  const int64_t ldx = k ? rows_of(x).stride : 0, ldw = k ? rows_of(w).stride : 0;
+  Workspace workspace(space, far_gemm_int8_workspace_bytes(m, n, k));
+  check(unlocked([&] {
+    out.make(place);
+    void* wp = workspace.make(place);
+    return gemm_int8(x.data_ptr(), ldx, static_cast<const float*>(xs.data_ptr()), w.data_ptr(), ldw,
+                     static_cast<const float*>(ws.data_ptr()), ptr(bias), out.t.data_ptr(), rows_of(out.t).stride, wp,
+                     workspace.bytes, m, n, k, od, place.stream);
+  }));
+  return out.object();
+}
+
+// ---------------------------------------------------------------------------
+// the gated feed-forward block
+// ---------------------------------------------------------------------------
+
+// the dtype shared by all, and the weights' [ffn, hidden] against x's hidden
+int ffn_dtype(const Tensor& x, const Tensor& wg, const Tensor& wu) {
+  if (x.dim() < 2 || wg.dim() != 2 || wg.sizes() != wu.sizes() || x.size(-1) != wg.size(1))
+    refuse("x is [..., hidden], w_gate and w_up [ffn, hidden]");
+  if (wg.scalar_type() != x.scalar_type() || wu.scalar_type() != x.scalar_type()) refuse("x and the weights must share a dtype");
+  const int code = code_of(x.scalar_type());
+  if (code == FAR_F32) throw Status{FAR_ERR_DTYPE};
+  return code;
+}
+struct Mat {
+  const Tensor& t;
+  void* p() const { return t.data_ptr(); }
+  int64_t ld() const { return t.numel() ? rows_of(t).stride : t.dim() ? t.size(-1) : 0; }
+};
+
+// x, w_gate, w_up, activation, save, out, gate_out, up_out
+PyObject* gated_ffn_(PyObject* const* a) {
+  const Tensor &x = tensor(a[0]), &wg = tensor(a[1]), &wu = tensor(a[2]);
+  const int dt = ffn_dtype(x, wg, wu), act = (int)integer(a[3]);
+  const bool save = integer(a[4]) != 0;
+  const int64_t m = rows_in(x), h = wg.size(1), f = wg.size(0);
+  const Place place{&x, &wg, &wu, maybe(a[5]), maybe(a[6]), maybe(a[7])};
+  const Shape shape = with_last(x, f);
+  const char* refusal = "an output has shape [..., ffn] and x's dtype";
+  Out out = given_or(a[5], shape, x.scalar_type(), refusal);
+  Out gate, up;
+  if (save) gate = given_or(a[6], shape, x.scalar_type(), refusal), up = given_or(a[7], shape, x.scalar_type(), refusal);
+  const Mat X{x}, G{wg}, U{wu};
+  const int64_t ldx = X.ld(), ldg = G.ld(), ldu = U.ld();
+  check(unlocked([&] {
+    out.make(place);
+    if (save) gate.make(place), up.make(place);
+    const int64_t ldo = Mat{out.t}.ld();
+    return gated_ffn(X.p(), ldx, G.p(), ldg, U.p(), ldu, out.t.data_ptr(), ldo, save ? gate.t.data_ptr() : nullptr,
+                     save ? Mat{gate.t}.ld() : f, save ? up.t.data_ptr() : nullptr, save ? Mat{up.t}.ld() : f, m, h, f, act, dt,
+                     place.stream);
+  }));
+  return save ? tuple({out.object(), gate.object(), up.object()}) : out.object();
+}
+
+// dout, gate, up, x, w_gate, w_up, activation, dx, dw_gate, dw_up, workspace
+PyObject* gated_ffn_backward_(PyObject* const* a) {
+  const Tensor &d = tensor(a[0]), &gate = tensor(a[1]), &up = tensor(a[2]), &x = tensor(a[3]), &wg = tensor(a[4]), &wu = tensor(a[5]);
+  const int dt = ffn_dtype(x, wg, wu), act = (int)integer(a[6]);
+  const int64_t m = rows_in(x), h = wg.size(1), f = wg.size(0);
+  const Shape shape = with_last(x, f);
+  for (const Tensor* t : {&d, &gate, &up})
+    if (t->sizes() != at::IntArrayRef(shape) || t->scalar_type() != x.scalar_type())
+      refuse("dout, gate and up have shape [..., ffn] and x's dtype");
+  const Tensor* space = maybe(a[10]);
+  const Place place{&d, &gate, &up, &x, &wg, &wu, maybe(a[7]), maybe(a[8]), maybe(a[9]), space};
+  Out dx = given_or(a[7], x.sizes(), x.scalar_type(), "a gradient has its tensor's shape and dtype");
+  Out dwg = given_or(a[8], wg.sizes(), x.scalar_type(), "a gradient has its tensor's shape and dtype");
+  Out dwu = given_or(a[9], wu.sizes(), x.scalar_type(), "a gradient has its tensor's shape and dtype");
+  Workspace workspace(space, far_gated_ffn_backward_workspace_bytes(m, f));
+  const Mat in[6] = {{d}, {gate}, {up}, {x}, {wg}, {wu}};
+  int64_t ld[6];
+  for (int i = 0; i < 6; ++i) ld[i] = in[i].ld();
+  check(unlocked([&] {
+    dx.make(place);
+    dwg.make(place);
+    dwu.make(place);
+    void* wp = workspace.make(place);
+    return gated_ffn_backward(in[0].p(), ld[0], in[1].p(), ld[1], in[2].p(), ld[2], in[3].p(), ld[3], in[4].p(), ld[4],
+                              in[5].p(), ld[5], dx.t.data_ptr(), Mat{dx.t}.ld(), dwg.t.data_ptr(), Mat{dwg.t}.ld(),
+                              dwu.t.data_ptr(), Mat{dwu.t}.ld(), wp, workspace.bytes, m, h, f, act, dt, place.stream);
+  }));
+  return tuple({dx.object(), dwg.object(), dwu.object()});
+}
+
+// ---------------------------------------------------------------------------
 // the module
 // ---------------------------------------------------------------------------
 
@@ -486,6 +648,10 @@ PyMethodDef g_methods[] = {FAR_ENTRY(qk_norm_rope, 10),
                            FAR_ENTRY(norm_quant_block, 7),
                            FAR_ENTRY(quant_block_fp8, 5),
                            FAR_ENTRY(gemm_fp8_block, 6),
+                           FAR_ENTRY(quant_rows_int8, 3),
+                           FAR_ENTRY(gemm_int8, 8),
+                           FAR_ENTRY(gated_ffn, 8),
+                           FAR_ENTRY(gated_ffn_backward, 11),
                            {"init_errors", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&init_errors)), METH_FASTCALL, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_far_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

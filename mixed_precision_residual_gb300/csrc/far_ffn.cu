@@ -4,8 +4,13 @@
 //   dgate = RNE(dh up act'(gate)), dup = RNE(dh act(gate)),
 //   dx = RNE(dgate wg + dup wu),  dwg = RNE(dgate^T x),  dwu = RNE(dup^T x).
 //
+// pair16_kernel  many tokens and every product of the way back: tensor cores over CTA pairs.  The way in
+//                gives a pair 128 columns of both weights at once, gate in one half of the accumulator
+//                and up in the other, so that act(gate) up is formed where they meet.
+// few_kernel     few tokens (a decode batch): the weights' rows on the TMEM lanes, 64 of each a CTA, 16 to
+//                128 tokens as the columns, k split over a cluster.  Bound by reading the weights once.
+// slope_kernel   dgate and dup, into the workspace.  Bound by HBM.
 // plain_gate_kernel, plain_product_kernel  any shape, stride and alignment: 64 x 64 tiles in binary32.
-// slope_kernel                             dgate and dup, into the workspace.  Bound by HBM.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -14,8 +19,10 @@
 #include "far.h"
 #include "far_device.cuh"
 #include "far_launch.h"
+#include "far_pair16.cuh"
 #include "far_params.h"
 #include "far_region.h"
+#include "far_tcgen05.cuh"
 
 namespace far {
 
@@ -83,6 +90,99 @@ template <class F> auto with_types(int dtype, int act, const F& f) {
   };
   return dtype == FAR_F16 ? typed(std::integral_constant<int, FAR_F16>{}) : typed(std::integral_constant<int, FAR_BF16>{});
 }
+
+// ---------------------------------------------------------------------------
+// tensor cores over CTA pairs
+// ---------------------------------------------------------------------------
+
+// 32 columns of a row, 16 words, into the warp's box: 16-byte units 4 half .. 4 half + 3
+__device__ __forceinline__ void box_words(unsigned char* box, int lane, int half, const uint32_t (&v)[16]) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * half + u) ^ (lane & 7)) * 16)) = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+}
+
+struct PairOuts {
+  PairOut out[3];
+};
+
+// The way in: gate in columns 0 .. cols - 1, up in cols .. 2 cols - 1.  SAVE: out, gate and up one after
+// the other, each from the accumulator again.
+template <int DT, int ACT, bool SAVE> struct GateEpilogue {
+  static constexpr bool kAMn = false, kBMn = false, kSplit = true, kDouble = false;
+  static constexpr int kWidth = 128, kStep = 16, kFlush = 0;
+  using Params = PairOuts;
+  static __device__ __forceinline__ bool tile(PairTileAt& at, const PairMaps& maps, const PairWalk& p, const Params& e) {
+    uint32_t t;
+    if (!at.next(p, t)) return false;
+    const int cols = at.item.cols, first = at.part * 64, mine = cols - first;
+    const int64_t row = (int64_t)at.item.tm * 256 + at.rank * 128 + at.quarter * 32, col = at.item.col0 + first;
+    if (mine <= 0) {
+      at.release();
+      return true;
+    }
+    constexpr int OUTS = SAVE ? 3 : 1;
+#pragma unroll 1
+    for (int j = 0; j < OUTS; ++j) {
+      pair_begin_box(e.out[j], at.lane);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (32 * c >= mine) break;
+        uint32_t g[32], u[32], v[16];
+        tmem_ld32x2_sync(t + first + 32 * c, t + cols + first + 32 * c, g, u);
+        if (j == OUTS - 1 && (c == 1 || mine <= 32)) at.release();
+        if (SAVE && j > 0) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            v[i] = j == 1 ? narrow2<DT>(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]))
+                          : narrow2<DT>(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            v[i] = narrow2<DT>(__fmul_rn(activation<ACT>(__uint_as_float(g[2 * i])), __uint_as_float(u[2 * i])),
+                               __fmul_rn(activation<ACT>(__uint_as_float(g[2 * i + 1])), __uint_as_float(u[2 * i + 1])));
+        }
+        box_words(at.box, at.lane, c, v);
+      }
+      pair_store_box(e.out[j], &maps.out[j], at.box, at.lane, row, col);
+    }
+    return true;
+  }
+};
+
+// The products of the way back, rounded.  dx: rows of dgate and dup, both summed; the weights' rows are k.
+// WEIGHTS: dgate and dup give the rows of one output each, tokens are k.
+template <int DT, bool WEIGHTS> struct ProductEpilogue {
+  static constexpr bool kAMn = WEIGHTS, kBMn = true, kSplit = false, kDouble = WEIGHTS;
+  static constexpr int kWidth = 256, kStep = 32, kFlush = 0;
+  using Params = PairOuts;
+  static __device__ __forceinline__ bool tile(PairTileAt& at, const PairMaps& maps, const PairWalk& p, const Params& e) {
+    uint32_t t;
+    if (!at.next(p, t)) return false;
+    const int first = at.part * 128, mine = at.item.cols - first;
+    const int tiles = WEIGHTS ? p.tiles_m / 2 : p.tiles_m, which = WEIGHTS && at.item.tm >= tiles ? 1 : 0;
+    const int64_t row = (int64_t)(at.item.tm - which * tiles) * 256 + at.rank * 128 + at.quarter * 32;
+    if (mine <= 0) {
+      at.release();
+      return true;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (32 * c >= mine) break;
+      uint32_t r[32], v[16];
+      tmem_ld32_sync(t + first + 32 * c, r);
+      const bool last = c == 3 || mine <= 32 * (c + 1);
+      if (last) at.release();
+      if ((c & 1) == 0) pair_begin_box(e.out[which], at.lane);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = narrow2<DT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+      box_words(at.box, at.lane, c & 1, v);
+      if ((c & 1) == 1 || last)
+        pair_store_box(e.out[which], &maps.out[which], at.box, at.lane, row, at.item.col0 + first + 64 * (c >> 1));
+    }
+    return true;
+  }
+};
 
 // ---------------------------------------------------------------------------
 // plain kernels
@@ -196,6 +296,167 @@ template <int DT> __global__ void __launch_bounds__(256) plain_product_kernel(co
 }
 
 // ---------------------------------------------------------------------------
+// few_kernel: 64 rows of each weight x NT tokens a CTA, the slices of 64 of k shared out over a cluster of
+// gridDim's x dimension (CTA rank r takes slices KB r / S .. KB (r + 1) / S - 1).
+//   warp 0 TMA producer, 1 MMA issuer (and TMEM), 4-7 read the sums: rows 0 .. 63 gate, 64 .. 127 up.
+// Each CTA leaves its sums in its shared memory; the cluster's CTAs add up every S-th token over all of
+// them, in the order of k, and form the outputs.
+// ---------------------------------------------------------------------------
+constexpr int kFewThreads = 256;
+template <int NT> struct FewShape {
+  static constexpr int ctas = 2;  // an SM
+  static constexpr uint32_t a_bytes = 2 * kPair16Box, b_bytes = NT * 128;
+  static constexpr int stages = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 4 : 3;
+  static constexpr uint32_t ring = stages * (a_bytes + b_bytes);
+  static constexpr uint32_t tmem_cols = NT < 32 ? 32 : NT;
+  static constexpr int bars = 2 * stages + 1;
+  static constexpr size_t smem = ring + bars * 8 + 16 + 1024;
+  static_assert(NT * 128 * 4 <= ring, "the sums that the cluster adds up lie in the ring");
+};
+
+template <int NT, int DT, int ACT>
+__global__ void __launch_bounds__(kFewThreads, FewShape<NT>::ctas)
+    few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
+               const __grid_constant__ CUtensorMap map_u, const __grid_constant__ GateParams p) {
+  using S = FewShape<NT>;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  unsigned char* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);  // the same offset in every CTA
+  const uint32_t a_base = smem_addr(smem), b_base = a_base + S::stages * S::a_bytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::ring);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + S::bars);
+  const uint32_t full0 = smem_addr(&bars[0]), empty0 = full0 + 8 * S::stages, done = empty0 + 8 * S::stages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = (int)gridDim.x, rank = (int)blockIdx.x;  // the cluster spans gridDim.x
+  const int64_t n0 = (int64_t)blockIdx.y * 64, m0 = (int64_t)blockIdx.z * NT;
+  const int KB = (int)(((int64_t)p.K + 63) / 64);
+  const int kb0 = (int)((int64_t)KB * rank / split), kb1 = (int)((int64_t)KB * (rank + 1) / split);
+
+  // the ring's first load of the weights starts for L2 while the CTA is set up and the kernel ahead drains
+  if (warp == 3 && lane == 0)
+    for (int kb = kb0; kb < kb1 && kb < kb0 + S::stages; ++kb) {
+      tma_prefetch_2d(&map_g, kb * 64, (int)n0);
+      tma_prefetch_2d(&map_u, kb * 64, (int)n0);
+    }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::stages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    mbar_init(done, 1);
+    fence_barrier_init();
+    tma_prefetch_map(&map_x);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_slot), S::tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();  // (not before the TMEM columns are this CTA's)
+  pdl_wait();
+
+  float* sums = reinterpret_cast<float*>(smem);
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t g = 0;
+      bool running = true;
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
+        const uint32_t s = g % S::stages;
+        if (!mbar_wait(empty0 + 8 * s, ((g / S::stages) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+          running = false;
+          break;
+        }
+        mbar_arrive_expect_tx(full0 + 8 * s, S::a_bytes + S::b_bytes);
+        tma_load_2d(a_base + s * S::a_bytes, &map_g, kb * 64, (int)n0, full0 + 8 * s);
+        tma_load_2d(a_base + s * S::a_bytes + kPair16Box, &map_u, kb * 64, (int)n0, full0 + 8 * s);
+        tma_load_2d(b_base + s * S::b_bytes, &map_x, kb * 64, (int)m0, full0 + 8 * s);
+      }
+      // Before the CTA may leave the last slices must have landed and their slots been freed by the MMA
+      // issuer's last commits (the barriers they arrive on go with the CTA).
+      const uint32_t last = g > (uint32_t)S::stages ? g - S::stages : 0u;
+      for (uint32_t j = last; j < g; ++j)
+        mbar_wait(full0 + 8 * (j % S::stages), (j / S::stages) & 1u, p.timeout_ns, p.status);
+      for (uint32_t j = last; running && j < g; ++j)
+        running = mbar_wait(empty0 + 8 * (j % S::stages), (j / S::stages) & 1u, p.timeout_ns, p.status);
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t IDESC = umma_idesc_16(128, NT, DT == FAR_BF16, false, false);
+    const bool leader = elect_one();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t a0 = sw128_kmajor_desc(a_base), x0 = sw128_kmajor_desc(b_base);
+    uint32_t s = 0, s_phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(full0 + 8 * s, s_phase, p.timeout_ns, p.status)) break;
+      tc_fence_after();
+      const uint64_t a = a0 + s * (S::a_bytes >> 4), x = x0 + s * (S::b_bytes >> 4);
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) umma_f16(tm, a + 2 * k, x + 2 * k, IDESC, (kb != kb0) | (k != 0));
+        umma_commit(empty0 + 8 * s);
+        if (kb == kb1 - 1) umma_commit(done);
+      }
+      __syncwarp();
+      if (++s == S::stages) {
+        s = 0;
+        s_phase ^= 1;
+      }
+    }
+  } else if (warp >= 4) {
+    // (a wait that runs out leaves the error word set and the outputs undefined)
+    mbar_wait(done, 0u, p.timeout_ns, p.status);
+    tc_fence_after();
+    // every MMA has read its operands, so every copy has landed: the ring now takes this CTA's sums [NT][128]
+    const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    constexpr int W = NT == 16 ? 16 : 32;  // columns a load
+#pragma unroll
+    for (int c = 0; c < NT; c += W) {
+      uint32_t r[W];
+      if constexpr (W == 32) tmem_ld32(src + c, r);
+      else tmem_ld16(src + c, r);
+      tmem_ld_wait(r);
+#pragma unroll
+      for (int i = 0; i < W; ++i) sums[(c + i) * 128 + (int)threadIdx.x - 128] = __uint_as_float(r[i]);
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::tmem_cols);
+  }
+  if (split > 1) cluster_sync();
+  const int f = threadIdx.x & 63;
+  const int64_t n = n0 + f;
+  for (int c = rank + split * (int)(threadIdx.x >> 6); c < NT && m0 + c < p.M; c += 4 * split) {
+    const uint32_t at = smem_addr(sums) + (c * 128 + f) * 4;
+    float g[8], u[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < split) {
+        const uint32_t a = map_to_cta(at, q);
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(g[q]) : "r"(a) : "memory");
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u[q]) : "r"(a + 256) : "memory");
+      }
+    float gate = g[0], up = u[0];
+#pragma unroll
+    for (int q = 1; q < 8; ++q)
+      if (q < split) gate = __fadd_rn(gate, g[q]), up = __fadd_rn(up, u[q]);
+    if (n < p.F) {
+      p.out[(m0 + c) * p.ldo + n] = round16<DT>(__fmul_rn(activation<ACT>(gate), up));
+      if (p.gate) {
+        p.gate[(m0 + c) * p.ldgate + n] = round16<DT>(gate);
+        p.up[(m0 + c) * p.ldup + n] = round16<DT>(up);
+      }
+    }
+  }
+  if (split > 1) cluster_sync();  // no CTA leaves while another still reads its sums
+}
+
+// ---------------------------------------------------------------------------
 // dgate and dup: rows of `ld` elements, a multiple of 8, in the workspace
 // ---------------------------------------------------------------------------
 
@@ -284,16 +545,100 @@ unsigned plain_grid(int64_t m, int64_t n, int sms) {
   return (unsigned)(tiles < cap ? tiles : cap);
 }
 
+struct GatePlan {
+  int kind;   // 0 plain, 1 pairs, 2 few
+  int nt;     // few: tokens a CTA
+  int split;  // few: CTAs that share a tile's k
+};
+
+GatePlan plan_gate(const GateParams& p, int sms) {
+  GatePlan g{0, 0, 0};
+  if (p.K == 0 || !tma_rows(p.x, p.ldx, 2) || !tma_rows(p.wg, p.ldwg, 2) || !tma_rows(p.wu, p.ldwu, 2)) return g;
+  g.nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  const int64_t tiles_n = ((int64_t)p.F + 63) / 64, tiles_m = ((int64_t)p.M + g.nt - 1) / g.nt, slots = 2ll * sms;
+  const int64_t slices = ((int64_t)p.K + 63) / 64;
+  // k is shared out while there are free places for it, not below four slices a CTA
+  g.split = 1;
+  while (g.split < 8 && tiles_n * tiles_m * g.split * 2 <= slots && slices >= 8 * g.split) g.split *= 2;
+  const bool fits = tiles_n <= 65535 && tiles_m <= 65535;
+  g.kind = fits && p.M <= 128 ? 2 : 1;
+  const int64_t pair_tiles = (((int64_t)p.M + 255) / 256) * (((int64_t)p.F + 127) / 128);
+  if (g.kind == 1 && pair_tiles > INT32_MAX) g.kind = 0;
+  return g;
+}
+
+template <int NT, int DT, int ACT> cudaError_t launch_few(const CUtensorMap* maps, const GateParams& p, int split, cudaStream_t s) {
+  const void* f = reinterpret_cast<const void*>(few_kernel<NT, DT, ACT>);
+  const cudaError_t e = ensure_smem_attribute(f, FewShape<NT>::smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)split, (unsigned)((p.F + 63ll) / 64), (unsigned)(((int64_t)p.M + NT - 1) / NT));
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = FewShape<NT>::smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = far_get_programmatic_launch() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, few_kernel<NT, DT, ACT>, maps[0], maps[1], maps[2], p);
+}
+
 int run_gate(GateParams& p, int dtype, int act, cudaStream_t s) {
   unsigned int* status = nullptr;
   int sms = 0;
-  const int st = device_info(&status, &sms);
+  int st = device_info(&status, &sms);
   if (st != FAR_OK) return st;
   p.status = status;
   p.timeout_ns = kWaitTimeoutNs;
-  const cudaError_t e = with_types(dtype, act, [&](auto dt, auto a) {
-    return launch_k(plain_gate_kernel<decltype(dt)::value, decltype(a)::value>, dim3(plain_grid(p.M, p.F, sms)), dim3(256), 0, s, p);
-  });
+  const GatePlan g = plan_gate(p, sms);
+  cudaError_t e;
+  if (g.kind == 0) {
+    e = with_types(dtype, act, [&](auto dt, auto a) {
+      return launch_k(plain_gate_kernel<decltype(dt)::value, decltype(a)::value>, dim3(plain_grid(p.M, p.F, sms)), dim3(256), 0, s, p);
+    });
+  } else if (g.kind == 2) {
+    CUtensorMap maps[3];
+    st = encode_box(&maps[0], p.x, p.M, p.K, p.ldx, 2, g.nt, tma_type(dtype));
+    if (st == FAR_OK) st = encode_operand(&maps[1], p.wg, p.F, p.K, p.ldwg, dtype);
+    if (st == FAR_OK) st = encode_operand(&maps[2], p.wu, p.F, p.K, p.ldwu, dtype);
+    if (st != FAR_OK) return st;
+    e = with_types(dtype, act, [&](auto dt, auto a) {
+      constexpr int DT = decltype(dt)::value, ACT = decltype(a)::value;
+      return g.nt == 16   ? launch_few<16, DT, ACT>(maps, p, g.split, s)
+             : g.nt == 32 ? launch_few<32, DT, ACT>(maps, p, g.split, s)
+             : g.nt == 64 ? launch_few<64, DT, ACT>(maps, p, g.split, s)
+                          : launch_few<128, DT, ACT>(maps, p, g.split, s);
+    });
+  } else {
+    PairMaps maps{};
+    PairOuts outs{};
+    st = encode_operand(&maps.a[0], p.x, p.M, p.K, p.ldx, dtype);
+    if (st == FAR_OK) st = encode_operand(&maps.b[0], p.wg, p.F, p.K, p.ldwg, dtype);
+    if (st == FAR_OK) st = encode_operand(&maps.b[1], p.wu, p.F, p.K, p.ldwu, dtype);
+    if (st == FAR_OK) st = pair_output(&outs.out[0], &maps.out[0], p.out, p.M, p.F, p.ldo, dtype);
+    if (st == FAR_OK && p.gate) st = pair_output(&outs.out[1], &maps.out[1], p.gate, p.M, p.F, p.ldgate, dtype);
+    if (st == FAR_OK && p.gate) st = pair_output(&outs.out[2], &maps.out[2], p.up, p.M, p.F, p.ldup, dtype);
+    if (st != FAR_OK) return st;
+    PairWalk w{};
+    w.tiles_m = (int32_t)(((int64_t)p.M + 255) / 256);
+    w.tiles_n = (int32_t)(((int64_t)p.F + 127) / 128);
+    w.num_tiles = w.tiles_m * w.tiles_n;
+    w.columns = p.F;
+    w.slices = (int32_t)(((int64_t)p.K + 63) / 64);
+    w.pairs = 1;
+    w.bf16 = dtype == FAR_BF16;
+    w.status = status;
+    w.timeout_ns = kWaitTimeoutNs;
+    e = with_types(dtype, act, [&](auto dt, auto a) {
+      constexpr int DT = decltype(dt)::value, ACT = decltype(a)::value;
+      return p.gate ? launch_pair16<GateEpilogue<DT, ACT, true>>(maps, w, outs, sms, s)
+                    : launch_pair16<GateEpilogue<DT, ACT, false>>(maps, w, outs, sms, s);
+    });
+  }
   return e == cudaSuccess ? FAR_OK : cuda_error_status(e);
 }
 
@@ -309,7 +654,7 @@ struct BackCall {
 int run_back(const BackCall& c, int dtype, int act, cudaStream_t s) {
   unsigned int* status = nullptr;
   int sms = 0;
-  const int st = device_info(&status, &sms);
+  int st = device_info(&status, &sms);
   if (st != FAR_OK) return st;
   const int64_t ld = padded(c.F);
   uint16_t *dg = c.ws, *du = c.ws + c.M * ld;
@@ -330,9 +675,54 @@ int run_back(const BackCall& c, int dtype, int act, cudaStream_t s) {
     e = launch_k(dtype == FAR_F16 ? plain_product_kernel<FAR_F16> : plain_product_kernel<FAR_BF16>, dim3(plain_grid(p.M, p.N, sms)),
                  dim3(256), 0, s, p);
   };
-  product(ProductParams{{dg, du}, {c.wg, c.wu}, c.dx, {ld, ld}, {1, 1}, {1, 1}, {c.ldwg, c.ldwu}, c.lddx, c.M, c.K, c.F, 2});
-  product(ProductParams{{dg, dg}, {c.x, c.x}, c.dwg, {1, 1}, {ld, ld}, {1, 1}, {c.ldx, c.ldx}, c.lddwg, c.F, c.K, c.M, 1});
-  product(ProductParams{{du, du}, {c.x, c.x}, c.dwu, {1, 1}, {ld, ld}, {1, 1}, {c.ldx, c.ldx}, c.lddwu, c.F, c.K, c.M, 1});
+  auto tiles = [](int64_t n) { return (n + 255) / 256; };
+  const int64_t dx_tiles = tiles(c.M) * tiles(c.K), dw_tiles = 2 * tiles(c.F) * tiles(c.K);
+  const bool dx_tma = c.M && c.F && tma_rows(c.wg, c.ldwg, 2) && tma_rows(c.wu, c.ldwu, 2) && dx_tiles <= INT32_MAX;
+  const bool dw_tma = c.M && c.F && tma_rows(c.x, c.ldx, 2) && dw_tiles <= INT32_MAX;
+  PairWalk w{};
+  w.columns = c.K;
+  w.tiles_n = (int32_t)tiles(c.K);
+  w.bf16 = dtype == FAR_BF16;
+  w.status = status;
+  w.timeout_ns = kWaitTimeoutNs;
+  PairMaps maps{};
+  PairOuts outs{};
+  if (dx_tma || dw_tma) {
+    st = encode_operand(&maps.a[0], dg, c.M, c.F, ld, dtype);
+    if (st == FAR_OK) st = encode_operand(&maps.a[1], du, c.M, c.F, ld, dtype);
+    if (st != FAR_OK) return st;
+  }
+  if (dx_tma) {
+    st = encode_operand(&maps.b[0], c.wg, c.F, c.K, c.ldwg, dtype);
+    if (st == FAR_OK) st = encode_operand(&maps.b[1], c.wu, c.F, c.K, c.ldwu, dtype);
+    if (st == FAR_OK) st = pair_output(&outs.out[0], &maps.out[0], c.dx, c.M, c.K, c.lddx, dtype);
+    if (st != FAR_OK) return st;
+    w.tiles_m = (int32_t)tiles(c.M);
+    w.num_tiles = (int32_t)dx_tiles;
+    w.slices = (int32_t)(((int64_t)c.F + 63) / 64);
+    w.pairs = 2;
+    if (e == cudaSuccess)
+      e = dtype == FAR_F16 ? launch_pair16<ProductEpilogue<FAR_F16, false>>(maps, w, outs, sms, s)
+                           : launch_pair16<ProductEpilogue<FAR_BF16, false>>(maps, w, outs, sms, s);
+  } else {
+    product(ProductParams{{dg, du}, {c.wg, c.wu}, c.dx, {ld, ld}, {1, 1}, {1, 1}, {c.ldwg, c.ldwu}, c.lddx, c.M, c.K, c.F, 2});
+  }
+  if (dw_tma) {
+    st = encode_operand(&maps.b[0], c.x, c.M, c.K, c.ldx, dtype);
+    if (st == FAR_OK) st = pair_output(&outs.out[0], &maps.out[0], c.dwg, c.F, c.K, c.lddwg, dtype);
+    if (st == FAR_OK) st = pair_output(&outs.out[1], &maps.out[1], c.dwu, c.F, c.K, c.lddwu, dtype);
+    if (st != FAR_OK) return st;
+    w.tiles_m = (int32_t)(2 * tiles(c.F));
+    w.num_tiles = (int32_t)dw_tiles;
+    w.slices = (int32_t)(((int64_t)c.M + 63) / 64);
+    w.pairs = 1;
+    if (e == cudaSuccess)
+      e = dtype == FAR_F16 ? launch_pair16<ProductEpilogue<FAR_F16, true>>(maps, w, outs, sms, s)
+                           : launch_pair16<ProductEpilogue<FAR_BF16, true>>(maps, w, outs, sms, s);
+  } else {
+    product(ProductParams{{dg, dg}, {c.x, c.x}, c.dwg, {1, 1}, {ld, ld}, {1, 1}, {c.ldx, c.ldx}, c.lddwg, c.F, c.K, c.M, 1});
+    product(ProductParams{{du, du}, {c.x, c.x}, c.dwu, {1, 1}, {ld, ld}, {1, 1}, {c.ldx, c.ldx}, c.lddwu, c.F, c.K, c.M, 1});
+  }
   return e == cudaSuccess ? FAR_OK : cuda_error_status(e);
 }
 

@@ -8,8 +8,10 @@
 // one round.
 //   warp 0     TMA producer (both CTAs): a ring of 6 slices running across tiles
 //   warp 1     MMA issuer (even CTA); allocates TMEM: two accumulators of 256 columns
-//   warps 2-9  epilogue, one accumulator behind: warp w the TMEM lanes 32 (w % 4) .. and one half of
+//   warps 4-11 epilogue, one accumulator behind: warp w the TMEM lanes 32 (w % 4) .. and one half of
 //              the columns
+// The registers a thread: 384 threads are launched at 168; warps 0-3 give theirs up to 72 and the
+// epilogue's take 216 (128 x 72 + 256 x 216 = 384 x 168), so that a thread may keep 128 sums.
 // An operand may lie either way in memory, both read by 64 x 64 boxes with the 128-byte swizzle:
 // k-major (rows of k values: a box is 64 rows x 128 bytes of k) or mn-major (rows of k are the
 // memory's columns: a box is 64 values of k x 128 bytes of rows).  So no operand is transposed first.
@@ -32,7 +34,7 @@ cudaError_t ensure_smem_attribute(const void* func, size_t bytes);
 
 constexpr int kPair16Stages = 6;
 constexpr int kPair16Epilogue = 8;  // warps
-constexpr int kPair16Threads = 64 + 32 * kPair16Epilogue;
+constexpr int kPair16Threads = 128 + 32 * kPair16Epilogue;
 constexpr uint32_t kPair16Slice = 128 * 64 * 2;  // bytes of a slice of A or B in a CTA
 constexpr uint32_t kPair16Box = 64 * 64 * 2;
 constexpr uint32_t kPair16Ring = kPair16Stages * 2 * kPair16Slice;
@@ -201,9 +203,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair16Threads, 1)
   pdl_launch_dependents();  // (not before the TMEM columns are this CTA's: a dependent that took them would wait for this grid)
   pdl_wait();
 
-  PairItem w;
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    PairItem w;
+    if (warp == 0 && lane == 0) {
       // ---------------- TMA producer (both CTAs) ----------------
       uint32_t g = 0;
       bool ok = true;
@@ -249,9 +252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair16Threads, 1)
           mbar_wait(full0 + 8 * (j % kPair16Stages), (j / kPair16Stages) & 1u, p.timeout_ns, p.status);
       for (uint32_t j = last; ok && j < g; ++j)
         ok = mbar_wait(empty0 + 8 * (j % kPair16Stages), (j / kPair16Stages) & 1u, p.timeout_ns, p.status);
-    }
-  } else if (warp == 1) {
-    if (rank == 0) {
+    } else if (warp == 1 && rank == 0) {
       // ---------------- MMA issuer (even CTA) ----------------
       const bool leader = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -298,16 +299,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair16Threads, 1)
       }
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---------------- epilogue ----------------
     PairTileAt at;
     at.rank = (int)rank;
     at.quarter = warp & 3;
-    at.part = (warp - 2) >> 2;
+    at.part = (warp - 4) >> 2;
     at.lane = lane;
     at.tmem = tmem + ((uint32_t)(at.quarter * 32) << 16);
     at.acc_full = acc_full0;
     at.acc_empty_even = map_to_cta(acc_empty0, 0);
-    at.box = smem + kPair16Ring + (warp - 2) * 4096;
+    at.box = smem + kPair16Ring + (warp - 4) * 4096;
     at.uses = 0;
     for (int n = 0; pair_item<E::kWidth, E::kStep>(p, pair, num_pairs, n, at.item); ++n) {
       if (at.item.cols == 0) continue;

@@ -465,6 +465,10 @@ int gemm_int8(const void* x, int64_t x_row_stride, const float* x_scale, const v
               const float* wt_scale, const void* bias, void* out, int64_t out_row_stride, void* workspace,
               int64_t workspace_bytes, int64_t m, int64_t n, int64_t k, int out_dtype, void* stream);
 
+/* the product's plan (host logic only; operands that TMA can read): out3 = {kind (0 plain, 1 CTA pairs, 2 few
+   rows of x a CTA), rows of x a tile, CTAs that share a tile's k (kind 2)} */
+int far_plan_gemm_int8(int64_t m, int64_t n, int64_t k, int* out3);
+
 /*
  * The gated feed-forward block's way in, both projections, the activation and the product in one
  * kernel: with gate = x @ w_gate^T and up = x @ w_up^T (binary32 sums of exact products),
@@ -492,6 +496,10 @@ int gated_ffn(const void* x, int64_t x_row_stride, const void* w_gate, int64_t w
               int64_t w_up_row_stride, void* out, int64_t out_row_stride, void* gate_out, int64_t gate_out_row_stride,
               void* up_out, int64_t up_out_row_stride, int64_t tokens, int64_t hidden, int64_t ffn, int activation,
               int dtype, void* stream);
+
+/* its plan (host logic only; operands that TMA can read): out3 = {kind (0 plain, 1 CTA pairs, 2 few tokens a CTA),
+   tokens a CTA (kind 2), CTAs that share a tile's k (kind 2)} */
+int far_plan_gated_ffn(int64_t tokens, int64_t hidden, int64_t ffn, int* out3);
 
 /*
  * Its gradients, given that of out and the projections that gated_ffn kept:

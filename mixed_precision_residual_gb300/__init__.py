@@ -544,7 +544,7 @@ def rmsnorm_quant_host(x, weight, eps, qtype, q, scale, workspace, stream=None) 
 
 from .block import (fused_add_rmsnorm_quant_block, gemm_fp8_block, plan_gemm_fp8_for_sms, quant_block_fp8,  # noqa: E402
                     rmsnorm_quant_block)
-from .ffn import gated_ffn, gated_ffn_backward, gated_ffn_backward_workspace_bytes  # noqa: E402
+from .ffn import gated_ffn, gated_ffn_backward, gated_ffn_backward_workspace_bytes, plan_gated_ffn  # noqa: E402
 from .heads import (qk_backward_workspace_bytes, qk_norm_rope, qk_norm_rope_backward, rope, rope_backward,  # noqa: E402
                     rope_frequencies, rope_table)
-from .int8 import gemm_int8, gemm_int8_workspace_bytes, quant_rows_int8  # noqa: E402
+from .int8 import gemm_int8, gemm_int8_workspace_bytes, plan_gemm_int8, quant_rows_int8  # noqa: E402

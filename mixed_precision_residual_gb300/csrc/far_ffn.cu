@@ -109,8 +109,8 @@ struct PairOuts {
 // The way in: gate in columns 0 .. cols - 1, up in cols .. 2 cols - 1.  SAVE: out, gate and up one after
 // the other, each from the accumulator again.
 template <int DT, int ACT, bool SAVE> struct GateEpilogue {
-  static constexpr bool kAMn = false, kBMn = false, kSplit = true, kDouble = false;
-  static constexpr int kWidth = 128, kStep = 16, kFlush = 0;
+  static constexpr bool kAMn = false, kBMn = false, kSplit = true, kDouble = false, kBeside = false;
+  static constexpr int kWidth = 128, kStep = 16;
   using Params = PairOuts;
   static __device__ __forceinline__ bool tile(PairTileAt& at, const PairMaps& maps, const PairWalk& p, const Params& e) {
     uint32_t t;
@@ -151,10 +151,11 @@ template <int DT, int ACT, bool SAVE> struct GateEpilogue {
 };
 
 // The products of the way back, rounded.  dx: rows of dgate and dup, both summed; the weights' rows are k.
-// WEIGHTS: dgate and dup give the rows of one output each, tokens are k.
+// WEIGHTS: dgate and dup give the rows of one output each, tokens are k; launched behind dx, which lets it start
+// beside itself (as every kernel of dx does).
 template <int DT, bool WEIGHTS> struct ProductEpilogue {
-  static constexpr bool kAMn = WEIGHTS, kBMn = true, kSplit = false, kDouble = WEIGHTS;
-  static constexpr int kWidth = 256, kStep = 32, kFlush = 0;
+  static constexpr bool kAMn = WEIGHTS, kBMn = true, kSplit = false, kDouble = WEIGHTS, kBeside = WEIGHTS;
+  static constexpr int kWidth = 256, kStep = 32;
   using Params = PairOuts;
   static __device__ __forceinline__ bool tile(PairTileAt& at, const PairMaps& maps, const PairWalk& p, const Params& e) {
     uint32_t t;
@@ -255,8 +256,8 @@ struct ProductParams {
 };
 template <int DT> __global__ void __launch_bounds__(256) plain_product_kernel(const ProductParams p) {
   __shared__ float as[32][65], bs[32][65];
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // (behind the wait for what runs beside dx)
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int64_t tiles_n = ((int64_t)p.N + 63) / 64, tiles = tiles_n * (((int64_t)p.M + 63) / 64);
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
@@ -296,12 +297,27 @@ template <int DT> __global__ void __launch_bounds__(256) plain_product_kernel(co
 }
 
 // ---------------------------------------------------------------------------
-// few_kernel: 64 rows of each weight x NT tokens a CTA, the slices of 64 of k shared out over a cluster of
+// few_kernel: 128 rows of weights x NT tokens a CTA, the slices of 64 of k shared out over a cluster of
 // gridDim's x dimension (CTA rank r takes slices KB r / S .. KB (r + 1) / S - 1).
-//   warp 0 TMA producer, 1 MMA issuer (and TMEM), 4-7 read the sums: rows 0 .. 63 gate, 64 .. 127 up.
+//   warp 0 TMA producer, 1 MMA issuer (and TMEM), 4-7 read the sums
 // Each CTA leaves its sums in its shared memory; the cluster's CTAs add up every S-th token over all of
 // them, in the order of k, and form the outputs.
+//   GATE  64 rows of either weight: gate in lanes 0 .. 63, up in 64 .. 127
+//   else  dx: 128 columns of the weights (mn-major), k all rows of w_gate and then all of w_up
 // ---------------------------------------------------------------------------
+struct FewParams {
+  uint16_t *out, *gate, *up;     // gate and up may be null
+  int64_t ldo, ldgate, ldup;     // elements
+  int32_t M, N;                  // tokens, columns of an output
+  int32_t slices, half;          // of k; dx: of which the first `half` are w_gate's
+  int32_t wide;                  // bits: out's, gate's, up's rows start on 8 bytes
+  unsigned int* status;
+  uint64_t timeout_ns;
+};
+struct FewMaps {
+  CUtensorMap w[2], x[2];  // GATE: x[0] alone
+};
+
 constexpr int kFewThreads = 256;
 template <int NT> struct FewShape {
   static constexpr int ctas = 2;  // an SM
@@ -314,10 +330,42 @@ template <int NT> struct FewShape {
   static_assert(NT * 128 * 4 <= ring, "the sums that the cluster adds up lie in the ring");
 };
 
-template <int NT, int DT, int ACT>
+// four neighbouring rows' sums over the cluster's CTAs, in their order
+__device__ __forceinline__ void cluster_sums4(uint32_t at, int split, float (&sum)[4]) {
+  float v[8][4];
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    if (q < split)
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[q][0]), "=f"(v[q][1]), "=f"(v[q][2]), "=f"(v[q][3])
+                   : "r"(map_to_cta(at, q))
+                   : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum[i] = v[0][i];
+#pragma unroll
+  for (int q = 1; q < 8; ++q)
+    if (q < split) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] = __fadd_rn(sum[i], v[q][i]);
+    }
+}
+
+// four neighbouring values of an output row, in one store where the row allows it
+template <int DT> __device__ __forceinline__ void store4(uint16_t* row, int64_t n, int64_t N, bool wide, const float (&v)[4]) {
+  const uint32_t lo = narrow2<DT>(v[0], v[1]), hi = narrow2<DT>(v[2], v[3]);
+  if (wide && n + 4 <= N) {
+    *reinterpret_cast<uint2*>(row + n) = make_uint2(lo, hi);
+    return;
+  }
+  const uint16_t h[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < N) row[n + i] = h[i];
+}
+
+template <int NT, int DT, int ACT, bool GATE>
 __global__ void __launch_bounds__(kFewThreads, FewShape<NT>::ctas)
-    few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
-               const __grid_constant__ CUtensorMap map_u, const __grid_constant__ GateParams p) {
+    few_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewParams p) {
   using S = FewShape<NT>;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -328,15 +376,21 @@ __global__ void __launch_bounds__(kFewThreads, FewShape<NT>::ctas)
   const uint32_t full0 = smem_addr(&bars[0]), empty0 = full0 + 8 * S::stages, done = empty0 + 8 * S::stages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = (int)gridDim.x, rank = (int)blockIdx.x;  // the cluster spans gridDim.x
-  const int64_t n0 = (int64_t)blockIdx.y * 64, m0 = (int64_t)blockIdx.z * NT;
-  const int KB = (int)(((int64_t)p.K + 63) / 64);
-  const int kb0 = (int)((int64_t)KB * rank / split), kb1 = (int)((int64_t)KB * (rank + 1) / split);
+  constexpr int ROWS = GATE ? 64 : 128;  // of the output's columns
+  const int64_t n0 = (int64_t)blockIdx.y * ROWS, m0 = (int64_t)blockIdx.z * NT;
+  const int kb0 = (int)((int64_t)p.slices * rank / split), kb1 = (int)((int64_t)p.slices * (rank + 1) / split);
 
   // the ring's first load of the weights starts for L2 while the CTA is set up and the kernel ahead drains
   if (warp == 3 && lane == 0)
     for (int kb = kb0; kb < kb1 && kb < kb0 + S::stages; ++kb) {
-      tma_prefetch_2d(&map_g, kb * 64, (int)n0);
-      tma_prefetch_2d(&map_u, kb * 64, (int)n0);
+      if constexpr (GATE) {
+        tma_prefetch_2d(&maps.w[0], kb * 64, (int)n0);
+        tma_prefetch_2d(&maps.w[1], kb * 64, (int)n0);
+      } else {
+        const int q = kb >= p.half, k = (kb - (q ? p.half : 0)) * 64;
+        tma_prefetch_2d(&maps.w[q], (int)n0, k);
+        tma_prefetch_2d(&maps.w[q], (int)n0 + 64, k);
+      }
     }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::stages; ++s) {
@@ -345,7 +399,7 @@ __global__ void __launch_bounds__(kFewThreads, FewShape<NT>::ctas)
     }
     mbar_init(done, 1);
     fence_barrier_init();
-    tma_prefetch_map(&map_x);
+    tma_prefetch_map(&maps.x[0]);
   }
   if (warp == 1) {
     tmem_alloc(smem_addr(tmem_slot), S::tmem_cols);
@@ -355,8 +409,8 @@ __global__ void __launch_bounds__(kFewThreads, FewShape<NT>::ctas)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_launch_dependents();  // (not before the TMEM columns are this CTA's)
   pdl_wait();
+  pdl_launch_dependents();  // (not before the TMEM columns are this CTA's; behind the wait for what runs beside dx)
 
   float* sums = reinterpret_cast<float*>(smem);
   if (warp == 0) {
@@ -370,9 +424,17 @@ __global__ void __launch_bounds__(kFewThreads, FewShape<NT>::ctas)
           break;
         }
         mbar_arrive_expect_tx(full0 + 8 * s, S::a_bytes + S::b_bytes);
-        tma_load_2d(a_base + s * S::a_bytes, &map_g, kb * 64, (int)n0, full0 + 8 * s);
-        tma_load_2d(a_base + s * S::a_bytes + kPair16Box, &map_u, kb * 64, (int)n0, full0 + 8 * s);
-        tma_load_2d(b_base + s * S::b_bytes, &map_x, kb * 64, (int)m0, full0 + 8 * s);
+        const uint32_t a = a_base + s * S::a_bytes, b = b_base + s * S::b_bytes;
+        if constexpr (GATE) {
+          tma_load_2d(a, &maps.w[0], kb * 64, (int)n0, full0 + 8 * s);
+          tma_load_2d(a + kPair16Box, &maps.w[1], kb * 64, (int)n0, full0 + 8 * s);
+          tma_load_2d(b, &maps.x[0], kb * 64, (int)m0, full0 + 8 * s);
+        } else {
+          const int q = kb >= p.half, k = (kb - (q ? p.half : 0)) * 64;
+          tma_load_2d(a, &maps.w[q], (int)n0, k, full0 + 8 * s);
+          tma_load_2d(a + kPair16Box, &maps.w[q], (int)n0 + 64, k, full0 + 8 * s);
+          tma_load_2d(b, &maps.x[q], k, (int)m0, full0 + 8 * s);
+        }
       }
       // Before the CTA may leave the last slices must have landed and their slots been freed by the MMA
       // issuer's last commits (the barriers they arrive on go with the CTA).
@@ -383,10 +445,11 @@ __global__ void __launch_bounds__(kFewThreads, FewShape<NT>::ctas)
         running = mbar_wait(empty0 + 8 * (j % S::stages), (j / S::stages) & 1u, p.timeout_ns, p.status);
     }
   } else if (warp == 1) {
-    constexpr uint32_t IDESC = umma_idesc_16(128, NT, DT == FAR_BF16, false, false);
+    constexpr uint32_t IDESC = umma_idesc_16(128, NT, DT == FAR_BF16, !GATE, false);
+    constexpr uint32_t a_step = GATE ? 2 : 128;
     const bool leader = elect_one();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t a0 = sw128_kmajor_desc(a_base), x0 = sw128_kmajor_desc(b_base);
+    const uint64_t a0 = GATE ? sw128_kmajor_desc(a_base) : sw128_mnmajor_desc(a_base, kPair16Box), x0 = sw128_kmajor_desc(b_base);
     uint32_t s = 0, s_phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!mbar_wait(full0 + 8 * s, s_phase, p.timeout_ns, p.status)) break;
@@ -394,7 +457,7 @@ __global__ void __launch_bounds__(kFewThreads, FewShape<NT>::ctas)
       const uint64_t a = a0 + s * (S::a_bytes >> 4), x = x0 + s * (S::b_bytes >> 4);
       if (leader) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) umma_f16(tm, a + 2 * k, x + 2 * k, IDESC, (kb != kb0) | (k != 0));
+        for (int k = 0; k < 4; ++k) umma_f16(tm, a + k * a_step, x + 2 * k, IDESC, (kb != kb0) | (k != 0));
         umma_commit(empty0 + 8 * s);
         if (kb == kb1 - 1) umma_commit(done);
       }
@@ -429,28 +492,29 @@ __global__ void __launch_bounds__(kFewThreads, FewShape<NT>::ctas)
     tmem_dealloc(tmem, S::tmem_cols);
   }
   if (split > 1) cluster_sync();
-  const int f = threadIdx.x & 63;
+  // A thread takes four neighbouring columns of a token: a trip to another CTA's shared memory costs most
+  // of a microsecond, so few and wide ones.
+  constexpr int QUADS = ROWS / 4, SETS = kFewThreads / QUADS;
+  const int f = 4 * (int)(threadIdx.x % QUADS);
   const int64_t n = n0 + f;
-  for (int c = rank + split * (int)(threadIdx.x >> 6); c < NT && m0 + c < p.M; c += 4 * split) {
+  const int tokens = (int)min((int64_t)NT, p.M - m0);
+  for (int c = rank + split * (int)(threadIdx.x / QUADS); c < tokens; c += SETS * split) {
     const uint32_t at = smem_addr(sums) + (c * 128 + f) * 4;
-    float g[8], u[8];
+    const int64_t m = m0 + c;
+    float a[4];
+    cluster_sums4(at, split, a);
+    if constexpr (GATE) {
+      float b[4], h[4];
+      cluster_sums4(at + 256, split, b);
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (q < split) {
-        const uint32_t a = map_to_cta(at, q);
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(g[q]) : "r"(a) : "memory");
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u[q]) : "r"(a + 256) : "memory");
-      }
-    float gate = g[0], up = u[0];
-#pragma unroll
-    for (int q = 1; q < 8; ++q)
-      if (q < split) gate = __fadd_rn(gate, g[q]), up = __fadd_rn(up, u[q]);
-    if (n < p.F) {
-      p.out[(m0 + c) * p.ldo + n] = round16<DT>(__fmul_rn(activation<ACT>(gate), up));
+      for (int i = 0; i < 4; ++i) h[i] = __fmul_rn(activation<ACT>(a[i]), b[i]);
+      store4<DT>(p.out + m * p.ldo, n, p.N, p.wide & 1, h);
       if (p.gate) {
-        p.gate[(m0 + c) * p.ldgate + n] = round16<DT>(gate);
-        p.up[(m0 + c) * p.ldup + n] = round16<DT>(up);
+        store4<DT>(p.gate + m * p.ldgate, n, p.N, p.wide & 2, a);
+        store4<DT>(p.up + m * p.ldup, n, p.N, p.wide & 4, b);
       }
+    } else {
+      store4<DT>(p.out + m * p.ldo, n, p.N, p.wide & 1, a);
     }
   }
   if (split > 1) cluster_sync();  // no CTA leaves while another still reads its sums
@@ -545,34 +609,44 @@ unsigned plain_grid(int64_t m, int64_t n, int sms) {
   return (unsigned)(tiles < cap ? tiles : cap);
 }
 
-struct GatePlan {
-  int kind;   // 0 plain, 1 pairs, 2 few
-  int nt;     // few: tokens a CTA
-  int split;  // few: CTAs that share a tile's k
+struct FewPlan {
+  int nt;     // tokens a CTA; 0: too many tiles for the grid
+  int split;  // CTAs that share a tile's k
+  double us;  // estimated, where tokens fill more than one kind of CTA (nt 128)
 };
-
-GatePlan plan_gate(const GateParams& p, int sms) {
-  GatePlan g{0, 0, 0};
-  if (p.K == 0 || !tma_rows(p.x, p.ldx, 2) || !tma_rows(p.wg, p.ldwg, 2) || !tma_rows(p.wu, p.ldwu, 2)) return g;
-  g.nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-  const int64_t tiles_n = ((int64_t)p.F + 63) / 64, tiles_m = ((int64_t)p.M + g.nt - 1) / g.nt, slots = 2ll * sms;
-  const int64_t slices = ((int64_t)p.K + 63) / 64;
-  // k is shared out while there are free places for it, not below four slices a CTA
-  g.split = 1;
-  while (g.split < 8 && tiles_n * tiles_m * g.split * 2 <= slots && slices >= 8 * g.split) g.split *= 2;
-  const bool fits = tiles_n <= 65535 && tiles_m <= 65535;
-  g.kind = fits && p.M <= 128 ? 2 : 1;
-  const int64_t pair_tiles = (((int64_t)p.M + 255) / 256) * (((int64_t)p.F + 127) / 128);
-  if (g.kind == 1 && pair_tiles > INT32_MAX) g.kind = 0;
-  return g;
+// `rows` output columns a CTA.  A CTA's set-up and its part of the cluster's sum take about the time of
+// ten slices.
+FewPlan plan_few(int64_t tokens, int64_t columns, int rows, int64_t slices) {
+  const int nt = tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128;
+  const int64_t tiles_n = (columns + rows - 1) / rows, tiles_m = (tokens + nt - 1) / nt;
+  if (tiles_n > 65535 || tiles_m > 65535) return FewPlan{0, 0, 0};
+  const ClusterPlan c = plan_clusters(tiles_n * tiles_m, slices, 2, 10);
+  const double ctas = (double)(tiles_n * tiles_m * c.split) / 152;
+  return FewPlan{nt, c.split, 5 + 0.55 * (double)(c.waves * ((slices + c.split - 1) / c.split)) + 1.5 * (ctas < 2 ? ctas : 2)};
 }
 
-template <int NT, int DT, int ACT> cudaError_t launch_few(const CUtensorMap* maps, const GateParams& p, int split, cudaStream_t s) {
-  const void* f = reinterpret_cast<const void*>(few_kernel<NT, DT, ACT>);
+// Does few_kernel pay, against pairs with `pair_tiles` tiles in `tiles_m` rows of tiles?  Up to 64 tokens always
+// (17 x 1024 x 1024 4.7 us, pairs 7.4; 60 x 2056 x 5640 14.0 and 16.1); above by both estimates, fitted to 35
+// shapes: a slice takes a pair 0.245 us, or what HBM gives of weights that no tile row above has read, a
+// half tile 0.21 (an SM's intake).  E.g. (few / pairs) 200 x 5120 x 512 12.5 / 19.8, 200 x 2048 x 5632
+// 19.5 / 15.5; dx of 777 x 512 x 8192 43 / 73 with the rest of the way back.
+bool few_pays(int64_t tokens, const FewPlan& g, int64_t pair_tiles, int64_t slices) {
+  if (g.nt == 0) return false;
+  if (tokens <= 64) return true;
+  const int64_t waves = pair_tiles / 76, rest = pair_tiles % 76;
+  const double fresh = 256.0 / (double)(tokens > 256 ? (tokens + 255) / 256 * 256 : 256);
+  const double whole = 0.36 * fresh > 0.245 ? 0.36 * fresh : 0.245, half = 0.18 * fresh > 0.21 ? 0.18 * fresh : 0.21;
+  return g.us < 3.9 + (double)slices * ((double)waves * whole + (rest == 0 ? 0 : 2 * rest <= 76 ? half : whole));
+}
+
+template <int NT, int DT, int ACT, bool GATE>
+cudaError_t launch_few_nt(const FewMaps& maps, const FewParams& p, int split, cudaStream_t s) {
+  const void* f = reinterpret_cast<const void*>(few_kernel<NT, DT, ACT, GATE>);
   const cudaError_t e = ensure_smem_attribute(f, FewShape<NT>::smem);
   if (e != cudaSuccess) return e;
+  constexpr int64_t ROWS = GATE ? 64 : 128;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)split, (unsigned)((p.F + 63ll) / 64), (unsigned)(((int64_t)p.M + NT - 1) / NT));
+  cfg.gridDim = dim3((unsigned)split, (unsigned)((p.N + ROWS - 1) / ROWS), (unsigned)(((int64_t)p.M + NT - 1) / NT));
   cfg.blockDim = dim3(kFewThreads);
   cfg.dynamicSmemBytes = FewShape<NT>::smem;
   cfg.stream = s;
@@ -584,7 +658,31 @@ template <int NT, int DT, int ACT> cudaError_t launch_few(const CUtensorMap* map
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = far_get_programmatic_launch() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, few_kernel<NT, DT, ACT>, maps[0], maps[1], maps[2], p);
+  return cudaLaunchKernelEx(&cfg, few_kernel<NT, DT, ACT, GATE>, maps, p);
+}
+template <int DT, int ACT, bool GATE>
+cudaError_t launch_few(const FewMaps& maps, const FewParams& p, const FewPlan& g, cudaStream_t s) {
+  return g.nt == 16   ? launch_few_nt<16, DT, ACT, GATE>(maps, p, g.split, s)
+         : g.nt == 32 ? launch_few_nt<32, DT, ACT, GATE>(maps, p, g.split, s)
+         : g.nt == 64 ? launch_few_nt<64, DT, ACT, GATE>(maps, p, g.split, s)
+                      : launch_few_nt<128, DT, ACT, GATE>(maps, p, g.split, s);
+}
+
+struct GatePlan {
+  int kind;  // 0 plain, 1 pairs, 2 few
+  FewPlan few;
+};
+int64_t slices_of(int64_t k) { return (k + 63) / 64; }
+int wide_rows(const void* p, int64_t ld) { return ((uintptr_t)p & 7) == 0 && ld % 4 == 0; }
+
+GatePlan plan_gate(const GateParams& p) {
+  GatePlan g{0, {0, 0, 0}};
+  if (p.K == 0 || !tma_rows(p.x, p.ldx, 2) || !tma_rows(p.wg, p.ldwg, 2) || !tma_rows(p.wu, p.ldwu, 2)) return g;
+  g.few = plan_few(p.M, p.F, 64, slices_of(p.K));
+  const int64_t pair_tiles = (((int64_t)p.M + 255) / 256) * (((int64_t)p.F + 127) / 128);
+  g.kind = few_pays(p.M, g.few, pair_tiles, slices_of(p.K)) ? 2 : 1;
+  if (g.kind == 1 && pair_tiles > INT32_MAX) g.kind = 0;
+  return g;
 }
 
 int run_gate(GateParams& p, int dtype, int act, cudaStream_t s) {
@@ -594,25 +692,21 @@ int run_gate(GateParams& p, int dtype, int act, cudaStream_t s) {
   if (st != FAR_OK) return st;
   p.status = status;
   p.timeout_ns = kWaitTimeoutNs;
-  const GatePlan g = plan_gate(p, sms);
+  const GatePlan g = plan_gate(p);
   cudaError_t e;
   if (g.kind == 0) {
     e = with_types(dtype, act, [&](auto dt, auto a) {
       return launch_k(plain_gate_kernel<decltype(dt)::value, decltype(a)::value>, dim3(plain_grid(p.M, p.F, sms)), dim3(256), 0, s, p);
     });
   } else if (g.kind == 2) {
-    CUtensorMap maps[3];
-    st = encode_box(&maps[0], p.x, p.M, p.K, p.ldx, 2, g.nt, tma_type(dtype));
-    if (st == FAR_OK) st = encode_operand(&maps[1], p.wg, p.F, p.K, p.ldwg, dtype);
-    if (st == FAR_OK) st = encode_operand(&maps[2], p.wu, p.F, p.K, p.ldwu, dtype);
+    FewMaps maps{};
+    st = encode_box(&maps.x[0], p.x, p.M, p.K, p.ldx, 2, g.few.nt, tma_type(dtype));
+    if (st == FAR_OK) st = encode_operand(&maps.w[0], p.wg, p.F, p.K, p.ldwg, dtype);
+    if (st == FAR_OK) st = encode_operand(&maps.w[1], p.wu, p.F, p.K, p.ldwu, dtype);
     if (st != FAR_OK) return st;
-    e = with_types(dtype, act, [&](auto dt, auto a) {
-      constexpr int DT = decltype(dt)::value, ACT = decltype(a)::value;
-      return g.nt == 16   ? launch_few<16, DT, ACT>(maps, p, g.split, s)
-             : g.nt == 32 ? launch_few<32, DT, ACT>(maps, p, g.split, s)
-             : g.nt == 64 ? launch_few<64, DT, ACT>(maps, p, g.split, s)
-                          : launch_few<128, DT, ACT>(maps, p, g.split, s);
-    });
+    const FewParams q{p.out, p.gate, p.up, p.ldo, p.ldgate, p.ldup, p.M, p.F, (int32_t)slices_of(p.K), 0,
+                      wide_rows(p.out, p.ldo) | wide_rows(p.gate, p.ldgate) << 1 | wide_rows(p.up, p.ldup) << 2, status, kWaitTimeoutNs};
+    e = with_types(dtype, act, [&](auto dt, auto a) { return launch_few<decltype(dt)::value, decltype(a)::value, true>(maps, q, g.few, s); });
   } else {
     PairMaps maps{};
     PairOuts outs{};
@@ -692,14 +786,27 @@ int run_back(const BackCall& c, int dtype, int act, cudaStream_t s) {
     if (st == FAR_OK) st = encode_operand(&maps.a[1], du, c.M, c.F, ld, dtype);
     if (st != FAR_OK) return st;
   }
-  if (dx_tma) {
+  const int64_t f_slices = slices_of(c.F);
+  const FewPlan few = plan_few(c.M, c.K, 128, 2 * f_slices);
+  if (dx_tma && few_pays(c.M, few, dx_tiles, 2 * f_slices)) {
+    FewMaps fm{};
+    st = encode_box(&fm.x[0], dg, c.M, c.F, ld, 2, few.nt, tma_type(dtype));
+    if (st == FAR_OK) st = encode_box(&fm.x[1], du, c.M, c.F, ld, 2, few.nt, tma_type(dtype));
+    if (st == FAR_OK) st = encode_operand(&fm.w[0], c.wg, c.F, c.K, c.ldwg, dtype);
+    if (st == FAR_OK) st = encode_operand(&fm.w[1], c.wu, c.F, c.K, c.ldwu, dtype);
+    if (st != FAR_OK) return st;
+    const FewParams q{c.dx, nullptr, nullptr, c.lddx, 0, 0, c.M, c.K, (int32_t)(2 * f_slices), (int32_t)f_slices,
+                      wide_rows(c.dx, c.lddx), status, kWaitTimeoutNs};
+    if (e == cudaSuccess)
+      e = dtype == FAR_F16 ? launch_few<FAR_F16, FAR_ACT_SILU, false>(fm, q, few, s) : launch_few<FAR_BF16, FAR_ACT_SILU, false>(fm, q, few, s);
+  } else if (dx_tma) {
     st = encode_operand(&maps.b[0], c.wg, c.F, c.K, c.ldwg, dtype);
     if (st == FAR_OK) st = encode_operand(&maps.b[1], c.wu, c.F, c.K, c.ldwu, dtype);
     if (st == FAR_OK) st = pair_output(&outs.out[0], &maps.out[0], c.dx, c.M, c.K, c.lddx, dtype);
     if (st != FAR_OK) return st;
     w.tiles_m = (int32_t)tiles(c.M);
     w.num_tiles = (int32_t)dx_tiles;
-    w.slices = (int32_t)(((int64_t)c.F + 63) / 64);
+    w.slices = (int32_t)f_slices;
     w.pairs = 2;
     if (e == cudaSuccess)
       e = dtype == FAR_F16 ? launch_pair16<ProductEpilogue<FAR_F16, false>>(maps, w, outs, sms, s)
@@ -759,6 +866,21 @@ extern "C" int gated_ffn(const void* x, int64_t x_row_stride, const void* w_gate
   p.F = (int32_t)ffn;
   p.K = (int32_t)hidden;
   return run_gate(p, dtype, activation, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int far_plan_gated_ffn(int64_t tokens, int64_t hidden, int64_t ffn, int* out3) {
+  if (!out3) return FAR_ERR_NULL;
+  if (tokens < 1 || hidden < 1 || ffn < 1 || tokens > INT32_MAX || hidden > INT32_MAX || ffn > INT32_MAX) return FAR_ERR_SHAPE;
+  GateParams p{};  // (16-byte aligned operands)
+  p.M = (int32_t)tokens;
+  p.F = (int32_t)ffn;
+  p.K = (int32_t)hidden;
+  p.ldx = p.ldwg = p.ldwu = 8;
+  const GatePlan g = plan_gate(p);
+  out3[0] = g.kind;
+  out3[1] = g.kind == 2 ? g.few.nt : 0;
+  out3[2] = g.kind == 2 ? g.few.split : 0;
+  return FAR_OK;
 }
 
 extern "C" int64_t far_gated_ffn_backward_workspace_bytes(int64_t tokens, int64_t ffn) {

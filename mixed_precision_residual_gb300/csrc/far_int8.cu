@@ -10,13 +10,15 @@
 // most 2^14 in magnitude, and the binary32 sum of 1024 of them at most 2^24: exact.  So the
 // products run at the tensor cores' f16 rate, and the sums move from TMEM to int32 every 1024 of k.
 //
-// widen_kernel  both operands as f16, into the workspace, for
-// pair16_kernel the product of many rows, on the tensor cores of CTA pairs.
+// pair8_kernel  many rows: CTA pairs; wt's codes are widened on their way from shared memory into TMEM
+//               (A), x's by widen_kernel ahead, into the workspace (B).
 // few8_kernel   few rows of x (a decode batch): codes are widened on their way from shared memory to
 //               the tensor cores, wt's rows into TMEM, x's into shared memory.  Bound by reading wt once.
 // plain_kernel  the product for any shape, stride and alignment: 64 x 64 tiles in int32.
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "far.h"
 #include "far_device.cuh"
@@ -187,6 +189,8 @@ struct Int8Params {
   int64_t ldx, ldw, ldo;  // elements
   int32_t M, N, K;
   int32_t out_dtype;
+  int32_t packed;         // pair8_kernel: wt's codes lie where widen_kernel writes
+  int32_t wide;           // four outputs of a row start on their size's multiple
   unsigned int* status;
   uint64_t timeout_ns;
 };
@@ -200,10 +204,51 @@ __device__ __forceinline__ float scaled(float acc, float a, float b) {
   return fabsf(a) > fabsf(b) ? __fmul_rn(__fmul_rn(acc, a), b) : __fmul_rn(__fmul_rn(acc, b), a);
 }
 
+__device__ __noinline__ float scaled_call(float acc, float a, float b) { return scaled(acc, a, b); }
+
 __device__ __forceinline__ float bias_at(const Int8Params& p, int64_t n) {
   if (p.out_dtype == FAR_F32) return static_cast<const float*>(p.bias)[n];
   const uint32_t h = static_cast<const uint16_t*>(p.bias)[n];
   return p.out_dtype == FAR_F16 ? widen2<FAR_F16>(h).x : widen2<FAR_BF16>(h).x;
+}
+
+// a scale whose product with another such is a normal number or 0
+__device__ __forceinline__ bool usual_scale(float s) {
+  const float m = fabsf(s);
+  return (m >= 0x1p-60f && m <= 0x1p60f) || m == 0.f;
+}
+
+// four neighbouring outputs of a row, in one store where the row allows it
+__device__ __forceinline__ void store4(const Int8Params& p, int64_t m, int64_t n, const float (&v)[4]) {
+  const int64_t i = m * p.ldo + n;
+  if (p.out_dtype == FAR_F32) {
+    float* o = static_cast<float*>(p.out) + i;
+    if (p.wide && n + 4 <= p.N) {
+      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < p.N) o[e] = v[e];
+    return;
+  }
+  uint16_t* o = static_cast<uint16_t*>(p.out) + i;
+  const bool f16 = p.out_dtype == FAR_F16;
+  const uint32_t lo = f16 ? narrow2<FAR_F16>(v[0], v[1]) : narrow2<FAR_BF16>(v[0], v[1]);
+  const uint32_t hi = f16 ? narrow2<FAR_F16>(v[2], v[3]) : narrow2<FAR_BF16>(v[2], v[3]);
+  if (p.wide && n + 4 <= p.N) {
+    *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
+    return;
+  }
+  const uint16_t h[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < p.N) o[e] = h[e];
+}
+
+template <int DT> __device__ __forceinline__ void store_value(void* at, float v) {
+  if constexpr (DT == FAR_F32) *static_cast<float*>(at) = v;
+  else *static_cast<uint16_t*>(at) = (uint16_t)narrow2<DT>(v, 0.f);
 }
 
 // one output
@@ -271,113 +316,381 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
 }
 
 struct WidenParams {
-  const int8_t* src[2];  // x, wt
-  __half* dst[2];        // rows of `ld` values
-  int64_t ldsrc[2], rows[2], ld;
+  const int8_t *x, *wt;
+  __half* wide;      // x as f16, rows of ld values
+  int8_t* packed;    // null, or wt with rows of ld codes, where TMA cannot read it as it stands
+  int64_t ldx, ldw, rows, wt_rows, ld;  // ld: k up to a multiple of 16
   int32_t K;
-  int32_t vec[2];        // whole 16-byte chunks of the source's rows may be read
+  int32_t vec;       // whole 16-byte chunks of x's rows may be read
 };
 
-// A thread takes 16 codes of a row (past k: zeros); neighbouring threads neighbouring chunks.
+// 16 codes of a row (past k: zeros)
+__device__ __forceinline__ void load_codes(uint32_t (&w)[4], const int8_t* row, int k, int K, bool vec) {
+  w[0] = w[1] = w[2] = w[3] = 0u;
+  if (vec && k + 16 <= K) {
+    load_bytes<16>(row + k, w);
+  } else {
+#pragma unroll
+    for (int b = 0; b < 16; ++b)
+      if (k + b < K) w[b >> 2] |= (uint32_t)(uint8_t)row[k + b] << (8 * (b & 3));
+  }
+}
+
+// A thread takes 16 codes; neighbouring threads neighbouring ones.  Bound by HBM.
 __global__ void __launch_bounds__(256) widen_kernel(const WidenParams p) {
-  pdl_launch_dependents();
   pdl_wait();
-  const int64_t per = p.ld / 16, first = per * p.rows[0], total = first + per * p.rows[1];
+  pdl_launch_dependents();  // (behind the wait: pair8_kernel reads wt before it waits itself)
+  const int64_t per = p.ld / 16, first = per * p.rows, total = first + (p.packed ? per * p.wt_rows : 0);
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int which = i >= first;
-    const int64_t j = which ? i - first : i, row = j / per;
-    const int k = (int)(j - row * per) * 16;
-    const int8_t* src = (which ? p.src[1] : p.src[0]) + row * (which ? p.ldsrc[1] : p.ldsrc[0]) + k;
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if ((which ? p.vec[1] : p.vec[0]) && k + 16 <= p.K) {
-      load_bytes<16>(src, w);
+    uint32_t w[4];
+    if (i < first) {
+      const int64_t row = i / per;
+      const int k = (int)(i - row * per) * 16;
+      load_codes(w, p.x + row * p.ldx, k, p.K, p.vec);
+      uint32_t h[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint2 v = widen4(w[e]);
+        h[2 * e] = v.x;
+        h[2 * e + 1] = v.y;
+      }
+      __half* dst = p.wide + row * p.ld + k;
+      store_bytes<16>(dst, h);
+      store_bytes<16>(dst + 8, h + 4);
     } else {
-#pragma unroll
-      for (int b = 0; b < 16; ++b)
-        if (k + b < p.K) w[b >> 2] |= (uint32_t)(uint8_t)src[b] << (8 * (b & 3));
+      const int64_t row = (i - first) / per;
+      const int k = (int)(i - first - row * per) * 16;
+      load_codes(w, p.wt + row * p.ldw, k, p.K, false);
+      store_bytes<16>(p.packed + row * p.ld + k, w);
     }
-    uint32_t h[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint2 v = widen4(w[e]);
-      h[2 * e] = v.x;
-      h[2 * e + 1] = v.y;
-    }
-    __half* dst = (which ? p.dst[1] : p.dst[0]) + row * p.ld + k;
-    store_bytes<16>(dst, h);
-    store_bytes<16>(dst + 8, h + 4);
   }
 }
 
 // ---------------------------------------------------------------------------
-// many rows: tensor cores over CTA pairs
+// pair8_kernel: tiles of 256 rows of wt x nt rows of x (32 .. 192) over a cluster of 2, wt's rows on the
+// TMEM lanes.  Each CTA holds its 128 rows of wt and half of the tile's rows of x; one thread of the even
+// CTA issues tcgen05.mma.cta_group::2 over both, A from each CTA's TMEM, B from shared memory, a block
+// of 128 of k at a time.  Persistent.
+//   warp 0      TMA producer (both CTAs): a ring of blocks of wt's codes, one of blocks of x
+//   warp 1      MMA issuer (even CTA); allocates TMEM: two accumulators of nt columns, blocks of A in
+//               the rest
+//   warps 4-11  widen wt's codes, a row a thread: warps 4-7 and 8-11 every other block
+//   warps 12-19 epilogue: warp w the TMEM lanes 32 (w % 4) .. and one half of the tile's rows of x; sums
+//               to int32 every 8 blocks
+// The registers a thread: 640 threads are launched at 96; warps 0-3 keep 56, 4-11 72, and the epilogue's
+// take 136 for 96 sums (128 x 56 + 256 x 72 + 256 x 136 = 60416 of 61440).
 // ---------------------------------------------------------------------------
+constexpr int kPair8Threads = 640;
+constexpr int kPair8Most = 192;  // rows of x
+constexpr int kPair8Codes = 5, kPair8Slots = 8;  // ring slots: of wt, of x and of A at most
+constexpr uint32_t kPair8CodeBytes = 128 * 128, kPair8XBytes = 120 * 1024;
+constexpr uint32_t kPair8Ring = kPair8Codes * kPair8CodeBytes + kPair8XBytes;
+constexpr int kPair8Bars = 2 * kPair8Codes + 4 * kPair8Slots + 4;
+constexpr size_t kPair8Smem = kPair8Ring + kPair8Bars * 8 + 16 + 1024;
+constexpr int kPair8Sum = 8;  // blocks that an accumulator sums exactly
 
-struct Int8Out {
-  PairOut out;
-  Int8Params p;
+struct Pair8Walk {
+  int32_t nt, tiles_m, tiles_n, num_tiles, blocks;
+  uint32_t xslots, aslots;
+  uint32_t xhalf;  // bytes of a CTA's rows of x of 64 of k, to 1024
 };
 
-struct Int8Epilogue {
-  static constexpr bool kAMn = false, kBMn = false, kSplit = false, kDouble = false;
-  static constexpr int kWidth = 256, kStep = 32, kFlush = 16;  // 1024 of k
-  using Params = Int8Out;
-  static __device__ __forceinline__ bool tile(PairTileAt& at, const PairMaps& maps, const PairWalk& w, const Params& e) {
-    const int first = at.part * 128, mine = at.item.cols - first;
-    const int64_t row0 = (int64_t)at.item.tm * 256 + at.rank * 128 + at.quarter * 32, row = row0 + at.lane;
-    const int64_t col0 = at.item.col0 + first;
-    const int chunks = (w.slices + kFlush - 1) / kFlush;
-    int acc[128];
-#pragma unroll
-    for (int i = 0; i < 128; ++i) acc[i] = 0;
-    // (all 128 columns always: those past a narrow tile's hold what nobody stores)
-#pragma unroll 1
-    for (int k = 0; k < chunks; ++k) {
-      uint32_t t;
-      if (!at.next(w, t)) return false;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        tmem_ld32_sync(t + first + 32 * c, r);
-        if (c == 3) at.release();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) acc[32 * c + i] += __float2int_rn(__uint_as_float(r[i]));
-      }
-    }
-    if (mine <= 0) return true;
-    const Int8Params& p = e.p;
-    const float xs = row < p.M ? p.xs[row] : 0.f;
-    const bool f32 = p.out_dtype == FAR_F32;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (32 * c >= mine) break;
-      const int64_t mycol = col0 + 32 * c + at.lane;  // a lane holds one column's scale and bias
-      const float ws = mycol < p.N ? p.ws[mycol] : 0.f;
-      const float bias = p.bias && mycol < p.N ? bias_at(p, mycol) : 0.f;
-      float v[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        v[i] = scaled(__int2float_rn(acc[32 * c + i]), xs, __shfl_sync(0xffffffffu, ws, i));
-        if (p.bias) v[i] = __fadd_rn(v[i], __shfl_sync(0xffffffffu, bias, i));
-      }
-      if (f32 || (c & 1) == 0) pair_begin_box(e.out, at.lane);
-      uint32_t o[32];
-      if (f32) narrow<FAR_F32, 32>(v, o);
-      else if (p.out_dtype == FAR_F16) narrow<FAR_F16, 32>(v, o);
-      else narrow<FAR_BF16, 32>(v, o);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        if (u < 4 || f32) {
-          const int unit = (f32 || (c & 1) == 0 ? u : u + 4) ^ (at.lane & 7);
-          *reinterpret_cast<uint4*>(at.box + at.lane * 128 + unit * 16) = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-        }
-      }
-      if (f32 || (c & 1) == 1 || mine <= 32 * (c + 1))
-        pair_store_box(e.out, &maps.out[0], at.box, at.lane, row0, col0 + (f32 ? 32 * c : 64 * (c / 2)));
-    }
-    return true;
+// a place in a ring: slot, and the parity of the wait for its use
+struct Place8 {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t slots) {
+    if (++slot == slots) slot = 0, phase ^= 1;
   }
 };
+
+// groups of 8 tiles of wt, x's tiles one after the other inside a group: pairs at work share both in L2
+__device__ __forceinline__ void pair8_tile(const Pair8Walk& w, int t, int& tm, int& tn) {
+  const int per = 8 * w.tiles_m, g = t / per, r = t - g * per, gn = min(w.tiles_n - 8 * g, 8);
+  tn = 8 * g + r % gn;
+  tm = r / gn;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair8Threads, 1)
+    pair8_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                 const __grid_constant__ Int8Params p, const __grid_constant__ Pair8Walk w) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  unsigned char* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);  // the same offset in both CTAs
+  const uint32_t w_base = smem_addr(smem), x_base = w_base + kPair8Codes * kPair8CodeBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kPair8Ring);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kPair8Bars);
+  const uint32_t w_full0 = smem_addr(&bars[0]), w_empty0 = w_full0 + 8 * kPair8Codes;
+  const uint32_t x_full0 = w_empty0 + 8 * kPair8Codes, x_empty0 = x_full0 + 8 * kPair8Slots;
+  const uint32_t a_full0 = x_empty0 + 8 * kPair8Slots, a_empty0 = a_full0 + 8 * kPair8Slots;
+  const uint32_t acc_full0 = a_empty0 + 8 * kPair8Slots, acc_empty0 = acc_full0 + 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_cta_rank();
+  const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+  const uint32_t a_col = 2u * (uint32_t)w.nt;  // TMEM: two accumulators, then A
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPair8Codes; ++s) {
+      mbar_init(w_full0 + 8 * s, 1);
+      mbar_init(w_empty0 + 8 * s, 4);  // the widening warps of a block
+    }
+    for (int s = 0; s < kPair8Slots; ++s) {
+      mbar_init(x_full0 + 8 * s, 1);   // even CTA: its producer's arrive + both CTAs' bytes
+      mbar_init(x_empty0 + 8 * s, 1);  // one multicast commit
+      mbar_init(a_full0 + 8 * s, 8);   // even CTA: four widening warps of each CTA
+      mbar_init(a_empty0 + 8 * s, 1);  // one multicast commit
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(acc_full0 + 8 * a, 1);    // one multicast commit
+      mbar_init(acc_empty0 + 8 * a, 16);  // even CTA: the epilogue warps of both CTAs
+    }
+    fence_barrier_init();
+    tma_prefetch_map(&map_x);
+    tma_prefetch_map(&map_w);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_addr(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any remote arrive or copy
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();  // (not before the TMEM columns are this CTA's)
+  // Only what widen_kernel writes is waited for: it lets this kernel start behind its own wait, when all
+  // work before it is done.  So wt's codes may be read, and widened, while it runs, unless it writes them.
+  if (p.packed) pdl_wait();
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0 && lane == 0) {
+      // ---------------- TMA producer (both CTAs) ----------------
+      Place8 pw, px;
+      uint32_t g = 0;
+      bool ok = true;
+      auto codes = [&](int kb, int row) {
+        mbar_arrive_expect_tx(w_full0 + 8 * pw.slot, kPair8CodeBytes);
+        tma_load_2d(w_base + pw.slot * kPair8CodeBytes, &map_w, kb * 128, row, w_full0 + 8 * pw.slot);
+        pw.next(kPair8Codes);
+      };
+      int early = 0;  // blocks of the first tile whose codes are on their way
+      {
+        int tm, tn;
+        pair8_tile(w, pair, tm, tn);
+        for (; early < min(w.blocks, kPair8Codes); ++early) codes(early, tn * 256 + (int)rank * 128);
+      }
+      pdl_wait();
+      for (int t = pair; ok && t < w.num_tiles; t += pairs) {
+        int tm, tn;
+        pair8_tile(w, t, tm, tn);
+        const int w_row = tn * 256 + (int)rank * 128, x_row = tm * w.nt + (int)rank * (w.nt / 2);
+        for (int kb = 0; kb < w.blocks; ++kb, ++g) {
+          if (early > 0) {
+            --early;
+          } else {
+            if (!mbar_wait(w_empty0 + 8 * pw.slot, pw.phase ^ 1u, p.timeout_ns, p.status)) {
+              ok = false;
+              break;
+            }
+            codes(kb, w_row);
+          }
+          if (!mbar_wait(x_empty0 + 8 * px.slot, px.phase ^ 1u, p.timeout_ns, p.status)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(x_full0 + 8 * px.slot, (uint32_t)w.nt * 256);
+          const uint32_t full_even = map_to_cta(x_full0 + 8 * px.slot, 0), x = x_base + px.slot * 2 * w.xhalf;
+          tma_load_2d_pair(x, &map_x, kb * 128, x_row, full_even);
+          tma_load_2d_pair(x + w.xhalf, &map_x, kb * 128 + 64, x_row, full_even);
+          px.next(w.xslots);
+        }
+      }
+      // Before exit the last copies must have landed, and the commits that free their slots and A's, which
+      // the MMA issuer multicasts, must have arrived in both CTAs.
+      for (uint32_t j = g > kPair8Codes ? g - kPair8Codes : 0u; j < g; ++j)
+        mbar_wait(w_full0 + 8 * (j % kPair8Codes), (j / kPair8Codes) & 1u, p.timeout_ns, p.status);
+      const uint32_t last = g > w.xslots ? g - w.xslots : 0u;
+      if (rank == 0)
+        for (uint32_t j = last; j < g; ++j)
+          mbar_wait(x_full0 + 8 * (j % w.xslots), (j / w.xslots) & 1u, p.timeout_ns, p.status);
+      for (uint32_t j = last; ok && j < g; ++j)
+        ok = mbar_wait(x_empty0 + 8 * (j % w.xslots), (j / w.xslots) & 1u, p.timeout_ns, p.status);
+      for (uint32_t j = g > w.aslots ? g - w.aslots : 0u; ok && j < g; ++j)
+        ok = mbar_wait(a_empty0 + 8 * (j % w.aslots), (j / w.aslots) & 1u, p.timeout_ns, p.status);
+    } else if (warp == 1 && rank == 0) {
+      // ---------------- MMA issuer (even CTA) ----------------
+      const bool leader = elect_one();
+      const uint32_t tm_ = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t idesc = umma_idesc_16(256, w.nt, false, false, false);
+      const uint64_t x0 = sw128_kmajor_desc(x_base);
+      const uint32_t half = w.xhalf >> 4;
+      Place8 px, pa;
+      uint32_t use = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < w.num_tiles; t += pairs) {
+        for (int k0 = 0; ok && k0 < w.blocks; k0 += kPair8Sum, ++use) {
+          const uint32_t acc = use & 1u;
+          if (!mbar_wait(acc_empty0 + 8 * acc, ((use >> 1) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t d = tm_ + acc * w.nt;
+          const int k1 = min(w.blocks, k0 + kPair8Sum);
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!mbar_wait(x_full0 + 8 * px.slot, px.phase, p.timeout_ns, p.status) ||
+                !mbar_wait(a_full0 + 8 * pa.slot, pa.phase, p.timeout_ns, p.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t x = x0 + px.slot * 2 * half;
+            const uint32_t a = tm_ + a_col + 64 * pa.slot;
+            if (leader) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                umma_f16_ts_pair(d, a + 8 * k, x + (k >> 2) * half + 2 * (k & 3), idesc, kb != k0 || k != 0);
+              umma_commit_pair(a_empty0 + 8 * pa.slot, 0x3);
+              umma_commit_pair(x_empty0 + 8 * px.slot, 0x3);
+              if (kb == k1 - 1) umma_commit_pair(acc_full0 + 8 * acc, 0x3);
+            }
+            __syncwarp();
+            px.next(w.xslots);
+            pa.next(w.aslots);
+          }
+        }
+      }
+    }
+  } else if (warp < 12) {
+    // ---------------- wt's codes: a row a thread ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t dst = tmem + a_col + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t a_full_even = map_to_cta(a_full0, 0);
+    const unsigned char* line = smem + row * 128;
+    int skip = (warp - 4) >> 2;  // the other warps' block is next
+    Place8 pw, pa;
+    bool ok = true;
+    for (int t = pair; ok && t < w.num_tiles; t += pairs)
+      for (int kb = 0; kb < w.blocks; ++kb, skip ^= 1, pw.next(kPair8Codes), pa.next(w.aslots)) {
+        if (skip) continue;
+        if (!mbar_wait(w_full0 + 8 * pw.slot, pw.phase, p.timeout_ns, p.status)) {
+          ok = false;
+          break;
+        }
+        const unsigned char* src = line + pw.slot * kPair8CodeBytes;
+        uint32_t v[32];
+        auto widen32 = [&](int h) {  // 64 codes: units 4 h .. of the swizzled row
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint4 c = *reinterpret_cast<const uint4*>(src + (((4 * h + u) ^ (row & 7)) * 16));
+            const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint2 f = widen4(cw[e]);
+              v[8 * u + 2 * e] = f.x;
+              v[8 * u + 2 * e + 1] = f.y;
+            }
+          }
+        };
+        widen32(0);
+        if (!mbar_wait(a_empty0 + 8 * pa.slot, pa.phase ^ 1u, p.timeout_ns, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        tmem_st32(dst + 64 * pa.slot, v);
+        widen32(1);
+        tmem_st32(dst + 64 * pa.slot + 32, v);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(w_empty0 + 8 * pw.slot);
+          mbar_arrive_remote(a_full_even + 8 * pa.slot);  // (tcgen05.wait has seen the stores done)
+        }
+      }
+  } else {
+    // ---------------- epilogue ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+    pdl_wait();  // the scales and the bias are read through L1
+    const int quarter = warp & 3, part = (warp - 12) >> 2, half = w.nt / 2;
+    const uint32_t src = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(part * half);
+    const uint32_t acc_empty_even = map_to_cta(acc_empty0, 0);
+    uint32_t use = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < w.num_tiles; t += pairs) {
+      int tm, tn;
+      pair8_tile(w, t, tm, tn);
+      int acc[kPair8Most / 2];  // (behind the last block: binary32 values)
+#pragma unroll
+      for (int i = 0; i < kPair8Most / 2; ++i) acc[i] = 0;
+#pragma unroll 1
+      for (int k0 = 0; k0 < w.blocks; k0 += kPair8Sum, ++use) {
+        const uint32_t buf = use & 1u;
+        if (!mbar_wait(acc_full0 + 8 * buf, (use >> 1) & 1u, p.timeout_ns, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kPair8Most / 2; c += 16) {
+          if (c < half) {
+            uint32_t r[16];
+            tmem_ld16(src + buf * w.nt + c, r);
+            tmem_ld_wait(r);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[c + i] += __float2int_rn(__uint_as_float(r[i]));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
+      }
+      if (!ok) break;
+      const int64_t n = (int64_t)tn * 256 + rank * 128 + quarter * 32 + lane, m0 = (int64_t)tm * w.nt + part * half;
+      const float ws = n < p.N ? p.ws[n] : 0.f, bias = p.bias && n < p.N ? bias_at(p, n) : -0.f;
+      // A thread's column of up to 96 rows: scaled in place, then stored, 32 neighbouring columns a store.  (The
+      // code of a tile's end runs once a tile, so what it costs is its length, in instruction fetches: with
+      // the scales' rare sizes and the types' stores inlined at each value it took 12 us, as it stands 2.)
+#pragma unroll
+      for (int c = 0; c < kPair8Most / 2; c += 16) {
+        const int64_t m = m0 + c + (lane & 15);
+        if (c < half && m0 + c < p.M) {
+          const float xs = m < p.M ? p.xs[m] : 0.f;
+          if (__all_sync(0xffffffffu, usual_scale(xs) && usual_scale(ws))) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              acc[c + i] = __float_as_int(__fadd_rn(__fmul_rn(__int2float_rn(acc[c + i]), __fmul_rn(__shfl_sync(0xffffffffu, xs, i), ws)), bias));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              acc[c + i] = __float_as_int(__fadd_rn(scaled_call(__int2float_rn(acc[c + i]), __shfl_sync(0xffffffffu, xs, i), ws), bias));
+          }
+        }
+      }
+      const int rows = n < p.N ? (int)min((int64_t)half, p.M - m0) : 0;
+      auto store = [&](auto dt) {
+        constexpr int DT = decltype(dt)::value, SIZE = DT == FAR_F32 ? 4 : 2;
+        char* out = static_cast<char*>(p.out) + (m0 * p.ldo + n) * SIZE;
+        const int64_t step = p.ldo * SIZE;
+#pragma unroll
+        for (int i = 0; i < kPair8Most / 2; ++i, out += step)
+          if (i < rows) store_value<DT>(out, __int_as_float(acc[i]));
+      };
+      if (p.out_dtype == FAR_F32) store(std::integral_constant<int, FAR_F32>{});
+      else if (p.out_dtype == FAR_F16) store(std::integral_constant<int, FAR_F16>{});
+      else store(std::integral_constant<int, FAR_BF16>{});
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while its peer may still signal its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
 
 // ---------------------------------------------------------------------------
 // few8_kernel: 128 rows of wt x NT rows of x a CTA, the blocks of 128 of k shared out over a cluster of
@@ -603,25 +916,49 @@ __global__ void __launch_bounds__(Few8Shape<NT>::threads, Few8Shape<NT>::ctas)
     tmem_dealloc(tmem, S::tmem_cols);
   }
   if (split > 1) cluster_sync();
-  const int64_t n = n0 + (threadIdx.x & 127);
-  const uint32_t mine = smem_addr(sums) + (threadIdx.x & 127) * 4;
-  const float ws = n < p.N ? p.ws[n] : 0.f;
-  constexpr int GROUPS = S::threads / 128;
-  if ((int)(threadIdx.x >> 7) < GROUPS)
-    for (int c = rank + split * (int)(threadIdx.x >> 7); c < NT && m0 + c < p.M; c += GROUPS * split) {
-      int v[8];
+  // a thread takes four neighbouring columns of a row of x at a time, over the cluster's CTAs
+  const int f = 4 * lane;
+  const int64_t n = n0 + f;
+  const int rows = (int)min((int64_t)NT, p.M - m0);
+  float ws[4], bias[4];
+  bool usual = true;
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q < split) {
-          const uint32_t a = map_to_cta(mine + c * 512, q);
-          asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[q]) : "r"(a) : "memory");
-        }
-      int s = v[0];
+  for (int i = 0; i < 4; ++i) {
+    ws[i] = n + i < p.N ? p.ws[n + i] : 0.f;
+    bias[i] = p.bias && n + i < p.N ? bias_at(p, n + i) : -0.f;
+    usual = usual && usual_scale(ws[i]);
+  }
+  for (int c = rank + split * warp; c < rows; c += split * (S::threads / 32)) {
+    const uint32_t at = smem_addr(sums) + (c * 128 + f) * 4;
+    const float xs = p.xs[m0 + c];
+    int v[8][4];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < split)
+        asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[q][0]), "=r"(v[q][1]), "=r"(v[q][2]), "=r"(v[q][3])
+                     : "r"(map_to_cta(at, q))
+                     : "memory");
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int sum = v[0][i];
 #pragma unroll
       for (int q = 1; q < 8; ++q)
-        if (q < split) s += v[q];
-      if (n < p.N) store_one(p, m0 + c, n, s, p.xs[m0 + c], ws);
+        if (q < split) sum += v[q][i];
+      y[i] = __int2float_rn(sum);
     }
+    if (usual && usual_scale(xs)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = __fmul_rn(y[i], __fmul_rn(xs, ws[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = scaled_call(y[i], xs, ws[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __fadd_rn(y[i], bias[i]);
+    store4(p, m0 + c, n, y);
+  }
   if (split > 1) cluster_sync();  // no CTA leaves while another still reads its sums
 }
 
@@ -643,33 +980,41 @@ int validate_int8(const Int8Params& p, int64_t m, int64_t n, int64_t k) {
 }
 
 struct Int8Plan {
-  int kind;   // 0 plain, 1 widened, over CTA pairs, 2 few
-  int nt;     // few: rows of x a CTA
+  int kind;   // 0 plain, 1 CTA pairs, 2 few
+  int nt;     // rows of x a tile
   int split;  // few: CTAs that share a tile's k
 };
 
-// What does not go by alignment, so that the workspace's size does not.
-constexpr int kFewRows = 256;
-bool many_rows(int64_t m, int64_t n, int64_t k) {
-  return k > 0 && m > kFewRows && ((m + 255) / 256) * ((n + 255) / 256) <= INT32_MAX;
-}
 int64_t wide_ld(int64_t k) { return (k + 15) / 16 * 16; }
 
-Int8Plan plan_int8(const Int8Params& p, int sms) {
-  Int8Plan g{0, 0, 0};
-  if (many_rows(p.M, p.N, p.K)) {
-    g.kind = 1;
-    return g;
+// By the sizes alone, so that the workspace's size goes by them too (a GB300's 152 SMs).
+Int8Plan plan_int8(int64_t m, int64_t n, int64_t k) {
+  if (k == 0) return Int8Plan{0, 0, 0};
+  const int64_t blocks = (k + 127) / 128;
+  Int8Plan few{0, m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128, 0};
+  const int64_t few_n = (n + 127) / 128, few_m = (m + few.nt - 1) / few.nt;
+  double few_us = 1e30;
+  if (few_n <= 65535 && few_m <= 65535) {
+    const ClusterPlan c = plan_clusters(few_n * few_m, blocks, few.nt <= 32 ? 2 : 1, 6);
+    few.kind = 2;
+    few.split = c.split;
+    few_us = 5.5 + 0.75 * (double)(c.waves * ((blocks + c.split - 1) / c.split));
+    if (m <= 128) return few;  // (128 x 8192 x 8192 29.9 us, pairs 35.0; 64 x 5120 x 2048 9.4 and 15.3)
   }
-  const int64_t tiles_n = ((int64_t)p.N + 127) / 128, KB = (p.K + 127) / 128;
-  g.nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-  const int64_t tiles_m = ((int64_t)p.M + g.nt - 1) / g.nt, slots = (g.nt <= 32 ? 2ll : 1ll) * sms;
-  if (p.K == 0 || !tma_rows(p.x, p.ldx, 1) || !tma_rows(p.wt, p.ldw, 1) || tiles_n > 65535 || tiles_m > 65535) return g;
-  // k is shared out while there are free places for it, not below two blocks a CTA
-  g.split = 1;
-  while (g.split < 8 && tiles_n * tiles_m * g.split * 2 <= slots && KB >= 4 * g.split) g.split *= 2;
-  g.kind = 2;
-  return g;
+  // Above: estimated microseconds, fitted to both kernels on 40 shapes (17 to 16384 rows).  A block takes a
+  // pair 0.2 us of hand-overs and 1.8 ns a row of x.  E.g. (few / pairs) 200 x 512 x 4096 9.9 / 21.0,
+  // 777 x 512 x 8192 17.0 / 36.1, 200 x 5120 x 13312 79 / 48, 256 x 8192 x 8192 52 / 35.
+  Int8Plan pairs{0, 0, 0};
+  double pairs_us = 1e30;
+  for (int nt = 32; nt <= kPair8Most; nt += 32) {
+    const int64_t tiles = ((n + 255) / 256) * ((m + nt - 1) / nt), waves = (tiles + 75) / 76;
+    const double us = 9.5 + (double)(waves * blocks) * (0.2 + 0.0018 * nt < 0.36 ? 0.36 : 0.2 + 0.0018 * nt);
+    if (tiles <= INT32_MAX && us <= pairs_us) {
+      pairs_us = us;
+      pairs = Int8Plan{1, nt, 0};
+    }
+  }
+  return few_us <= pairs_us ? few : pairs;  // (neither: the plain kernel)
 }
 
 template <int NT> cudaError_t launch_few8(const CUtensorMap& mx, const CUtensorMap& mw, const Int8Params& p, int split, cudaStream_t s) {
@@ -698,7 +1043,10 @@ int run_int8(Int8Params& p, void* workspace, cudaStream_t s) {
   if (st != FAR_OK) return st;
   p.status = status;
   p.timeout_ns = kWaitTimeoutNs;
-  const Int8Plan g = plan_int8(p, sms);
+  const int64_t so = p.out_dtype == FAR_F32 ? 4 : 2;
+  p.wide = (uintptr_t)p.out % (4 * so) == 0 && p.ldo % 4 == 0;
+  Int8Plan g = plan_int8(p.M, p.N, p.K);
+  if (g.kind == 2 && (!tma_rows(p.x, p.ldx, 1) || !tma_rows(p.wt, p.ldw, 1))) g.kind = 0;
   cudaError_t e;
   if (g.kind == 0) {
     const int64_t tiles = (((int64_t)p.M + 63) / 64) * (((int64_t)p.N + 63) / 64), cap = (int64_t)sms * 8;
@@ -714,28 +1062,30 @@ int run_int8(Int8Params& p, void* workspace, cudaStream_t s) {
                      : launch_few8<128>(mx, mw, p, g.split, s);
   } else {
     const int64_t ld = wide_ld(p.K);
-    __half* wx = static_cast<__half*>(workspace);
-    WidenParams q{{p.x, p.wt}, {wx, wx + p.M * ld}, {p.ldx, p.ldw}, {p.M, p.N}, ld, p.K, {tma_rows(p.x, p.ldx, 1), tma_rows(p.wt, p.ldw, 1)}};
-    const int64_t blocks = (((int64_t)p.M + p.N) * (ld / 16) + 255) / 256, cap = (int64_t)sms * 32;
+    __half* wide = static_cast<__half*>(workspace);
+    int8_t* packed = tma_rows(p.wt, p.ldw, 1) ? nullptr : reinterpret_cast<int8_t*>(wide + p.M * ld);
+    p.packed = packed != nullptr;
+    const WidenParams q{p.x, p.wt, wide, packed, p.ldx, p.ldw, p.M, p.N, ld, p.K, tma_rows(p.x, p.ldx, 1)};
+    const int64_t blocks = (((int64_t)p.M + (packed ? p.N : 0)) * (ld / 16) + 255) / 256, cap = (int64_t)sms * 32;
     e = launch_k(widen_kernel, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, s, q);
     if (e != cudaSuccess) return cuda_error_status(e);
-    PairMaps maps{};
-    Int8Out out{};
-    out.p = p;
-    st = encode_operand(&maps.a[0], q.dst[0], p.M, p.K, ld, FAR_F16);
-    if (st == FAR_OK) st = encode_operand(&maps.b[0], q.dst[1], p.N, p.K, ld, FAR_F16);
-    if (st == FAR_OK) st = pair_output(&out.out, &maps.out[0], p.out, p.M, p.N, p.ldo, p.out_dtype);
-    if (st != FAR_OK) return st;
-    PairWalk w{};
-    w.tiles_m = (int32_t)(((int64_t)p.M + 255) / 256);
+    Pair8Walk w{};
+    w.nt = g.nt;
+    w.tiles_m = (int32_t)(((int64_t)p.M + g.nt - 1) / g.nt);
     w.tiles_n = (int32_t)(((int64_t)p.N + 255) / 256);
     w.num_tiles = w.tiles_m * w.tiles_n;
-    w.columns = p.N;
-    w.slices = (p.K + 63) / 64;
-    w.pairs = 1;
-    w.status = status;
-    w.timeout_ns = kWaitTimeoutNs;
-    e = launch_pair16<Int8Epilogue>(maps, w, out, sms, s);
+    w.blocks = (p.K + 127) / 128;
+    w.xhalf = (uint32_t)(g.nt * 64 + 1023) / 1024 * 1024;
+    const uint32_t xslots = kPair8XBytes / (2 * w.xhalf), aslots = (uint32_t)(512 - 2 * g.nt) / 64;
+    w.xslots = xslots < kPair8Slots ? xslots : kPair8Slots;
+    w.aslots = aslots < kPair8Slots ? aslots : kPair8Slots;
+    CUtensorMap mx, mw;
+    st = encode_box(&mx, wide, p.M, p.K, ld, 2, g.nt / 2, CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
+    if (st == FAR_OK) st = encode_box(&mw, packed ? packed : p.wt, p.N, p.K, packed ? ld : p.ldw, 1, 128, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+    if (st != FAR_OK) return st;
+    e = ensure_smem_attribute(reinterpret_cast<const void*>(pair8_kernel), kPair8Smem);
+    const int pairs = w.num_tiles < sms / 2 ? w.num_tiles : sms / 2;
+    if (e == cudaSuccess) e = launch_k(pair8_kernel, dim3(2 * pairs), dim3(kPair8Threads), kPair8Smem, s, mx, mw, p, w);
   }
   return e == cudaSuccess ? FAR_OK : cuda_error_status(e);
 }
@@ -777,7 +1127,17 @@ extern "C" int quant_rows_int8(const void* x, int64_t x_row_stride, void* q, flo
 
 extern "C" int64_t far_gemm_int8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   if (m < 0 || n < 0 || k < 0 || m > INT32_MAX || n > INT32_MAX || k > 131071) return -FAR_ERR_SHAPE;
-  return many_rows(m, n, k) ? (m + n) * wide_ld(k) * 2 : 0;  // both operands as f16
+  return m && n && plan_int8(m, n, k).kind == 1 ? (2 * m + n) * wide_ld(k) : 0;  // x as f16, and wt's codes in case TMA cannot read them as they stand
+}
+
+extern "C" int far_plan_gemm_int8(int64_t m, int64_t n, int64_t k, int* out3) {
+  if (!out3) return FAR_ERR_NULL;
+  if (m < 1 || n < 1 || k < 1 || m > INT32_MAX || n > INT32_MAX || k > 131071) return FAR_ERR_SHAPE;
+  const Int8Plan g = plan_int8(m, n, k);
+  out3[0] = g.kind;
+  out3[1] = g.kind ? g.nt : 0;
+  out3[2] = g.split;
+  return FAR_OK;
 }
 
 extern "C" int gemm_int8(const void* x, int64_t x_row_stride, const float* x_scale, const void* wt, int64_t wt_row_stride,

@@ -1,5 +1,5 @@
 // Products of 16-bit matrices on the tensor cores of CTA pairs, with an epilogue of the caller's (what
-// gated_ffn, its gradients and gemm_int8 share).
+// gated_ffn and its gradients share).
 //
 // pair16_kernel<E>: output tiles of 256 rows x up to 256 accumulator columns over a cluster of 2.
 // Each CTA holds its 128 rows of A and half of the tile's rows of B for a slice of 64 of k; one
@@ -8,10 +8,8 @@
 // one round.
 //   warp 0     TMA producer (both CTAs): a ring of 6 slices running across tiles
 //   warp 1     MMA issuer (even CTA); allocates TMEM: two accumulators of 256 columns
-//   warps 4-11 epilogue, one accumulator behind: warp w the TMEM lanes 32 (w % 4) .. and one half of
+//   warps 2-9  epilogue, one accumulator behind: warp w the TMEM lanes 32 (w % 4) .. and one half of
 //              the columns
-// The registers a thread: 384 threads are launched at 168; warps 0-3 give theirs up to 72 and the
-// epilogue's take 216 (128 x 72 + 256 x 216 = 384 x 168), so that a thread may keep 128 sums.
 // An operand may lie either way in memory, both read by 64 x 64 boxes with the 128-byte swizzle:
 // k-major (rows of k values: a box is 64 rows x 128 bytes of k) or mn-major (rows of k are the
 // memory's columns: a box is 64 values of k x 128 bytes of rows).  So no operand is transposed first.
@@ -34,7 +32,7 @@ cudaError_t ensure_smem_attribute(const void* func, size_t bytes);
 
 constexpr int kPair16Stages = 6;
 constexpr int kPair16Epilogue = 8;  // warps
-constexpr int kPair16Threads = 128 + 32 * kPair16Epilogue;
+constexpr int kPair16Threads = 64 + 32 * kPair16Epilogue;
 constexpr uint32_t kPair16Slice = 128 * 64 * 2;  // bytes of a slice of A or B in a CTA
 constexpr uint32_t kPair16Box = 64 * 64 * 2;
 constexpr uint32_t kPair16Ring = kPair16Stages * 2 * kPair16Slice;
@@ -160,8 +158,8 @@ __device__ __forceinline__ void pair_store_box(const PairOut& o, const CUtensorM
 
 // E: kAMn, kBMn (the operand is mn-major), kSplit (B's halves are two operands' rows, gate and up: the
 // even CTA loads b[0], the odd one b[1]), kDouble (the tile rows are those of two outputs, a[0]'s and then
-// a[1]'s), kWidth (output columns of a tile), kStep (to which a narrow tile is rounded), kFlush
-// (slices to an accumulator; 0: all), Params, and tile(): takes a tile's accumulators and stores it.
+// a[1]'s), kBeside (above), kWidth (output columns of a tile), kStep (to which a narrow tile is rounded), Params, and
+// tile(): takes a tile's accumulator and stores it.
 template <class E>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair16Threads, 1)
     pair16_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairWalk p, const __grid_constant__ typename E::Params e) {
@@ -200,11 +198,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair16Threads, 1)
   cluster_sync();  // both CTAs' barriers exist before any remote arrive or copy
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_launch_dependents();  // (not before the TMEM columns are this CTA's: a dependent that took them would wait for this grid)
-  pdl_wait();
+  // (Dependents not before the TMEM columns are this CTA's: one that took them would wait for this grid.)
+  // E::kBeside: the kernel ahead, of the same call, writes nothing that this one reads, and lets it start only
+  // behind its own wait, when all work before it is done.  So this one runs beside its last CTAs, and
+  // waits for it at the end, so that whoever waits for this grid has waited for both.
+  if constexpr (E::kBeside) {
+    pdl_launch_dependents();
+  } else {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
 
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  if (warp < 2) {
     PairItem w;
     if (warp == 0 && lane == 0) {
       // ---------------- TMA producer (both CTAs) ----------------
@@ -260,56 +265,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair16Threads, 1)
       const uint64_t b0 = E::kBMn ? sw128_mnmajor_desc(b_base, kPair16Box) : sw128_kmajor_desc(b_base);
       // 16 of k further: 32 bytes along k-major rows, 16 mn-major rows of 128 bytes (16-byte units)
       constexpr uint32_t a_step = E::kAMn ? 128 : 2, b_step = E::kBMn ? 128 : 2;
-      const int flush = E::kFlush ? E::kFlush : total;
       uint32_t s = 0, s_phase = 0, use = 0;
       bool ok = true;
       for (int n = 0; ok && pair_item<E::kWidth, E::kStep>(p, pair, num_pairs, n, w); ++n) {
         if (w.cols == 0) continue;
         const uint32_t idesc = umma_idesc_16(256, E::kSplit ? 2 * w.cols : w.cols, p.bf16, E::kAMn, E::kBMn);
-        for (int k0 = 0; ok && k0 < total; k0 += flush, ++use) {
-          const uint32_t acc = use & 1u;
-          if (!mbar_wait(acc_empty0 + 8 * acc, ((use >> 1) & 1u) ^ 1u, p.timeout_ns, p.status)) {
+        const uint32_t acc = use & 1u;
+        if (!mbar_wait(acc_empty0 + 8 * acc, ((use >> 1) & 1u) ^ 1u, p.timeout_ns, p.status)) break;
+        ++use;
+        tc_fence_after();
+        const uint32_t d = tm + acc * 256;
+        for (int kb = 0; kb < total; ++kb) {
+          if (!mbar_wait(full0 + 8 * s, s_phase, p.timeout_ns, p.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t d = tm + acc * 256;
-          const int k1 = min(total, k0 + flush);
-          for (int kb = k0; kb < k1; ++kb) {
-            if (!mbar_wait(full0 + 8 * s, s_phase, p.timeout_ns, p.status)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t a = a0 + s * (kPair16Slice >> 4), b = b0 + s * (kPair16Slice >> 4);
-            if (leader) {
-              umma_f16_pair(d, a, b, idesc, kb != k0);
+          const uint64_t a = a0 + s * (kPair16Slice >> 4), b = b0 + s * (kPair16Slice >> 4);
+          if (leader) {
+            umma_f16_pair(d, a, b, idesc, kb != 0);
 #pragma unroll
-              for (int k = 1; k < 4; ++k) umma_f16_pair(d, a + k * a_step, b + k * b_step, idesc, 1);
-              umma_commit_pair(empty0 + 8 * s, 0x3);  // both CTAs' slots are free once read
-              if (kb == k1 - 1) umma_commit_pair(acc_full0 + 8 * acc, 0x3);
-            }
-            __syncwarp();
-            if (++s == kPair16Stages) {
-              s = 0;
-              s_phase ^= 1;
-            }
+            for (int k = 1; k < 4; ++k) umma_f16_pair(d, a + k * a_step, b + k * b_step, idesc, 1);
+            umma_commit_pair(empty0 + 8 * s, 0x3);  // both CTAs' slots are free once read
+            if (kb == total - 1) umma_commit_pair(acc_full0 + 8 * acc, 0x3);
+          }
+          __syncwarp();
+          if (++s == kPair16Stages) {
+            s = 0;
+            s_phase ^= 1;
           }
         }
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---------------- epilogue ----------------
     PairTileAt at;
     at.rank = (int)rank;
     at.quarter = warp & 3;
-    at.part = (warp - 4) >> 2;
+    at.part = (warp - 2) >> 2;
     at.lane = lane;
     at.tmem = tmem + ((uint32_t)(at.quarter * 32) << 16);
     at.acc_full = acc_full0;
     at.acc_empty_even = map_to_cta(acc_empty0, 0);
-    at.box = smem + kPair16Ring + (warp - 4) * 4096;
+    at.box = smem + kPair16Ring + (warp - 2) * 4096;
     at.uses = 0;
     for (int n = 0; pair_item<E::kWidth, E::kStep>(p, pair, num_pairs, n, at.item); ++n) {
       if (at.item.cols == 0) continue;
@@ -321,6 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair16Threads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no CTA leaves while its peer may still signal its barriers
+  if constexpr (E::kBeside) pdl_wait();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);

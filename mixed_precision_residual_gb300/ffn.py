@@ -16,7 +16,7 @@ import ctypes
 
 import torch
 
-from . import FarError, lib
+from . import FarError, _check, lib
 from ._launch import native, on_stream
 
 _vp, _i64, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -27,6 +27,8 @@ lib.far_gated_ffn_backward_workspace_bytes.argtypes = [_i64, _i64]
 lib.far_gated_ffn_backward_workspace_bytes.restype = _i64
 lib.gated_ffn_backward.argtypes = _MATRIX * 9 + [_vp, _i64, _i64, _i64, _i64, _int, _int, _vp]
 lib.gated_ffn_backward.restype = _int
+lib.far_plan_gated_ffn.argtypes = [_i64, _i64, _i64, _vp]
+lib.far_plan_gated_ffn.restype = _int
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
@@ -70,3 +72,10 @@ def gated_ffn_backward(dout: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
     """
     args = (dout, gate, up, x, w_gate, w_up, _code(activation), dx, dw_gate, dw_up, workspace)
     return native.gated_ffn_backward(*args) if stream is None else on_stream(stream, native.gated_ffn_backward, *args)
+
+
+def plan_gated_ffn(tokens: int, hidden: int, ffn: int) -> dict:
+    """gated_ffn's plan for aligned operands (host logic only)."""
+    buf = (ctypes.c_int * 3)()
+    _check(lib.far_plan_gated_ffn(tokens, hidden, ffn, ctypes.addressof(buf)))
+    return dict(zip(("kind", "tokens", "split"), list(buf)))

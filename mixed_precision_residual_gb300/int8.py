@@ -11,7 +11,7 @@ import ctypes
 
 import torch
 
-from . import FarError, lib
+from . import FarError, _check, lib
 from ._launch import native, on_stream
 
 _vp, _i64, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -21,6 +21,8 @@ lib.far_gemm_int8_workspace_bytes.argtypes = [_i64, _i64, _i64]
 lib.far_gemm_int8_workspace_bytes.restype = _i64
 lib.gemm_int8.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _int, _vp]
 lib.gemm_int8.restype = _int
+lib.far_plan_gemm_int8.argtypes = [_i64, _i64, _i64, _vp]
+lib.far_plan_gemm_int8.restype = _int
 
 
 def quant_rows_int8(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
@@ -53,3 +55,10 @@ def gemm_int8(x: torch.Tensor, x_scale: torch.Tensor, wt: torch.Tensor, wt_scale
     """
     args = (x, x_scale, wt, wt_scale, bias, out_dtype, out, workspace)
     return native.gemm_int8(*args) if stream is None else on_stream(stream, native.gemm_int8, *args)
+
+
+def plan_gemm_int8(m: int, n: int, k: int) -> dict:
+    """gemm_int8's plan for aligned operands (host logic only)."""
+    buf = (ctypes.c_int * 3)()
+    _check(lib.far_plan_gemm_int8(m, n, k, ctypes.addressof(buf)))
+    return dict(zip(("kind", "rows", "split"), list(buf)))

@@ -59,6 +59,20 @@ def test_backward_refusals(far, kw, status):
     assert back(far, **kw) == status
 
 
+def test_plans(far):
+    """Up to 64 tokens always a cluster of CTAs a tile; more by estimate; many tokens CTA pairs."""
+    plan = far.plan_gated_ffn
+    assert plan(1, 5120, 13312) == {"kind": 2, "tokens": 16, "split": 1}
+    assert plan(60, 2056, 5640) == {"kind": 2, "tokens": 64, "split": 3}
+    assert plan(1, 1024, 1024)["split"] == 8 and plan(1, 64, 64) == {"kind": 2, "tokens": 16, "split": 1}
+    assert plan(200, 5120, 512)["kind"] == 2 and plan(200, 2048, 5632)["kind"] == 1
+    assert plan(8192, 5120, 13312) == {"kind": 1, "tokens": 0, "split": 0}
+    assert plan(2 ** 31 - 1, 8, 2 ** 31 - 1)["kind"] == 0  # more tiles than are counted
+    for bad in ((0, 1, 1), (1, 0, 1), (1, 1, 0), (1 << 31, 1, 1)):
+        with pytest.raises(far.FarError):
+            plan(*bad)
+
+
 def test_workspace_sizes(far):
     assert far.gated_ffn_backward_workspace_bytes(4, 512) == 8192
     assert far.gated_ffn_backward_workspace_bytes(3, 5) == 3 * 8 * 4  # rows of whole 16 bytes

@@ -50,6 +50,39 @@ def test_gemm_refusals(far, kw, status):
     assert gemm(far, **kw) == status
 
 
+@pytest.mark.parametrize("kw,status", [
+    (dict(space=None), 9), (dict(bytes=6 * MB - 1), 9), (dict(space=A + 64 * MB + 8), 9), (dict(space=A), 5),
+    (dict(space=A + 5 * MB - 4096), 5)])
+def test_gemm_workspace_refusals(far, kw, status):
+    """Many rows: x as f16 and room for wt's codes, (2 m + n) k bytes."""
+    m, n, k = 2048, 2048, 1024
+    assert far.gemm_int8_workspace_bytes(m, n, k) == (2 * m + n) * k and far.plan_gemm_int8(m, n, k)["kind"] == 1
+    d = dict(x=A, w=A + 16 * MB, xs=A + 32 * MB, ws=A + 33 * MB, b=None, out=A + 5 * MB, ldo=n, space=A + 64 * MB, bytes=6 * MB,
+             m=m, n=n, k=k, ldx=k, ldw=k)
+    d.update(kw)
+    assert gemm(far, **d) == status
+
+
+def test_plans(far):
+    """Few rows a cluster of CTAs, as many as share k and fit at once; many rows CTA pairs, where their tiles fill them."""
+    plan = far.plan_gemm_int8
+    assert plan(1, 8192, 8192) == {"kind": 2, "rows": 16, "split": 4}
+    assert plan(16, 5120, 5120)["split"] == 6  # clusters of 7 do not all fit
+    assert plan(17, 8192, 8192)["rows"] == 32 and plan(64, 512, 8192)["rows"] == 64 and plan(65, 512, 8192)["rows"] == 128
+    assert plan(128, 8192, 8192) == {"kind": 2, "rows": 128, "split": 2}
+    assert plan(777, 512, 8192)["kind"] == 2 and plan(300, 512, 2048)["kind"] == 2
+    assert plan(200, 5120, 13312)["kind"] == 1 and plan(777, 2056, 4112) == {"kind": 1, "rows": 128, "split": 0}
+    assert plan(16384, 8192, 8192) == {"kind": 1, "rows": 192, "split": 0}
+    assert plan(1, 1, 1) == {"kind": 2, "rows": 16, "split": 1}
+    assert plan(2 ** 31 - 1, 2 ** 31 - 1, 64)["kind"] == 0  # more tiles than are counted
+    for m, n, k in ((1, 1 << 30, 128), (1 << 30, 1, 128), (5000, 5000, 131071)):
+        plan(m, n, k)
+        far.gemm_int8_workspace_bytes(m, n, k)
+    for bad in ((0, 1, 1), (1, 0, 1), (1, 1, 0), (1, 1, 131072)):
+        with pytest.raises(far.FarError):
+            plan(*bad)
+
+
 def test_workspace_sizes(far):
     for bad in ((-1, 1, 1), (1, -1, 1), (1, 1, -1), (1, 1, 131072), (1 << 31, 1, 1)):
         with pytest.raises(far.FarError):

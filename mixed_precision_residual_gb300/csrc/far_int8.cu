@@ -319,7 +319,7 @@ struct WidenParams {
   const int8_t *x, *wt;
   __half* wide;      // x as f16, rows of ld values
   int8_t* packed;    // null, or wt with rows of ld codes, where TMA cannot read it as it stands
-  int64_t ldx, ldw, rows, wt_rows, ld;  // ld: k up to a multiple of 16
+  int64_t ldx, ldw, rows, wt_rows, ld;  // ld: wide_ld(k)
   int32_t K;
   int32_t vec;       // whole 16-byte chunks of x's rows may be read
 };
@@ -371,7 +371,8 @@ __global__ void __launch_bounds__(256) widen_kernel(const WidenParams p) {
 // TMEM lanes.  Each CTA holds its 128 rows of wt and half of the tile's rows of x; one thread of the even
 // CTA issues tcgen05.mma.cta_group::2 over both, A from each CTA's TMEM, B from shared memory, a block
 // of 128 of k at a time.  Persistent.
-//   warp 0      TMA producer (both CTAs): a ring of blocks of wt's codes, one of blocks of x
+//   warps 0, 2  TMA producers (both CTAs): a ring of blocks of wt's codes, one of blocks of x.  (One thread for
+//               both spent 630 cycles a block, most of what a block took: 200 x 5120 x 13312 48 us.)
 //   warp 1      MMA issuer (even CTA); allocates TMEM: two accumulators of nt columns, blocks of A in
 //               the rest
 //   warps 4-11  widen wt's codes, a row a thread: warps 4-7 and 8-11 every other block
@@ -392,7 +393,7 @@ constexpr int kPair8Sum = 8;  // blocks that an accumulator sums exactly
 struct Pair8Walk {
   int32_t nt, tiles_m, tiles_n, num_tiles, blocks;
   uint32_t xslots, aslots;
-  uint32_t xhalf;  // bytes of a CTA's rows of x of 64 of k, to 1024
+  uint32_t xhalf;  // bytes of a CTA's rows of x of 64 of k
 };
 
 // a place in a ring: slot, and the parity of the wait for its use
@@ -464,59 +465,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair8Threads, 1)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && lane == 0) {
-      // ---------------- TMA producer (both CTAs) ----------------
-      Place8 pw, px;
+      // ---------------- wt's blocks (both CTAs) ----------------
+      Place8 at;
       uint32_t g = 0;
       bool ok = true;
-      auto codes = [&](int kb, int row) {
-        mbar_arrive_expect_tx(w_full0 + 8 * pw.slot, kPair8CodeBytes);
-        tma_load_2d(w_base + pw.slot * kPair8CodeBytes, &map_w, kb * 128, row, w_full0 + 8 * pw.slot);
-        pw.next(kPair8Codes);
-      };
-      int early = 0;  // blocks of the first tile whose codes are on their way
-      {
-        int tm, tn;
-        pair8_tile(w, pair, tm, tn);
-        for (; early < min(w.blocks, kPair8Codes); ++early) codes(early, tn * 256 + (int)rank * 128);
-      }
-      pdl_wait();
       for (int t = pair; ok && t < w.num_tiles; t += pairs) {
         int tm, tn;
         pair8_tile(w, t, tm, tn);
-        const int w_row = tn * 256 + (int)rank * 128, x_row = tm * w.nt + (int)rank * (w.nt / 2);
+        const int row = tn * 256 + (int)rank * 128;
         for (int kb = 0; kb < w.blocks; ++kb, ++g) {
-          if (early > 0) {
-            --early;
-          } else {
-            if (!mbar_wait(w_empty0 + 8 * pw.slot, pw.phase ^ 1u, p.timeout_ns, p.status)) {
-              ok = false;
-              break;
-            }
-            codes(kb, w_row);
-          }
-          if (!mbar_wait(x_empty0 + 8 * px.slot, px.phase ^ 1u, p.timeout_ns, p.status)) {
+          if (!mbar_wait(w_empty0 + 8 * at.slot, at.phase ^ 1u, p.timeout_ns, p.status)) {
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(x_full0 + 8 * px.slot, (uint32_t)w.nt * 256);
-          const uint32_t full_even = map_to_cta(x_full0 + 8 * px.slot, 0), x = x_base + px.slot * 2 * w.xhalf;
-          tma_load_2d_pair(x, &map_x, kb * 128, x_row, full_even);
-          tma_load_2d_pair(x + w.xhalf, &map_x, kb * 128 + 64, x_row, full_even);
-          px.next(w.xslots);
+          mbar_arrive_expect_tx(w_full0 + 8 * at.slot, kPair8CodeBytes);
+          tma_load_2d(w_base + at.slot * kPair8CodeBytes, &map_w, kb * 128, row, w_full0 + 8 * at.slot);
+          at.next(kPair8Codes);
         }
       }
-      // Before exit the last copies must have landed, and the commits that free their slots and A's, which
-      // the MMA issuer multicasts, must have arrived in both CTAs.
+      // Before exit the last copies must have landed, and the commits that free A's places, which the MMA
+      // issuer multicasts, must have arrived in both CTAs.
       for (uint32_t j = g > kPair8Codes ? g - kPair8Codes : 0u; j < g; ++j)
         mbar_wait(w_full0 + 8 * (j % kPair8Codes), (j / kPair8Codes) & 1u, p.timeout_ns, p.status);
+      for (uint32_t j = g > w.aslots ? g - w.aslots : 0u; ok && j < g; ++j)
+        ok = mbar_wait(a_empty0 + 8 * (j % w.aslots), (j / w.aslots) & 1u, p.timeout_ns, p.status);
+    } else if (warp == 2 && lane == 0) {
+      // ---------------- x's blocks (both CTAs) ----------------
+      pdl_wait();
+      Place8 at;
+      uint32_t g = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < w.num_tiles; t += pairs) {
+        int tm, tn;
+        pair8_tile(w, t, tm, tn);
+        const int row = tm * w.nt + (int)rank * (w.nt / 2);
+        for (int kb = 0; kb < w.blocks; ++kb, ++g) {
+          if (!mbar_wait(x_empty0 + 8 * at.slot, at.phase ^ 1u, p.timeout_ns, p.status)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(x_full0 + 8 * at.slot, (uint32_t)w.nt * 256);
+          tma_load_3d_pair(x_base + at.slot * 2 * w.xhalf, &map_x, 0, row, 2 * kb, map_to_cta(x_full0 + 8 * at.slot, 0));
+          at.next(w.xslots);
+        }
+      }
       const uint32_t last = g > w.xslots ? g - w.xslots : 0u;
       if (rank == 0)
         for (uint32_t j = last; j < g; ++j)
           mbar_wait(x_full0 + 8 * (j % w.xslots), (j / w.xslots) & 1u, p.timeout_ns, p.status);
       for (uint32_t j = last; ok && j < g; ++j)
         ok = mbar_wait(x_empty0 + 8 * (j % w.xslots), (j / w.xslots) & 1u, p.timeout_ns, p.status);
-      for (uint32_t j = g > w.aslots ? g - w.aslots : 0u; ok && j < g; ++j)
-        ok = mbar_wait(a_empty0 + 8 * (j % w.aslots), (j / w.aslots) & 1u, p.timeout_ns, p.status);
     } else if (warp == 1 && rank == 0) {
       // ---------------- MMA issuer (even CTA) ----------------
       const bool leader = elect_one();
@@ -985,7 +983,7 @@ struct Int8Plan {
   int split;  // few: CTAs that share a tile's k
 };
 
-int64_t wide_ld(int64_t k) { return (k + 15) / 16 * 16; }
+int64_t wide_ld(int64_t k) { return (k + 127) / 128 * 128; }  // a row in the workspace: whole blocks, zeros behind k
 
 // By the sizes alone, so that the workspace's size goes by them too (a GB300's 152 SMs).
 Int8Plan plan_int8(int64_t m, int64_t n, int64_t k) {
@@ -994,7 +992,11 @@ Int8Plan plan_int8(int64_t m, int64_t n, int64_t k) {
   Int8Plan few{0, m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128, 0};
   const int64_t few_n = (n + 127) / 128, few_m = (m + few.nt - 1) / few.nt;
   double few_us = 1e30;
-  if (few_n <= 65535 && few_m <= 65535) {
+  if (k % 16 != 0) {
+    // few8_kernel cannot step over such rows: the plain kernel (3 us a step of 32 of k: 400 x 1000 x 3000 298 us), or
+    // pairs, whose widening repacks wt
+    few_us = 5 + 3 * (double)((((m + 63) / 64) * ((n + 63) / 64) + 1215) / 1216) * (double)((k + 31) / 32);
+  } else if (few_n <= 65535 && few_m <= 65535) {
     const ClusterPlan c = plan_clusters(few_n * few_m, blocks, few.nt <= 32 ? 2 : 1, 6);
     few.kind = 2;
     few.split = c.split;
@@ -1002,19 +1004,34 @@ Int8Plan plan_int8(int64_t m, int64_t n, int64_t k) {
     if (m <= 128) return few;  // (128 x 8192 x 8192 29.9 us, pairs 35.0; 64 x 5120 x 2048 9.4 and 15.3)
   }
   // Above: estimated microseconds, fitted to both kernels on 40 shapes (17 to 16384 rows).  A block takes a
-  // pair 0.2 us of hand-overs and 1.8 ns a row of x.  E.g. (few / pairs) 200 x 512 x 4096 9.9 / 21.0,
-  // 777 x 512 x 8192 17.0 / 36.1, 200 x 5120 x 13312 79 / 48, 256 x 8192 x 8192 52 / 35.
+  // pair 0.2 us of issuing and hand-overs and 1.6 ns a row of x.  E.g. (few / pairs) 200 x 512 x 4096 9.9 / 21.0,
+  // 777 x 512 x 8192 17.0 / 36.1, 200 x 5120 x 13312 79 / 41, 256 x 8192 x 8192 52 / 32.
   Int8Plan pairs{0, 0, 0};
   double pairs_us = 1e30;
   for (int nt = 32; nt <= kPair8Most; nt += 32) {
     const int64_t tiles = ((n + 255) / 256) * ((m + nt - 1) / nt), waves = (tiles + 75) / 76;
-    const double us = 9.5 + (double)(waves * blocks) * (0.2 + 0.0018 * nt < 0.36 ? 0.36 : 0.2 + 0.0018 * nt);
+    const double block = 0.2 + 0.0016 * nt, us = 7 + (double)(waves * blocks) * (block < 0.34 ? 0.34 : block);
     if (tiles <= INT32_MAX && us <= pairs_us) {
       pairs_us = us;
       pairs = Int8Plan{1, nt, 0};
     }
   }
-  return few_us <= pairs_us ? few : pairs;  // (neither: the plain kernel)
+  if (k % 16 != 0) pairs_us += 3 + (double)n * (double)k * 4e-7;  // (repacking)
+  return few_us <= pairs_us ? few : pairs;
+}
+
+// Rows of f16, whole blocks of 128, as [row][64 of k][which 64]: a box of two is a block of `rows` rows, one half behind
+// the other.  (One copy instead of two a block: its thread spent 470 cycles a block on them.)
+int encode_wide(CUtensorMap* map, const void* base, int64_t m, int64_t ld, int rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  const int st = get_encoder(&enc);
+  if (st != FAR_OK) return st;
+  cuuint64_t dims[3] = {64, (cuuint64_t)m, (cuuint64_t)(ld / 64)}, strides[2] = {(cuuint64_t)ld * 2, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)rows, 2}, estr[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FAR_OK : FAR_ERR_CUDA;
 }
 
 template <int NT> cudaError_t launch_few8(const CUtensorMap& mx, const CUtensorMap& mw, const Int8Params& p, int split, cudaStream_t s) {
@@ -1075,12 +1092,12 @@ int run_int8(Int8Params& p, void* workspace, cudaStream_t s) {
     w.tiles_n = (int32_t)(((int64_t)p.N + 255) / 256);
     w.num_tiles = w.tiles_m * w.tiles_n;
     w.blocks = (p.K + 127) / 128;
-    w.xhalf = (uint32_t)(g.nt * 64 + 1023) / 1024 * 1024;
+    w.xhalf = (uint32_t)g.nt * 64;
     const uint32_t xslots = kPair8XBytes / (2 * w.xhalf), aslots = (uint32_t)(512 - 2 * g.nt) / 64;
     w.xslots = xslots < kPair8Slots ? xslots : kPair8Slots;
     w.aslots = aslots < kPair8Slots ? aslots : kPair8Slots;
     CUtensorMap mx, mw;
-    st = encode_box(&mx, wide, p.M, p.K, ld, 2, g.nt / 2, CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
+    st = encode_wide(&mx, wide, p.M, ld, g.nt / 2);
     if (st == FAR_OK) st = encode_box(&mw, packed ? packed : p.wt, p.N, p.K, packed ? ld : p.ldw, 1, 128, CU_TENSOR_MAP_DATA_TYPE_UINT8);
     if (st != FAR_OK) return st;
     e = ensure_smem_attribute(reinterpret_cast<const void*>(pair8_kernel), kPair8Smem);

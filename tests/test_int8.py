@@ -73,7 +73,9 @@ def test_plans(far):
     assert plan(777, 512, 8192)["kind"] == 2 and plan(300, 512, 2048)["kind"] == 2
     assert plan(200, 5120, 13312)["kind"] == 1 and plan(777, 2056, 4112) == {"kind": 1, "rows": 128, "split": 0}
     assert plan(16384, 8192, 8192) == {"kind": 1, "rows": 192, "split": 0}
-    assert plan(1, 1, 1) == {"kind": 2, "rows": 16, "split": 1}
+    assert plan(1, 1, 16) == {"kind": 2, "rows": 16, "split": 1}
+    assert plan(1, 1, 1)["kind"] == 0 and plan(4, 1000, 20)["kind"] == 0  # k that TMA cannot step over:
+    assert plan(4, 8192, 8191)["kind"] == 1 and plan(400, 1000, 3000)["kind"] == 1  # plain while short, else repacked
     assert plan(2 ** 31 - 1, 2 ** 31 - 1, 64)["kind"] == 0  # more tiles than are counted
     for m, n, k in ((1, 1 << 30, 128), (1 << 30, 1, 128), (5000, 5000, 131071)):
         plan(m, n, k)

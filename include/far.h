@@ -454,8 +454,10 @@ int quant_rows_int8(const void* x, int64_t x_row_stride, void* q, float* scale, 
  * rounded once to binary32; the scales' product is rounded first where it is a normal number, else acc
  * is multiplied by one scale after the other, so that the result is right to a few units of
  * 2^-24 wherever it lies in binary32's range.  A zero scale gives 0 + bias, unless the other scale is
- * infinite or NaN.  out shares no byte with another buffer.  m == 0 or n == 0 is a no-op; k == 0 gives
- * 0 + bias.  Statuses: FAR_ERR_DTYPE (out_dtype), FAR_ERR_SHAPE (sizes negative or above 2^31 - 1,
+ * infinite or NaN.  Tensor cores (tcgen05, in f16, which holds every code) are used, with up to 128
+ * rows and few more, when the row strides of x and wt are multiples of 16 and both lie on 16-byte
+ * boundaries, with many rows for any; what is left takes a plain kernel with the same results.  out
+ * shares no byte with another buffer.  m == 0 or n == 0 is a no-op; k == 0 gives 0 + bias.  Statuses: FAR_ERR_DTYPE (out_dtype), FAR_ERR_SHAPE (sizes negative or above 2^31 - 1,
  * k above 131071, a row stride too small, a pointer off its elements' alignment), FAR_ERR_NULL,
  * FAR_ERR_ALIAS, FAR_ERR_WORKSPACE (too small or misaligned), FAR_ERR_CUDA.
  */
@@ -511,7 +513,8 @@ int far_plan_gated_ffn(int64_t tokens, int64_t hidden, int64_t ffn, int* out3);
  *   workspace  far_gated_ffn_backward_workspace_bytes(tokens, ffn) bytes of device memory on a 16-byte
  *              boundary, written and read by this call alone: calls that may overlap (other streams,
  *              other graphs) need one each.  Nothing in it is kept.
- * Sums are binary32, in an order that is not specified but the same every run (no atomics).  tokens
+ * Sums are binary32, in an order that is not specified but the same every run (no atomics).  At an
+ * infinite gate the gradients are what the formulas give (NaN for FAR_ACT_SILU).  tokens
  * == 0 gives zero gradients of the weights, ffn == 0 a zero dx.  Everything else is as for gated_ffn;
  * FAR_ERR_WORKSPACE: too small or misaligned.
  */

@@ -302,6 +302,10 @@ template <int DT> __global__ void __launch_bounds__(256) plain_product_kernel(co
 //   warp 0 TMA producer, 1 MMA issuer (and TMEM), 4-7 read the sums
 // Each CTA leaves its sums in its shared memory; the cluster's CTAs add up every S-th token over all of
 // them, in the order of k, and form the outputs.
+// Bound by reading the weights: 1 x 5120 x 13312 43.7 us (6.2 TB/s), 1 x 2048 x 5632 10.4 (4.4), 1 x 1024 x 1024 4.0; what
+// is not bytes is the launch, the set-up and the sum over the cluster, 3 to 4 us (7 with 128 tokens, whose
+// sums are eight times as many).  Rows off 128 bytes cost two: 60 x 2056 x 5640 14.0 us, 48 x 2048 x 5632
+// 11.9.  (Sums read a value at a time from the other CTAs, not four: 100 x 5120 x 13312 54.6 us against 49.5.)
 //   GATE  64 rows of either weight: gate in lanes 0 .. 63, up in 64 .. 127
 //   else  dx: 128 columns of the weights (mn-major), k all rows of w_gate and then all of w_up
 // ---------------------------------------------------------------------------
@@ -521,7 +525,9 @@ __global__ void __launch_bounds__(kFewThreads, FewShape<NT>::ctas)
 }
 
 // ---------------------------------------------------------------------------
-// dgate and dup: rows of `ld` elements, a multiple of 8, in the workspace
+// dgate and dup: rows of `ld` elements, a multiple of 8, in the workspace.  Written once for the two products that
+// read them as tensor-core operands (16 and 2 tiles' worth of times at 4096 columns): 5 tensors through HBM,
+// 4096 x 8192 48 us (7.0 TB/s), 7 % of the way back of 8192 x 4096 x 8192.
 // ---------------------------------------------------------------------------
 
 struct SlopeParams {

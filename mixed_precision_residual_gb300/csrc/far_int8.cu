@@ -3,8 +3,10 @@
 //   out[i, j] = RNE( fl32(sum_k x[i, k] wt[j, k]) (xs[i] ws[j]) + bias[j] ),  the sum an exact integer.
 //
 // rows_kernel   a row's 16-byte chunks in the registers of 1 to 16 warps: its maximum is known
-//               before its values are needed again, so each is read once.  Bound by HBM.
-// long_kernel   any length and alignment: a row read twice, the second time mostly from L2.
+//               before its values are needed again, so each is read once.  Bound by HBM: 8192 x 8192
+//               bf16 31.4 us (6.4 TB/s, 95 % of the copy rate); 48 x 13312 2.9 us.
+// long_kernel   any length and alignment: a row read twice, the second time mostly from L2 (2000 x 40000
+//               bf16 48 us; a value at a time 86).
 //
 // sm_103a's tcgen05 multiplies no integers, but f16 holds every code exactly, a product of two is at
 // most 2^14 in magnitude, and the binary32 sum of 1024 of them at most 2^24: exact.  So the
@@ -129,30 +131,66 @@ template <int ACT> __device__ __forceinline__ float element(const char* row, int
   else return widen2<ACT>(reinterpret_cast<const uint16_t*>(row)[i]).x;
 }
 
-template <int ACT>
-__global__ void __launch_bounds__(256) long_kernel(const QrParams p) {
-  __shared__ float part[8];
+// VEC: 16-byte chunks, four in flight a thread; else a value at a time.
+template <int ACT, bool VEC>
+__global__ void __launch_bounds__(512) long_kernel(const QrParams p) {
+  constexpr int V = VEC ? 16 / dtype_size<ACT>::value : 1, T = 512, U = 4;
+  __shared__ float part[T / 32];
   pdl_launch_dependents();
   pdl_wait();
+  const int units = VEC ? p.cols / V : p.cols;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const char* xr = p.x + row * p.x_stride;
+    float f[U][V];
+    auto load = [&](int64_t c0) {
+      if constexpr (VEC) {
+        uint32_t raw[U][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          raw[u][0] = raw[u][1] = raw[u][2] = raw[u][3] = 0u;
+          if (c0 + u * T < units) load_bytes<16>(xr + (c0 + u * T) * 16, raw[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) widen<ACT, V>(raw[u], f[u]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) f[u][0] = c0 + u * T < units ? element<ACT>(xr, c0 + u * T) : 0.f;
+      }
+    };
     float m = 0.f;
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < p.cols; i += 256) m = max_nan(m, fabsf(element<ACT>(xr, i)));
+    for (int64_t c = threadIdx.x; c < units; c += U * T) {
+      load(c);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < V; ++e) m = max_nan(m, fabsf(f[u][e]));
+    }
     m = warp_max_allreduce(m);
     __syncthreads();  // the last row's parts have been read
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
     m = 0.f;
-    for (int w = 0; w < 8; ++w) m = max_nan(m, part[w]);
+    for (int w = 0; w < T / 32; ++w) m = max_nan(m, part[w]);
     if (threadIdx.x == 0) p.scale[row] = row_scale(m);
     const float inv = row_inverse(m);
     const bool usual = isfinite(m);
     unsigned char* qr = p.q + row * p.cols;
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < p.cols; i += 256) {
-      const float v[4] = {element<ACT>(xr, i), 0.f, 0.f, 0.f};
-      qr[i] = usual ? (unsigned char)(int8_codes4(v, inv) & 0xffu) : (unsigned char)0;
+    for (int64_t c = threadIdx.x; c < units; c += U * T) {
+      load(c);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (c + u * T >= units) break;
+        if constexpr (VEC) {
+          uint32_t w[V / 4];
+#pragma unroll
+          for (int e = 0; e < V / 4; ++e) w[e] = usual ? int8_codes4(f[u] + 4 * e, inv) : 0u;
+          if constexpr (V == 8) *reinterpret_cast<uint2*>(qr + (c + u * T) * 8) = make_uint2(w[0], w[1]);
+          else *reinterpret_cast<uint32_t*>(qr + (c + u * T) * 4) = w[0];
+        } else {
+          const float v[4] = {f[u][0], 0.f, 0.f, 0.f};
+          qr[c + u * T] = usual ? (unsigned char)(int8_codes4(v, inv) & 0xffu) : (unsigned char)0;
+        }
+      }
     }
   }
 }
@@ -171,8 +209,9 @@ cudaError_t launch_rows(QrParams p, bool vec, int sms, cudaStream_t s) {
     return launch_k(wide ? rows_kernel<ACT, 2 * kRowChunks> : rows_kernel<ACT, kRowChunks>,
                     dim3((unsigned)((p.rows + per - 1) / per)), dim3(threads), 0, s, p);
   }
-  const int64_t cap = (int64_t)sms * 8;
-  return launch_k(long_kernel<ACT>, dim3((unsigned)(p.rows < cap ? p.rows : cap)), dim3(256), 0, s, p);
+  const int64_t cap = (int64_t)sms * 4;
+  return launch_k(vec ? long_kernel<ACT, true> : long_kernel<ACT, false>, dim3((unsigned)(p.rows < cap ? p.rows : cap)), dim3(512),
+                  0, s, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -324,44 +363,45 @@ struct WidenParams {
   int32_t vec;       // whole 16-byte chunks of x's rows may be read
 };
 
-// 16 codes of a row (past k: zeros)
-__device__ __forceinline__ void load_codes(uint32_t (&w)[4], const int8_t* row, int k, int K, bool vec) {
-  w[0] = w[1] = w[2] = w[3] = 0u;
-  if (vec && k + 16 <= K) {
-    load_bytes<16>(row + k, w);
+// 8 codes of a row (past k: zeros)
+__device__ __forceinline__ uint2 load_codes(const int8_t* row, int k, int K, bool vec) {
+  uint32_t w[2] = {0u, 0u};
+  if (vec && k + 8 <= K) {
+    load_bytes<8>(row + k, w);
   } else {
 #pragma unroll
-    for (int b = 0; b < 16; ++b)
+    for (int b = 0; b < 8; ++b)
       if (k + b < K) w[b >> 2] |= (uint32_t)(uint8_t)row[k + b] << (8 * (b & 3));
   }
+  return make_uint2(w[0], w[1]);
 }
 
-// A thread takes 16 codes; neighbouring threads neighbouring ones.  Bound by HBM.
+// blockDim.x threads along a row, 8 codes each, blockDim.y rows a CTA; blockIdx.y 1: wt.  Bound by HBM.
 __global__ void __launch_bounds__(256) widen_kernel(const WidenParams p) {
   pdl_wait();
   pdl_launch_dependents();  // (behind the wait: pair8_kernel reads wt before it waits itself)
-  const int64_t per = p.ld / 16, first = per * p.rows, total = first + (p.packed ? per * p.wt_rows : 0);
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    uint32_t w[4];
-    if (i < first) {
-      const int64_t row = i / per;
-      const int k = (int)(i - row * per) * 16;
-      load_codes(w, p.x + row * p.ldx, k, p.K, p.vec);
-      uint32_t h[8];
+  const bool repack = blockIdx.y != 0;
+  const int64_t rows = repack ? p.wt_rows : p.rows;
+  const int step = (int)blockDim.x * 8;
+  constexpr int U = 4;
+  for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < rows; row += (int64_t)gridDim.x * blockDim.y) {
+    const int8_t* src = repack ? p.wt + row * p.ldw : p.x + row * p.ldx;
+    for (int k0 = (int)threadIdx.x * 8; k0 < p.ld; k0 += U * step) {
+      uint2 w[U];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint2 v = widen4(w[e]);
-        h[2 * e] = v.x;
-        h[2 * e + 1] = v.y;
+      for (int u = 0; u < U; ++u)
+        if (k0 + u * step < p.ld) w[u] = load_codes(src, k0 + u * step, p.K, p.vec && !repack);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * step;
+        if (k >= p.ld) break;
+        if (repack) {
+          *reinterpret_cast<uint2*>(p.packed + row * p.ld + k) = w[u];
+        } else {
+          const uint2 a = widen4(w[u].x), b = widen4(w[u].y);
+          *reinterpret_cast<uint4*>(p.wide + row * p.ld + k) = make_uint4(a.x, a.y, b.x, b.y);
+        }
       }
-      __half* dst = p.wide + row * p.ld + k;
-      store_bytes<16>(dst, h);
-      store_bytes<16>(dst + 8, h + 4);
-    } else {
-      const int64_t row = (i - first) / per;
-      const int k = (int)(i - first - row * per) * 16;
-      load_codes(w, p.wt + row * p.ldw, k, p.K, false);
-      store_bytes<16>(p.packed + row * p.ld + k, w);
     }
   }
 }
@@ -380,6 +420,16 @@ __global__ void __launch_bounds__(256) widen_kernel(const WidenParams p) {
 //               to int32 every 8 blocks
 // The registers a thread: 640 threads are launched at 96; warps 0-3 keep 56, 4-11 72, and the epilogue's
 // take 136 for 96 sums (128 x 56 + 256 x 72 + 256 x 136 = 60416 of 61440).
+// Why A in TMEM: widened codes in shared memory for both operands would be written once and read once more
+// there, 160 bytes a cycle of MMA against the 128 that shared memory gives; TMEM takes wt's half of it.
+// Why 192 rows at most: two accumulators of nt columns, so that sums leave while the next block's products
+// arrive, and at least two blocks of A share 512 columns.
+// Measured: 16384 x 8192 x 8192 with widen_kernel 1273 us (1.73 PFLOP/s; both operands widened ahead and
+// 256 x 256 tiles: 1361), 2048 x 4096 x 4096 50 (80), 200 x 5120 x 13312 41 (few8_kernel 79).  At 192 rows
+// a block takes 841 cycles, 768 of them the MMA's; below 128 rows it stays at 670: issuing 8 MMAs and 2
+// commits takes one thread 340 of them, two waits 130, the hand-overs between the widening warps and the
+// issuer in two CTAs the rest.  (An arrival released at cluster scope on the other CTA's barrier instead of
+// one behind tcgen05.wait alone: 0.68 us a slice of 64 against 0.29.)
 // ---------------------------------------------------------------------------
 constexpr int kPair8Threads = 640;
 constexpr int kPair8Most = 192;  // rows of x
@@ -699,6 +749,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair8Threads, 1)
 //              shared memory: B, two blocks
 // Then each CTA leaves its sums in its shared memory and adds up every S-th row of x over the
 // cluster's CTAs (integers: in any order the same), scales and stores.
+// Bound by reading wt: 4 x 8192 x 8192 14.6 us (4.6 TB/s), 4 x 32768 x 4096 24.2 (5.5); about 3 us is the launch,
+// the set-up and the sum over the cluster, and a CTA alone on its SM has 80 KB in flight, which takes
+// 3 us to arrive under load.  Two sets of widening warps and three places for A and B: the same
+// (14.9 and 24.2).
 // ---------------------------------------------------------------------------
 template <int NT> struct Few8Shape {
   static constexpr int ctas = NT <= 32 ? 2 : 1;  // an SM
@@ -1083,8 +1137,10 @@ int run_int8(Int8Params& p, void* workspace, cudaStream_t s) {
     int8_t* packed = tma_rows(p.wt, p.ldw, 1) ? nullptr : reinterpret_cast<int8_t*>(wide + p.M * ld);
     p.packed = packed != nullptr;
     const WidenParams q{p.x, p.wt, wide, packed, p.ldx, p.ldw, p.M, p.N, ld, p.K, tma_rows(p.x, p.ldx, 1)};
-    const int64_t blocks = (((int64_t)p.M + (packed ? p.N : 0)) * (ld / 16) + 255) / 256, cap = (int64_t)sms * 32;
-    e = launch_k(widen_kernel, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, s, q);
+    unsigned along = 16;  // threads: a row of one block of k has 16 units of 8 codes
+    while (along < 256 && (int64_t)along * 8 < ld) along *= 2;
+    const int64_t most = packed && p.N > p.M ? p.N : p.M, per = 256 / along, groups = (most + per - 1) / per, cap = (int64_t)sms * 64;
+    e = launch_k(widen_kernel, dim3((unsigned)(groups < cap ? groups : cap), packed ? 2 : 1), dim3(along, (unsigned)per), 0, s, q);
     if (e != cudaSuccess) return cuda_error_status(e);
     Pair8Walk w{};
     w.nt = g.nt;

@@ -1,4 +1,4 @@
-"""The native binding of the per-head and block-scaled operators, and their explicit streams.
+"""The native binding of the per-head, block-scaled, int8 and feed-forward operators, and their explicit streams.
 
 ``_build/_far_torch.so`` (csrc/far_torch.cpp) checks a call's tensors, allocates its outputs and
 enqueues it on the tensors' device, whatever the current one is, and that device's current

@@ -1,4 +1,4 @@
-// What the per-head and block-scaled operators' host code shares: a kernel launch with the
+// What the per-head, block-scaled, int8 and feed-forward operators' host code shares: a kernel launch with the
 // process's choice of programmatic dependent launch.  (Every such kernel waits for the
 // kernels ahead of it, griddepcontrol.wait, before it reads or writes global memory, but for
 // two things: the kernels of few rows have lines of a weight brought into L2 earlier, and

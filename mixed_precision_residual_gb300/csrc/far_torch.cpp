@@ -1,5 +1,5 @@
-// Binding of the per-head and block-scaled operators to PyTorch tensors: the same functions as
-// heads.py and block.py document, checked and allocated here.  A decode step makes each of
+// Binding of the per-head, block-scaled, int8 and feed-forward operators to PyTorch tensors: the same functions
+// as heads.py, block.py, int8.py and ffn.py document, checked and allocated here.  A decode step makes each of
 // these calls for a few tokens, where its time is the host's: about 20 us of interpreted
 // checks, ctypes conversions and two allocations before a kernel of 3 us; here 3.5 (the product), 4 (a
 // matrix quantised), 4.5 (qk_norm_rope) and 5 (the norm), 9 for qk_norm_rope's gradients.

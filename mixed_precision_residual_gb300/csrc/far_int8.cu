@@ -425,9 +425,10 @@ __global__ void __launch_bounds__(256) widen_kernel(const WidenParams p) {
 // Why 192 rows at most: two accumulators of nt columns, so that sums leave while the next block's products
 // arrive, and at least two blocks of A share 512 columns.
 // Measured: 16384 x 8192 x 8192 with widen_kernel 1273 us (1.73 PFLOP/s; both operands widened ahead and
-// 256 x 256 tiles: 1361), 2048 x 4096 x 4096 50 (80), 200 x 5120 x 13312 41 (few8_kernel 79).  At 192 rows
-// a block takes 841 cycles, 768 of them the MMA's; below 128 rows it stays at 670: issuing 8 MMAs and 2
-// commits takes one thread 340 of them, two waits 130, the hand-overs between the widening warps and the
+// 256 x 256 tiles: 1361), 2048 x 4096 x 4096 50 (80), 200 x 5120 x 13312 40 (few8_kernel 79).  At 192 rows
+// a block takes 841 cycles, 768 of them the MMA's; below 128 rows it stays at about 600: issuing 8 MMAs and 2
+// commits takes one thread 340 of them, a look at its two barriers 100 (looked at one after the other 200: 200 x
+// 5120 x 13312 42 us, 4096 x 1024 x 8192 67 against 60), the hand-overs between the widening warps and the
 // issuer in two CTAs the rest.  (An arrival released at cluster scope on the other CTA's barrier instead of
 // one behind tcgen05.wait alone: 0.68 us a slice of 64 against 0.29.)
 // ---------------------------------------------------------------------------
@@ -585,8 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair8Threads, 1)
           const uint32_t d = tm_ + acc * w.nt;
           const int k1 = min(w.blocks, k0 + kPair8Sum);
           for (int kb = k0; kb < k1; ++kb) {
-            if (!mbar_wait(x_full0 + 8 * px.slot, px.phase, p.timeout_ns, p.status) ||
-                !mbar_wait(a_full0 + 8 * pa.slot, pa.phase, p.timeout_ns, p.status)) {
+            if (!mbar_wait_both(x_full0 + 8 * px.slot, px.phase, a_full0 + 8 * pa.slot, pa.phase, p.timeout_ns, p.status)) {
               ok = false;
               break;
             }
@@ -1059,7 +1059,7 @@ Int8Plan plan_int8(int64_t m, int64_t n, int64_t k) {
   }
   // Above: estimated microseconds, fitted to both kernels on 40 shapes (17 to 16384 rows).  A block takes a
   // pair 0.2 us of issuing and hand-overs and 1.6 ns a row of x.  E.g. (few / pairs) 200 x 512 x 4096 9.9 / 21.0,
-  // 777 x 512 x 8192 17.0 / 36.1, 200 x 5120 x 13312 79 / 41, 256 x 8192 x 8192 52 / 32.
+  // 777 x 512 x 8192 17.0 / 36.1, 200 x 5120 x 13312 79 / 40, 256 x 8192 x 8192 52 / 30.
   Int8Plan pairs{0, 0, 0};
   double pairs_us = 1e30;
   for (int nt = 32; nt <= kPair8Most; nt += 32) {

@@ -256,6 +256,24 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
                : "memory");
 }
 
+// mbar_wait for two barriers, first looked at together: a look takes about 100 cycles, and neither waits for the
+// other's.
+__device__ __forceinline__ bool mbar_wait_both(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b, uint32_t parity_b,
+                                               uint64_t timeout_ns, unsigned int* status) {
+  uint32_t both;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %5;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4, %5;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(both)
+      : "r"(bar_a), "r"(parity_a), "r"(bar_b), "r"(parity_b), "r"(kSuspendHintNs)
+      : "memory");
+  return both != 0 ||
+         (mbar_wait(bar_a, parity_a, timeout_ns, status) && mbar_wait(bar_b, parity_b, timeout_ns, status));
+}
+
 // ---------------------------------------------------------------------------
 // CTA pairs (a cluster of 2): one MMA spans both CTAs' tensor cores
 // ---------------------------------------------------------------------------

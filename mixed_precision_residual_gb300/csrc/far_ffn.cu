@@ -525,9 +525,9 @@ __global__ void __launch_bounds__(kFewThreads, FewShape<NT>::ctas)
 }
 
 // ---------------------------------------------------------------------------
-// dgate and dup: rows of `ld` elements, a multiple of 8, in the workspace.  Written once for the two products that
-// read them as tensor-core operands (16 and 2 tiles' worth of times at 4096 columns): 5 tensors through HBM,
-// 4096 x 8192 48 us (7.0 TB/s), 7 % of the way back of 8192 x 4096 x 8192.
+// dgate and dup: rows of `ld` elements, a multiple of 8, in the workspace.  Written once, because every column of
+// dx's tiles and both weights' gradients read them again as the tensor cores' operands.  Bound by HBM, five
+// tensors: 4096 x 8192 48 us (7.0 TB/s); 7 % of the way back of 8192 x 4096 x 8192.
 // ---------------------------------------------------------------------------
 
 struct SlopeParams {

@@ -70,7 +70,7 @@ def test_forward_exact_sums(far, t, m, h, f):
 @pytest.mark.parametrize("name", ref.ACTS)
 @pytest.mark.parametrize("t", TYPES)
 def test_activation_everywhere(far, t, name):
-    """One value of hidden: gate is x itself, over every finite value of the type; up is 1."""
+    """One value of hidden: gate and up are x itself, over every finite value of the type: out is act(x) x."""
     x = torch.arange(-2 ** 15, 2 ** 15, dtype=torch.int32, device="cuda").to(torch.int16).view(TYPES[t])
     x = x[x.isfinite()][:, None]
     pad = torch.zeros(x.shape[0], 8, dtype=TYPES[t], device="cuda")
@@ -79,7 +79,6 @@ def test_activation_everywhere(far, t, name):
     one[:, 0] = 1
     for m in (slice(0, 40), slice(None)):
         out = far.gated_ffn(pad[m], one, one, activation=name)
-        # up is 1 only where x is: with w_up = w_gate, out = act(x) x
         v = x[m].double()
         want = ref.act(v, name) * v
         big = want.abs() > torch.finfo(TYPES[t]).max

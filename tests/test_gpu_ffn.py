@@ -98,6 +98,29 @@ def test_non_finite(far):
         assert bool((out[3] == 0).all()) and bool((gate[1] == float("inf")).all())
 
 
+@pytest.mark.parametrize("m,h,f", [(5, 72, 136), (300, 264, 200), (40, 77, 50)])
+def test_nan_stays_in_its_row(far, m, h, f):
+    """A NaN token, a NaN weight row: one row and one column of out are NaN, everything else is what it is without them (no kernel
+    multiplies what lies past an edge); the same for dx and a NaN token of dout."""
+    x, wg, wu = inputs(m, h, f, torch.bfloat16, 5)
+    clean = far.gated_ffn(x, wg, wu)
+    bad_x, bad_w = x.clone(), wu.clone()
+    bad_x[m - 2], bad_w[f - 3, h - 1] = float("nan"), float("nan")
+    out = far.gated_ffn(bad_x, wg, bad_w)
+    bad = torch.zeros(m, f, dtype=torch.bool, device="cuda")
+    bad[m - 2], bad[:, f - 3] = True, True
+    assert torch.equal(out.isnan(), bad) and torch.equal(out[~bad], clean[~bad])
+    args = gradients(m, h, f, torch.bfloat16, 6)
+    clean = far.gated_ffn_backward(*args)
+    dh = args[0].clone()
+    dh[m - 2, f - 1] = float("nan")
+    dx, dwg, dwu = far.gated_ffn_backward(dh, *args[1:])
+    rows = torch.arange(m, device="cuda") == m - 2
+    assert bool(dx[rows].isnan().all()) and torch.equal(dx[~rows], clean[0][~rows])
+    for a, b in ((dwg, clean[1]), (dwu, clean[2])):
+        assert bool(a[f - 1].isnan().all()) and torch.equal(a[:f - 1], b[:f - 1])
+
+
 BACK = [(1, 8, 8), (1, 256, 64), (3, 64, 40), (16, 512, 200), (33, 1032, 333), (64, 128, 129), (65, 256, 1000), (100, 520, 264),
         (128, 136, 1024), (200, 264, 512), (257, 1024, 640), (333, 1032, 1100), (777, 136, 257), (1030, 320, 513), (40, 77, 50),
         (300, 5, 70)]
@@ -213,6 +236,29 @@ def test_strides_and_places(far, m, h, f):
             assert r is o and torch.equal(o, w)
             o.fill_(5.0)
             assert bool((b == 5.0).all())
+
+
+def test_leading_axes_and_one_weight_twice(far):
+    """[batch, tokens, hidden] there and back, on a stream with every output and the workspace given; both weights one tensor."""
+    t = torch.bfloat16
+    x, w, _ = inputs(2 * 35, 264, 136, t, 3)
+    dh = torch.randn(70, 136, generator=rng(4), device="cuda").to(t)
+    flat = far.gated_ffn(x, w, w, save=True)
+    back = far.gated_ffn_backward(dh, flat[1], flat[2], x, w, w)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [torch.empty(2, 35, 136, device="cuda", dtype=t) for _ in range(3)]
+    got = far.gated_ffn(x.view(2, 35, 264), w, w, save=True, out=outs[0], gate_out=outs[1], up_out=outs[2], stream=stream)
+    grads = [torch.empty(2, 35, 264, device="cuda", dtype=t), torch.empty_like(w), torch.empty_like(w)]
+    space = torch.empty(far.gated_ffn_backward_workspace_bytes(70, 136), dtype=torch.uint8, device="cuda")
+    more = far.gated_ffn_backward(dh.view(2, 35, 136), got[1], got[2], x.view(2, 35, 264), w, w, dx=grads[0], dw_gate=grads[1],
+                                  dw_up=grads[2], workspace=space, stream=stream)
+    stream.synchronize()
+    for a, b in zip((*got, *more), (*flat, *back)):
+        assert torch.equal(a.view(b.shape), b)
+    assert all(a is b for a, b in zip((*got, *more), (*outs, *grads)))
+    for v, (e, allowed) in zip(flat, ref.forward(x, w, w, "silu")):
+        assert ref.within(v, e, allowed)
 
 
 @pytest.mark.parametrize("m,h,f", [(2, 512, 256), (50, 512, 256), (300, 512, 640)])

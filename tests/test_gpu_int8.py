@@ -98,6 +98,14 @@ def test_quant_places(far):
     assert bool((buf[:700] == 99).all()) and bool((buf[41 * 700:] == 99).all()) and float(sc[0]) == 7 and float(sc[41]) == 7
 
 
+def test_quant_of_one_row(far):
+    """A vector has one scale, without an axis."""
+    x = torch.randn(264, generator=rng(8), device="cuda").half()
+    q, s = far.quant_rows_int8(x)
+    qr, sr = quantised(x)
+    assert q.shape == (264,) and s.shape == () and torch.equal(q.cpu(), qr) and torch.equal(s.cpu(), sr)
+
+
 def product(x, xs, w, ws, bias, t):
     """The contract: the exact integer rounded to binary32, the scales' product, the bias, one rounding."""
     acc = torch.zeros(x.shape[0], w.shape[0], dtype=torch.float64, device=x.device)
@@ -259,3 +267,28 @@ def test_projection_behind_the_norm(far):
     hq, hs = far.quant_rows_int8(h)
     y = far.gemm_int8(hq, hs, q2, s2, out_dtype=torch.float16)
     assert torch.equal(y, product(hq, hs, q2, s2, None, torch.float16))
+
+
+def test_threads_on_their_own_streams(far):
+    """Four threads, each with a stream, calling at once with the lock let go inside: every result its own."""
+    import threading
+
+    cases = [operands(m, 520, 1024, m) for m in (3, 70, 300, 700)]
+    want = [product(*c, None, torch.bfloat16) for c in cases]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got = [far.gemm_int8(*cases[i]) for _ in range(50)]
+        s.synchronize()
+        if not all(torch.equal(g, want[i]) for g in got):
+            wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and far.device_status() == 0

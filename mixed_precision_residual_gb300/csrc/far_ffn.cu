@@ -124,7 +124,7 @@ template <int DT, int ACT, bool SAVE> struct GateEpilogue {
     constexpr int OUTS = SAVE ? 3 : 1;
 #pragma unroll 1
     for (int j = 0; j < OUTS; ++j) {
-      pair_begin_box(e.out[j], at.lane);
+      pair_begin_box(at.lane);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         if (32 * c >= mine) break;
@@ -174,7 +174,7 @@ template <int DT, bool WEIGHTS> struct ProductEpilogue {
       tmem_ld32_sync(t + first + 32 * c, r);
       const bool last = c == 3 || mine <= 32 * (c + 1);
       if (last) at.release();
-      if ((c & 1) == 0) pair_begin_box(e.out[which], at.lane);
+      if ((c & 1) == 0) pair_begin_box(at.lane);
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = narrow2<DT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
       box_words(at.box, at.lane, c & 1, v);

@@ -122,11 +122,10 @@ struct PairOut {
   int32_t align;     // bytes that p and its rows are multiples of: 16, 4 or 2
   int32_t size;      // of an element
 };
-__device__ __forceinline__ void pair_begin_box(const PairOut& o, int lane) {
-  if (o.align >= 16) {
-    if (lane == 0) bulk_wait_read();  // the copy of the last box has read it
-    __syncwarp();
-  }
+// The copy of the last box has read it, whichever output that was: the next one may leave the other way.
+__device__ __forceinline__ void pair_begin_box(int lane) {
+  if (lane == 0) bulk_wait_read();
+  __syncwarp();
 }
 __device__ __forceinline__ void pair_store_box(const PairOut& o, const CUtensorMap* map, unsigned char* box, int lane,
                                                int64_t row, int64_t col) {

@@ -114,11 +114,14 @@ struct PairTileAt {
 
 // A warp's outputs leave in boxes of 32 rows x 128 bytes, put together in shared memory (16-byte units of
 // a row permuted by XOR with row % 8: the 128-byte swizzle): by TMA where out's rows allow, leaving out
-// what lies past the edges, else by the warp, row by row.
+// what lies past the edges, else by the warp, row by row.  A copy writes whole 16-byte units: in rows that end
+// inside one the values behind their end became zeros (measured; rows past the last are left alone).  So the
+// last box of such rows, too, is the warp's.
 struct PairOut {
   void* p;
   int64_t ld;        // elements
   int32_t rows, cols;
+  int32_t copied;    // boxes that start at a column below this leave by TMA
   int32_t align;     // bytes that p and its rows are multiples of: 16, 4 or 2
   int32_t size;      // of an element
 };
@@ -129,10 +132,10 @@ __device__ __forceinline__ void pair_begin_box(int lane) {
 }
 __device__ __forceinline__ void pair_store_box(const PairOut& o, const CUtensorMap* map, unsigned char* box, int lane,
                                                int64_t row, int64_t col) {
-  if (o.align >= 16) {
+  if (col < o.copied) {
     fence_async_shared();
     __syncwarp();
-    if (lane == 0 && col < o.cols && row < o.rows) {
+    if (lane == 0 && row < o.rows) {
       tma_store_2d(map, smem_addr(box), (int)col, (int)row);
       bulk_commit();
     }
@@ -362,8 +365,10 @@ inline bool tma_rows(const void* p, int64_t ld, int elem) { return ((uintptr_t)p
 inline int pair_output(PairOut* o, CUtensorMap* map, void* p, int64_t rows, int64_t cols, int64_t ld, int dt) {
   const int size = dt == FAR_F32 ? 4 : 2;
   const uint64_t bits = (uint64_t)(uintptr_t)p | (uint64_t)(ld * size);
-  *o = PairOut{p, ld, (int32_t)rows, (int32_t)cols, bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2, size};
-  return o->align >= 16 ? encode_box(map, p, rows, cols, ld, size, 32, tma_type(dt)) : FAR_OK;
+  const int align = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+  const int64_t box = 128 / size, copied = align < 16 ? 0 : cols * size % 16 == 0 ? cols : cols / box * box;
+  *o = PairOut{p, ld, (int32_t)rows, (int32_t)cols, (int32_t)copied, align, size};
+  return copied ? encode_box(map, p, rows, cols, ld, size, 32, tma_type(dt)) : FAR_OK;
 }
 
 template <class E>

@@ -68,3 +68,44 @@ def test_backward(far, t, m, h, f):
             far.gated_ffn_backward(dh, gate, up, x, wg, wu, dx=outs[0], dw_gate=outs[1], dw_up=outs[2])
             check(outs, bigs, want, lefts)
     assert far.device_status() == 0
+
+
+@pytest.mark.parametrize("m,h,f", [(9, 77, 333), (60, 72, 1001), (300, 264, 329), (300, 77, 334), (2000, 264, 1100), (2000, 520, 2743)])
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float16])
+def test_rows_that_end_inside_16_bytes(far, t, m, h, f):
+    """Aligned rows of wider matrices, of widths that are no multiple of 8: what lies behind the outputs' rows stays, and what
+    lies behind the inputs' (NaN) does not count."""
+    def rows(v):
+        wide = torch.full((v.shape[0], (v.shape[1] + 7) // 8 * 8 + 8), float("nan"), device="cuda", dtype=t)
+        return wide[:, :v.shape[1]].copy_(v)
+
+    x, wg, wu = normal(m + f, t, (m, h), (f, h), (f, h))
+    wg, wu = wg / h ** 0.5, wu / h ** 0.5
+    x, wg, wu = rows(x), rows(wg), rows(wu)
+    want = far.gated_ffn(x, wg, wu, save=True)
+    assert all(bool(v.isfinite().all()) for v in want)
+    for lefts in itertools.product((0, 8), (0, 1, 2), (0, 8)):
+        outs, bigs = places(lefts, [(m, f)] * 3, t)
+        far.gated_ffn(x, wg, wu, save=True, out=outs[0], gate_out=outs[1], up_out=outs[2])
+        check(outs, bigs, want, lefts)
+    dh, gate, up = (rows(v) for v in (normal(f, t, (m, f))[0], want[1], want[2]))
+    space = torch.full((far.gated_ffn_backward_workspace_bytes(m, f),), 255, dtype=torch.uint8, device="cuda")
+    want = far.gated_ffn_backward(dh, gate, up, x, wg, wu, workspace=space)
+    assert all(bool(v.isfinite().all()) for v in want)
+    for lefts in itertools.product((0, 8), (0, 1, 2), (0, 8)):
+        outs, bigs = places(lefts, [(m, h), (f, h), (f, h)], t)
+        far.gated_ffn_backward(dh, gate, up, x, wg, wu, dx=outs[0], dw_gate=outs[1], dw_up=outs[2])
+        check(outs, bigs, want, lefts)
+    assert far.device_status() == 0
+
+
+@pytest.mark.parametrize("m,h,f", [(300, 264, 332), (2000, 264, 1100)])
+def test_both_projections_in_one_buffer(far, m, h, f):
+    """Halves of [tokens, 2 ffn]: the first on 16 bytes, the second 8 bytes off and right behind it."""
+    x, wg, wu = normal(f, torch.bfloat16, (m, h), (f, h), (f, h))
+    want = far.gated_ffn(x, wg, wu, save=True)
+    both = torch.empty(m, 2 * f, device="cuda", dtype=torch.bfloat16)
+    for first in (0, f):
+        for _ in range(5):
+            out, gate, up = far.gated_ffn(x, wg, wu, save=True, gate_out=both[:, first:first + f], up_out=both[:, f - first:2 * f - first])
+            assert all(torch.equal(a, b) for a, b in zip((out, gate, up), want))

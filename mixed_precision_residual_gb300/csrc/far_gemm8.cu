@@ -42,7 +42,7 @@ struct Gemm8Params {
   int32_t M, N, K, KB;    // KB: blocks of 128 along k
   int32_t tile_scales;    // ws: one a 128 rows of wt (1) or one a row (0)
   int32_t out_dtype;
-  int32_t out_align;      // bytes that out and its row stride are multiples of: 16, 4 or 2
+  int32_t out_align;      // bytes that out, its row stride and, for 16, its rows' length are multiples of: 16, 4 or 2
   int32_t xs_vec, ws_vec; // rows of scales start on 16-byte boundaries
   int32_t tiles_m, tiles_n, num_tiles;  // pair_kernel
   unsigned int* status;
@@ -257,7 +257,9 @@ __device__ __forceinline__ bool fill_scales(float* ring, uint32_t full0, uint32_
 // A warp's outputs leave in boxes of 32 rows x 128 bytes, put together in shared memory (16-byte
 // units of a row permuted by XOR with row % 8: the 128-byte swizzle).  Where out's rows allow, TMA
 // copies a box out while the next tile's blocks arrive, leaving out what lies past the edges;
-// else the warp stores it row by row, 32 neighbouring words (or half words) at a time.
+// else the warp stores it row by row, 32 neighbouring words (or half words) at a time.  (A copy writes
+// whole 16-byte units, so rows that end inside one are the warp's, wherever they start.  Only their last boxes,
+// with the choice made box by box: 2 to 8 % slower for every output, in spills.)
 __device__ __forceinline__ void begin_box(const Gemm8Params& p, int lane) {
   if (p.out_align >= 16) {
     if (lane == 0) bulk_wait_read();  // the copy of the last box has read it
@@ -1239,7 +1241,7 @@ int run_gemm8(Gemm8Params& p, void* stream) {
   p.timeout_ns = kWaitTimeoutNs;
   const int64_t so = p.out_dtype == FAR_F32 ? 4 : 2;
   const uint64_t bits = (uint64_t)(uintptr_t)p.out | (uint64_t)(p.ldo * so);
-  p.out_align = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+  p.out_align = (bits | (uint64_t)(p.N * so)) % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
   p.xs_vec = p.KB % 4 == 0 && ((uintptr_t)p.xs & 15) == 0;
   p.ws_vec = p.KB % 4 == 0 && ((uintptr_t)p.ws & 15) == 0;
   const Gemm8Plan g = plan_gemm8(p, sms);

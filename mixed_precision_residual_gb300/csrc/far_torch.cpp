@@ -501,7 +501,7 @@ PyObject* gemm_int8_(PyObject* const* a) {
   const Tensor &x = tensor(a[0]), &xs = tensor(a[1]), &w = tensor(a[2]), &ws = tensor(a[3]);
   const Tensor *bias = maybe(a[4]), *space = maybe(a[7]);
   if (x.scalar_type() != at::ScalarType::Char || w.scalar_type() != at::ScalarType::Char) refuse("x and wt hold int8 codes");
-  if (x.dim() < 2 || w.dim() != 2 || x.size(-1) != w.size(1)) refuse("x is [..., k] and wt [n, k]");
+  if (x.dim() < 1 || w.dim() != 2 || x.size(-1) != w.size(1)) refuse("x is [..., k] and wt [n, k]");
   if (!THPDtype_Check(a[5])) throw Refused{PyExc_TypeError, "out_dtype is a torch.dtype"};
   const at::ScalarType ot = reinterpret_cast<THPDtype*>(a[5])->scalar_type;
   const int od = code_of(ot);
@@ -533,7 +533,7 @@ PyObject* gemm_int8_(PyObject* const* a) {
 // the dtype shared by all, and the weights' [ffn, hidden] against x's hidden
 int ffn_dtype(const Tensor& x, const Tensor& wg, const Tensor& wu) {
   if (x.dim() < 2 || wg.dim() != 2 || wg.sizes() != wu.sizes() || x.size(-1) != wg.size(1))
-    refuse("x is [..., hidden], w_gate and w_up [ffn, hidden]");
+    refuse("x is [..., tokens, hidden], w_gate and w_up [ffn, hidden]");
   if (wg.scalar_type() != x.scalar_type() || wu.scalar_type() != x.scalar_type()) refuse("x and the weights must share a dtype");
   const int code = code_of(x.scalar_type());
   if (code == FAR_F32) throw Status{FAR_ERR_DTYPE};

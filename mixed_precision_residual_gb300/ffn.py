@@ -44,7 +44,7 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activat
               stream=None):
     """act(x @ w_gate^T) * (x @ w_up^T), or with save=True (that, x @ w_gate^T, x @ w_up^T).
 
-    x: [..., hidden], w_gate and w_up: [ffn, hidden], all float16 or all bfloat16.  The projections
+    x: [..., tokens, hidden], w_gate and w_up: [ffn, hidden], all float16 or all bfloat16.  The projections
     stay in float32 until the product; the kept ones are rounded.
     """
     if not save and (gate_out is not None or up_out is not None):

@@ -48,8 +48,9 @@ def gemm_int8(x: torch.Tensor, x_scale: torch.Tensor, wt: torch.Tensor, wt_scale
               workspace: torch.Tensor | None = None, stream=None):
     """out = (x * x_scale) @ (wt * wt_scale)^T + bias of int8 matrices with a scale for each row.
 
-    x: [..., k], x_scale: [...]; wt: [n, k], wt_scale: [n]; bias: [n] of out_dtype.  The integer sums
-    are exact (k <= 131071); one rounding to out_dtype behind the scales and the bias.
+    x: [..., k], x_scale: [...]; wt: [n, k], wt_scale: [n]; bias: [n] of out_dtype; out: [..., n].  One
+    token's vector has a scale without an axis, as quant_rows_int8 gives it.  The integer sums are
+    exact (k <= 131071); one rounding to out_dtype behind the scales and the bias.
     workspace: gemm_int8_workspace_bytes(m, n, k) bytes, allocated when not given; calls that may
     overlap need one each.
     """

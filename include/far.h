@@ -430,8 +430,9 @@ int far_plan_gemm_fp8_for_sms(int64_t m, int64_t n, int64_t k, int wt_block, int
  *   gives that scale and codes 0
  *   x      [rows, cols] act (FAR_F32, FAR_F16 or FAR_BF16), row stride in elements (>= cols), device
  *   q      [rows, cols] int8, contiguous, device;  scale  [rows] binary32, device
- * (what the int8 output of fused_add_rmsnorm_quant is, of x as it stands.)  rows, cols >= 0, at most
- * 2^31 - 1 each; rows == 0 is a no-op, cols == 0 gives scales 0.  q and scale share no byte with
+ * For a row that is zero or from 2^-100 up this is what the int8 output of fused_add_rmsnorm_quant is, of x as it
+ * stands; between 0 and 2^-100 that one gives amax / 127 and codes, this one zeros.  rows, cols >= 0, at
+ * most 2^31 - 1 each; rows == 0 is a no-op, cols == 0 gives scales 0.  q and scale share no byte with
  * another buffer.
  */
 int quant_rows_int8(const void* x, int64_t x_row_stride, void* q, float* scale, int64_t rows, int64_t cols, int act,

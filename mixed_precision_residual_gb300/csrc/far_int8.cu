@@ -48,8 +48,9 @@ struct QrParams {
   int32_t warps;     // rows_kernel: warps a row
 };
 
-// 127 / amax leaves binary32's range for a row below 2^-100 (long before any value matters): such
-// rows count as zero, as 128-blocks of E4M3 do.
+// A row below 2^-100 counts as zero, as 128-blocks of E4M3 do: a chosen limit, above 2^-121, where 127 / amax
+// leaves binary32's range and would turn the row's zeros into NaN.  (The norm's int8 output takes a row as
+// zero at amax == 0 alone.)
 __device__ __forceinline__ float row_scale(float amax) { return amax < kBlockTiny ? 0.f : __fdiv_rn(amax, 127.0f); }
 __device__ __forceinline__ float row_inverse(float amax) { return amax < kBlockTiny ? 0.f : __fdiv_rn(127.0f, amax); }
 

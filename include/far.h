@@ -482,8 +482,8 @@ int far_plan_gemm_int8(int64_t m, int64_t n, int64_t k, int* out3);
  *   activation  FAR_ACT_SILU       g / (1 + exp(-g))
  *               FAR_ACT_GELU       g * Phi(g), Phi the normal distribution
  *               FAR_ACT_GELU_TANH  g / 2 * (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))
- * in binary32, right to 2^-15 of each value (an infinite g follows the formula's limit at +inf and
- * gives NaN at -inf; NaN gives NaN).  Few tokens read both weights once; the order of the binary32
+ * in binary32, right to 2^-15 of each value or to 2^-143, whichever is more (an infinite g follows the
+ * formula's limit at +inf and gives NaN at -inf; NaN gives NaN).  Few tokens read both weights once; the order of the binary32
  * additions is not specified but the same every run.  Tensor cores (tcgen05) are used when x's and the
  * weights' row strides are multiples of 8 and their pointers on 16-byte boundaries; any other call
  * takes a plain kernel with the same contract.  No output shares a byte with another buffer.  Sizes
@@ -514,7 +514,9 @@ int far_plan_gated_ffn(int64_t tokens, int64_t hidden, int64_t ffn, int* out3);
  *   workspace  far_gated_ffn_backward_workspace_bytes(tokens, ffn) bytes of device memory on a 16-byte
  *              boundary, written and read by this call alone: calls that may overlap (other streams,
  *              other graphs) need one each.  Nothing in it is kept.
- * Sums are binary32, in an order that is not specified but the same every run (no atomics).  At an
+ * Sums are binary32, in an order that is not specified but the same every run (no atomics).  dgate and dup
+ * have dtype's range before the sums: in FAR_F16 one of 65520 or more is infinite and one up to 2^-25
+ * zero, whatever the sums would be (a loss scaled for f16 keeps them inside).  At an
  * infinite gate the gradients are what the formulas give (NaN for FAR_ACT_SILU).  tokens
  * == 0 gives zero gradients of the weights, ffn == 0 a zero dx.  Everything else is as for gated_ffn;
  * FAR_ERR_WORKSPACE: too small or misaligned.

@@ -66,7 +66,8 @@ def gated_ffn_backward(dout: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
                        workspace: torch.Tensor | None = None, stream=None):
     """(dx, dw_gate, dw_up): gated_ffn's gradients given its output's, at the projections it kept.
 
-    Sums over tokens are float32, in a fixed order; the gradients have the inputs' dtype.
+    Sums over tokens are float32, in a fixed order; the gradients have the inputs' dtype.  What the sums are
+    of, the projections' gradients, is rounded to that dtype first (float16: infinite from 65520 up).
     workspace: gated_ffn_backward_workspace_bytes(tokens, ffn) bytes, allocated when not given; calls
     that may overlap need one each.
     """

@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(256) widen_kernel(const WidenParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// pair8_kernel: tiles of 256 rows of wt x nt rows of x (32 .. 192) over a cluster of 2, wt's rows on the
+// pair8_kernel: tiles of 256 rows of wt x nt rows of x (64 .. 192) over a cluster of 2, wt's rows on the
 // TMEM lanes.  Each CTA holds its 128 rows of wt and half of the tile's rows of x; one thread of the even
 // CTA issues tcgen05.mma.cta_group::2 over both, A from each CTA's TMEM, B from shared memory, a block
 // of 128 of k at a time.  Persistent.
@@ -1063,7 +1063,8 @@ Int8Plan plan_int8(int64_t m, int64_t n, int64_t k) {
   // 777 x 512 x 8192 17.0 / 36.1, 200 x 5120 x 13312 79 / 40, 256 x 8192 x 8192 52 / 30.
   Int8Plan pairs{0, 0, 0};
   double pairs_us = 1e30;
-  for (int nt = 32; nt <= kPair8Most; nt += 32) {
+  // (Tiles of 32 rows would take as long a block as 64.)
+  for (int nt = 64; nt <= kPair8Most; nt += 32) {
     const int64_t tiles = ((n + 255) / 256) * ((m + nt - 1) / nt), waves = (tiles + 75) / 76;
     const double block = 0.2 + 0.0016 * nt, us = 7 + (double)(waves * blocks) * (block < 0.34 ? 0.34 : block);
     if (tiles <= INT32_MAX && us <= pairs_us) {

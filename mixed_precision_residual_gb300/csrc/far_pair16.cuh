@@ -95,7 +95,7 @@ struct PairTileAt {
   uint32_t acc_full, acc_empty_even;
   unsigned char* box;
   uint32_t uses;           // accumulators taken so far, by this warp
-  // waits for the next accumulator: its TMEM address, or 0 when the wait ran out
+  // waits for the next accumulator, and gives its TMEM address; false when the wait ran out
   __device__ __forceinline__ bool next(const PairWalk& p, uint32_t& at) {
     const uint32_t acc = uses & 1u;
     if (!mbar_wait(acc_full + 8 * acc, (uses >> 1) & 1u, p.timeout_ns, p.status)) return false;
@@ -118,12 +118,11 @@ struct PairTileAt {
 // inside one the values behind their end became zeros (measured; rows past the last are left alone).  So the
 // last box of such rows, too, is the warp's.
 struct PairOut {
-  void* p;
+  uint16_t* p;
   int64_t ld;        // elements
   int32_t rows, cols;
   int32_t copied;    // boxes that start at a column below this leave by TMA
   int32_t align;     // bytes that p and its rows are multiples of: 16, 4 or 2
-  int32_t size;      // of an element
 };
 // The copy of the last box has read it, whichever output that was: the next one may leave the other way.
 __device__ __forceinline__ void pair_begin_box(int lane) {
@@ -146,17 +145,13 @@ __device__ __forceinline__ void pair_store_box(const PairOut& o, const CUtensorM
 #pragma unroll 4
   for (int r = 0; r < rows; ++r) {
     const uint32_t v = *reinterpret_cast<const uint32_t*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4);
-    if (o.size == 4) {
-      if (col + lane < o.cols) static_cast<uint32_t*>(o.p)[(row + r) * o.ld + col + lane] = v;
+    const int64_t n = col + 2 * lane;
+    uint16_t* d = o.p + (row + r) * o.ld + n;
+    if (o.align >= 4 && n + 1 < o.cols) {
+      *reinterpret_cast<uint32_t*>(d) = v;
     } else {
-      const int64_t n = col + 2 * lane;
-      uint16_t* d = static_cast<uint16_t*>(o.p) + (row + r) * o.ld + n;
-      if (o.align >= 4 && n + 1 < o.cols) {
-        *reinterpret_cast<uint32_t*>(d) = v;
-      } else {
-        if (n < o.cols) d[0] = (uint16_t)v;
-        if (n + 1 < o.cols) d[1] = (uint16_t)(v >> 16);
-      }
+      if (n < o.cols) d[0] = (uint16_t)v;
+      if (n + 1 < o.cols) d[1] = (uint16_t)(v >> 16);
     }
   }
   __syncwarp();  // before the next box
@@ -353,7 +348,7 @@ inline int encode_box(CUtensorMap* map, const void* base, int64_t rows, int64_t 
   return r == CUDA_SUCCESS ? FAR_OK : FAR_ERR_CUDA;
 }
 inline CUtensorMapDataType tma_type(int dt) {
-  return dt == FAR_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : dt == FAR_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return dt == FAR_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 }
 // an operand [rows, cols] of 16-bit values, and whether TMA can read it
 inline int encode_operand(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int dt) {
@@ -362,13 +357,12 @@ inline int encode_operand(CUtensorMap* map, const void* base, int64_t rows, int6
 inline bool tma_rows(const void* p, int64_t ld, int elem) { return ((uintptr_t)p & 15) == 0 && (ld * elem) % 16 == 0; }
 
 // an output, and its tensor map where its rows allow one
-inline int pair_output(PairOut* o, CUtensorMap* map, void* p, int64_t rows, int64_t cols, int64_t ld, int dt) {
-  const int size = dt == FAR_F32 ? 4 : 2;
-  const uint64_t bits = (uint64_t)(uintptr_t)p | (uint64_t)(ld * size);
+inline int pair_output(PairOut* o, CUtensorMap* map, uint16_t* p, int64_t rows, int64_t cols, int64_t ld, int dt) {
+  const uint64_t bits = (uint64_t)(uintptr_t)p | (uint64_t)(ld * 2);
   const int align = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
-  const int64_t box = 128 / size, copied = align < 16 ? 0 : cols * size % 16 == 0 ? cols : cols / box * box;
-  *o = PairOut{p, ld, (int32_t)rows, (int32_t)cols, (int32_t)copied, align, size};
-  return copied ? encode_box(map, p, rows, cols, ld, size, 32, tma_type(dt)) : FAR_OK;
+  const int64_t copied = align < 16 ? 0 : cols % 8 == 0 ? cols : cols / 64 * 64;
+  *o = PairOut{p, ld, (int32_t)rows, (int32_t)cols, (int32_t)copied, align};
+  return copied ? encode_box(map, p, rows, cols, ld, 2, 32, tma_type(dt)) : FAR_OK;
 }
 
 template <class E>

@@ -462,7 +462,7 @@ int quant_rows_int8(const void* x, int64_t x_row_stride, void* q, float* scale, 
  * where wt has few rows: 4096 x 128 x 8192) a kernel that wants the row strides of x and wt to be
  * multiples of 16 and both on 16-byte boundaries.  A call of that plan with other strides or starts, and
  * small products with a k that is no multiple of 16, take a plain kernel with the same results
- * (4 x 8192 x 8192 0.5 ms where the other takes 15 us).  The workspace, too, goes by the sizes: it always
+ * (4 x 8192 x 8192 0.5 to 1 ms where the other takes 15 us).  The workspace, too, goes by the sizes: it always
  * has room for wt's codes, which are copied only where TMA cannot read them as they stand.
  * Statuses: FAR_ERR_DTYPE (out_dtype), FAR_ERR_SHAPE (sizes negative or above 2^31 - 1, k above 131071,
  * a row stride too small, a pointer off its elements' alignment), FAR_ERR_NULL,

@@ -4,9 +4,9 @@
 //
 // rows_kernel   a row's 16-byte chunks in the registers of 1 to 16 warps: its maximum is known
 //               before its values are needed again, so each is read once.  Bound by HBM: 8192 x 8192
-//               bf16 31.4 us (6.4 TB/s, 95 % of the copy rate); 48 x 13312 2.9 us.
+//               bf16 31.6 us (6.4 TB/s, 94 % of the copy rate); 48 x 13312 2.9 us.
 // long_kernel   any length and alignment: a row read twice, the second time mostly from L2 (2000 x 40000
-//               bf16 48 us; a value at a time 86).
+//               bf16 48 us).  Off 16 bytes a value at a time: 8192 x 100 16.5, 8192 x 8191 77, 2000 x 40001 87.
 //
 // sm_103a's tcgen05 multiplies no integers, but f16 holds every code exactly, a product of two is at
 // most 2^14 in magnitude, and the binary32 sum of 1024 of them at most 2^24: exact.  So the
@@ -16,7 +16,7 @@
 //               (A), x's by widen_kernel ahead, into the workspace (B).
 // few8_kernel   few rows of x (a decode batch): codes are widened on their way from shared memory to
 //               the tensor cores, wt's rows into TMEM, x's into shared memory.  Bound by reading wt once.
-// plain_kernel  the product for any shape, stride and alignment: 64 x 64 tiles in int32.
+// plain_kernel  the product for any shape, stride and alignment: 64 x 64 tiles in int32 (4 x 8192 x 8192 0.5 to 1 ms).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -425,8 +425,8 @@ __global__ void __launch_bounds__(256) widen_kernel(const WidenParams p) {
 // there, 160 bytes a cycle of MMA against the 128 that shared memory gives; TMEM takes wt's half of it.
 // Why 192 rows at most: two accumulators of nt columns, so that sums leave while the next block's products
 // arrive, and at least two blocks of A share 512 columns.
-// Measured: 16384 x 8192 x 8192 with widen_kernel 1273 us (1.73 PFLOP/s; both operands widened ahead and
-// 256 x 256 tiles: 1361), 2048 x 4096 x 4096 50 (80), 200 x 5120 x 13312 40 (few8_kernel 79).  At 192 rows
+// Measured: 16384 x 8192 x 8192 with widen_kernel 1267 to 1297 us (1.70 to 1.74 PFLOP/s; both operands widened ahead
+// and 256 x 256 tiles: 1361), 2048 x 4096 x 4096 50 (80), 200 x 5120 x 13312 41 (few8_kernel 79).  At 192 rows
 // a block takes 841 cycles, 768 of them the MMA's; below 128 rows it stays at about 600: issuing 8 MMAs and 2
 // commits takes one thread 340 of them, a look at its two barriers 100 (looked at one after the other 200: 200 x
 // 5120 x 13312 42 us, 4096 x 1024 x 8192 67 against 60), the hand-overs between the widening warps and the

@@ -15,8 +15,8 @@
 // memory's columns: a box is 64 values of k x 128 bytes of rows).  So no operand is transposed first.
 // Every wait is bounded (FAR_ERR_TIMEOUT in the device error word on expiry).
 // Bound by the MMA and, over a long run, the power it draws: gated_ffn of 8192 x 5120 x 13312 1214 to
-// 1275 us (1.75 to 1.84 PFLOP/s, 90 to 94 % of the cuBLAS burst rate; in ncu the tensor cores are active 92 % of 4096 x
-// 4096 x 8192, 86 % for dx and 92 % for dw there).  A half tile's slice takes 0.21 us where its MMA takes 0.13:
+// 1310 us on different GB300s (1.70 to 1.84 PFLOP/s, 91 to 98 % of the cuBLAS burst rate; in ncu the tensor
+// cores are active 92 % of 4096 x 4096 x 8192, 86 % for dx and 92 % for dw there).  A half tile's slice takes 0.21 us where its MMA takes 0.13:
 // 24 KB into an SM at 60 bytes a cycle.  (A producer thread for each operand: the same times.)
 #pragma once
 

@@ -194,8 +194,6 @@ struct GateParams {
   uint16_t *out, *gate, *up;                    // gate and up may be null
   int64_t ldx, ldwg, ldwu, ldo, ldgate, ldup;   // elements
   int32_t M, F, K;                              // tokens, ffn, hidden
-  unsigned int* status;
-  uint64_t timeout_ns;
 };
 
 // 64 x 64 outputs a CTA of 256 threads, 4 x 4 a thread (16 apart), both projections at once.
@@ -699,8 +697,6 @@ int run_gate(GateParams& p, int dtype, int act, cudaStream_t s) {
   int sms = 0;
   int st = device_info(&status, &sms);
   if (st != FAR_OK) return st;
-  p.status = status;
-  p.timeout_ns = kWaitTimeoutNs;
   const GatePlan g = plan_gate(p);
   cudaError_t e;
   if (g.kind == 0) {
@@ -714,7 +710,8 @@ int run_gate(GateParams& p, int dtype, int act, cudaStream_t s) {
     if (st == FAR_OK) st = encode_operand(&maps.w[1], p.wu, p.F, p.K, p.ldwu, dtype);
     if (st != FAR_OK) return st;
     const FewParams q{p.out, p.gate, p.up, p.ldo, p.ldgate, p.ldup, p.M, p.F, (int32_t)slices_of(p.K), 0,
-                      wide_rows(p.out, p.ldo) | wide_rows(p.gate, p.ldgate) << 1 | wide_rows(p.up, p.ldup) << 2, status, kWaitTimeoutNs};
+                      wide_rows(p.out, p.ldo) | wide_rows(p.gate, p.ldgate) << 1 | wide_rows(p.up, p.ldup) << 2, status,
+                      wait_limit_ns(slices_of(p.K))};
     e = with_types(dtype, act, [&](auto dt, auto a) { return launch_few<decltype(dt)::value, decltype(a)::value, true>(maps, q, g.few, s); });
   } else {
     PairMaps maps{};
@@ -735,7 +732,7 @@ int run_gate(GateParams& p, int dtype, int act, cudaStream_t s) {
     w.pairs = 1;
     w.bf16 = dtype == FAR_BF16;
     w.status = status;
-    w.timeout_ns = kWaitTimeoutNs;
+    w.timeout_ns = wait_limit_ns(w.slices);
     e = with_types(dtype, act, [&](auto dt, auto a) {
       constexpr int DT = decltype(dt)::value, ACT = decltype(a)::value;
       return p.gate ? launch_pair16<GateEpilogue<DT, ACT, true>>(maps, w, outs, sms, s)
@@ -787,7 +784,6 @@ int run_back(const BackCall& c, int dtype, int act, cudaStream_t s) {
   w.tiles_n = (int32_t)tiles(c.K);
   w.bf16 = dtype == FAR_BF16;
   w.status = status;
-  w.timeout_ns = kWaitTimeoutNs;
   PairMaps maps{};
   PairOuts outs{};
   if (dx_tma || dw_tma) {
@@ -805,7 +801,7 @@ int run_back(const BackCall& c, int dtype, int act, cudaStream_t s) {
     if (st == FAR_OK) st = encode_operand(&fm.w[1], c.wu, c.F, c.K, c.ldwu, dtype);
     if (st != FAR_OK) return st;
     const FewParams q{c.dx, nullptr, nullptr, c.lddx, 0, 0, c.M, c.K, (int32_t)(2 * f_slices), (int32_t)f_slices,
-                      wide_rows(c.dx, c.lddx), status, kWaitTimeoutNs};
+                      wide_rows(c.dx, c.lddx), status, wait_limit_ns(2 * f_slices)};
     if (e == cudaSuccess)
       e = dtype == FAR_F16 ? launch_few<FAR_F16, FAR_ACT_SILU, false>(fm, q, few, s) : launch_few<FAR_BF16, FAR_ACT_SILU, false>(fm, q, few, s);
   } else if (dx_tma) {
@@ -817,6 +813,7 @@ int run_back(const BackCall& c, int dtype, int act, cudaStream_t s) {
     w.num_tiles = (int32_t)dx_tiles;
     w.slices = (int32_t)f_slices;
     w.pairs = 2;
+    w.timeout_ns = wait_limit_ns(2 * f_slices);
     if (e == cudaSuccess)
       e = dtype == FAR_F16 ? launch_pair16<ProductEpilogue<FAR_F16, false>>(maps, w, outs, sms, s)
                            : launch_pair16<ProductEpilogue<FAR_BF16, false>>(maps, w, outs, sms, s);
@@ -832,6 +829,7 @@ int run_back(const BackCall& c, int dtype, int act, cudaStream_t s) {
     w.num_tiles = (int32_t)dw_tiles;
     w.slices = (int32_t)(((int64_t)c.M + 63) / 64);
     w.pairs = 1;
+    w.timeout_ns = wait_limit_ns(w.slices);
     if (e == cudaSuccess)
       e = dtype == FAR_F16 ? launch_pair16<ProductEpilogue<FAR_F16, true>>(maps, w, outs, sms, s)
                            : launch_pair16<ProductEpilogue<FAR_BF16, true>>(maps, w, outs, sms, s);

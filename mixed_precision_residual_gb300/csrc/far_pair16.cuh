@@ -356,6 +356,10 @@ inline int encode_operand(CUtensorMap* map, const void* base, int64_t rows, int6
 }
 inline bool tma_rows(const void* p, int64_t ld, int elem) { return ((uintptr_t)p & 15) == 0 && (ld * elem) % 16 == 0; }
 
+// The limit of a kernel's waits, of which the longest is an epilogue's for a whole sum: a slice takes 0.25 us, so a sum
+// over 2^30 values 4 s.
+inline uint64_t wait_limit_ns(int64_t slices) { return kWaitTimeoutNs + (uint64_t)slices * 1000; }
+
 // an output, and its tensor map where its rows allow one
 inline int pair_output(PairOut* o, CUtensorMap* map, uint16_t* p, int64_t rows, int64_t cols, int64_t ld, int dt) {
   const uint64_t bits = (uint64_t)(uintptr_t)p | (uint64_t)(ld * 2);
